@@ -367,6 +367,144 @@ int kan_surface_backward(const kan_surface_desc_t* desc, const void* x, const vo
  * float32 layer output becomes the next layer's bf16 input. */
 int kan_cast_f32_to_bf16(const float* in, void* out, int64_t n, void* stream);
 
+/* ---- Token rows, sequence mixing and distillation ---------------------------
+ * The layers above work on rows.  The three operators below surround them in a
+ * model over tokens: an embedding makes the rows, a gated linear recurrence
+ * mixes the rows of a sequence, and a distillation loss compares the last
+ * layer's logits with a teacher's.  They are not on the pages.  The
+ * conventions at the top hold, with two additions:
+ * - token ids, sequence lengths and slots are device integers that the host
+ *   never reads; values out of range are defined for each entry point and
+ *   never address memory outside the arrays;
+ * - where a description gives strides (in elements), rows need only the
+ *   alignment of their element, the last dimension is contiguous, and the
+ *   rows of one array must not overlap.  Other tensors are 16-byte aligned,
+ *   workspaces 256-byte aligned. */
+typedef enum { KAN_I32 = 0, KAN_I64 = 1 } kan_index_t;
+
+/* Embedding: y[n, :] = scale * E[ids[n], :], rounded once to `row_dtype`; a
+ * row whose id is outside [0, V) (padding) is zero.  Gradient:
+ *
+ *     dE[v, :] = scale * sum over n with ids[n] = v of dy[n, :]
+ *
+ * with dy in `row_dtype`, summed in float32 over the rows of a token in
+ * ascending order, in fixed chunks whose sums are then added in order.
+ * Layouts: ids [N] (kan_index_t id_dtype), E [V, D] in `dtype`, y, dy [N, D]
+ * in `row_dtype`, dE [V, D] float32, every row of it written. */
+typedef struct {
+    int64_t N;          /* tokens, 0 .. 2^24 */
+    int64_t V;          /* table rows, 1 .. 2^26 */
+    int64_t D;          /* row width, 1 .. 2^23 */
+    int32_t dtype;      /* kan_dtype_t: storage of E */
+    int32_t row_dtype;  /* kan_dtype_t: storage of y and dy */
+    int32_t id_dtype;   /* kan_index_t: storage of ids */
+    float scale;        /* finite */
+} kan_embed_desc_t;
+
+/* Bytes of workspace kan_embed_backward needs (SIZE_MAX if `desc` is
+ * invalid): the tokens' rows in token order, each token's first place in that
+ * order, and the sums of chunks cut by a token's end. */
+size_t kan_embed_workspace_size(const kan_embed_desc_t* desc);
+int kan_embed_forward(const kan_embed_desc_t* desc, const void* ids, const void* E, void* y, void* stream);
+int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void* dy, float* dE,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gated linear recurrence over B sequences of T rows of D channels, each
+ * channel on its own:
+ *
+ *     u_t = sigmoid(-g_t),  f_t = sigmoid(g_t) = 1 - u_t
+ *     h_t = f_t h_{t-1} + u_t x_t = h_{t-1} + u_t (x_t - h_{t-1}),   h_{-1} = h0 (0 if NULL)
+ *     y_t = h_t for t < len, 0 from there to T;    hT = h_{len-1} (h0 where len = 0)
+ *
+ * with len = lengths[b] limited to [0, T] (T if `lengths` is NULL).  x and g
+ * past a sequence's length are never used.  Backward, from dy and the
+ * gradient dhT of hT (0 if NULL):
+ *
+ *     del_t = dy_t + f_{t+1} del_{t+1},   del_{len-1} = dy_{len-1} + dhT
+ *     dx_t  = u_t del_t
+ *     dg_t  = f_t u_t (h_{t-1} - x_t) del_t
+ *     dh0   = f_0 del_0 (dhT where len = 0)
+ *
+ * dx and dg are 0 from a sequence's length to T.  Runs of rows are composed in
+ * the form h -> h + (b - U h), with U = 1 - prod f accumulated directly, so
+ * that gates near 1 (long memories) lose no digits; all of it in float32, in
+ * a fixed order.  x, g in `dtype` and dx, dg in `grad_dtype` have strides
+ * (elements from one row to the next, and from one sequence to the next), so
+ * they may be the halves of one projection; y, dy [B, T, D], h0, hT, dhT, dh0
+ * [B, D] are contiguous float32. */
+typedef struct {
+    int64_t B;              /* sequences, >= 0; B times D (rounded up to 64) at most 2^28 */
+    int64_t T;              /* rows of a sequence, >= 0 */
+    int64_t D;              /* channels, >= 1 */
+    int64_t x_row, x_seq;   /* strides of x */
+    int64_t g_row, g_seq;   /* strides of g */
+    int64_t dx_row, dx_seq; /* strides of dx (backward only) */
+    int64_t dg_row, dg_seq; /* strides of dg (backward only) */
+    int32_t dtype;          /* kan_dtype_t: storage of x and g */
+    int32_t grad_dtype;     /* kan_dtype_t: storage of dx and dg */
+} kan_recur_desc_t;
+
+/* Bytes of workspace a pass (kan_pass_t) needs (SIZE_MAX if `desc` is
+ * invalid): with few channels and long sequences, the composed runs of a
+ * sequence's segments; otherwise 0. */
+size_t kan_recur_workspace_size(const kan_recur_desc_t* desc, int pass);
+/* y and hT out (hT may be NULL). */
+int kan_recur_forward(const kan_recur_desc_t* desc, const void* x, const void* g, const float* h0,
+                      const int32_t* lengths, float* y, float* hT, void* workspace, size_t workspace_bytes,
+                      void* stream);
+/* dx, dg and dh0 out (dx and dg both or neither; dh0 may be NULL); y is the forward's. */
+int kan_recur_backward(const kan_recur_desc_t* desc, const void* x, const void* g, const float* h0,
+                       const int32_t* lengths, const float* y, const float* dy, const float* dhT, void* dx,
+                       void* dg, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+/* One row of each of B sequences (desc->T is 1): the states live in a pool
+ * state [S, D] float32, sequence b's in row slots[b] (row b if `slots` is
+ * NULL; then S >= B), which is read and replaced by h; y [B, D] = h.  A
+ * sequence whose slot is outside [0, S) is skipped and its y is 0.  The slots
+ * of one call must differ from each other.  x_seq and g_seq are the strides
+ * between rows of x and g. */
+int kan_recur_step(const kan_recur_desc_t* desc, int64_t S, const void* x, const void* g, float* state,
+                   const int32_t* slots, float* y, void* stream);
+
+/* Distillation from a teacher's top logits.  With p the softmax of a row's K
+ * teacher logits t / tau over the entries whose id is inside [0, V) (the rest
+ * are absent), and q the softmax of its V student logits z / tau:
+ *
+ *     lse     = log sum_v exp(z_v / tau)
+ *     loss_b  = w_b tau^2 sum_k p_k (log p_k - log q_{ids[k]})
+ *     dz_v    = dloss_b w_b tau (q_v - sum over k with ids[k] = v of p_k)
+ *
+ * A row with w_b = 0, with no teacher entry (all absent or all t = -inf), or
+ * whose z are all -inf has loss 0 and dz 0; rows with w_b = 0 are not read,
+ * and their lse is 0.  A teacher entry with t = -inf adds nothing.  Layouts: z
+ * [N, V] in `dtype` with row stride z_row, dz [N, V] in `grad_dtype` with row
+ * stride dz_row; ids [N, K] (id_dtype), t [N, K] in `teacher_dtype`; w (NULL:
+ * all 1), loss, lse, dloss [N] float32. */
+typedef struct {
+    int64_t N;              /* rows, 0 .. 2^22 */
+    int64_t V;              /* student logits of a row, >= 1 */
+    int64_t K;              /* teacher logits of a row, 1 .. 1024 */
+    int64_t z_row;          /* stride of z, >= V */
+    int64_t dz_row;         /* stride of dz, >= V (backward and step) */
+    int32_t dtype;          /* kan_dtype_t: storage of z */
+    int32_t teacher_dtype;  /* kan_dtype_t: storage of t */
+    int32_t id_dtype;       /* kan_index_t: storage of ids */
+    int32_t grad_dtype;     /* kan_dtype_t: storage of dz */
+    float tau;              /* finite, > 0 */
+} kan_distill_desc_t;
+
+/* Bytes of workspace kan_distill_forward and kan_distill_step need (SIZE_MAX
+ * if `desc` is invalid): with few rows, the maxima and sums of a row's parts. */
+size_t kan_distill_workspace_size(const kan_distill_desc_t* desc);
+int kan_distill_forward(const kan_distill_desc_t* desc, const void* z, const void* ids, const void* t,
+                        const float* w, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream);
+int kan_distill_backward(const kan_distill_desc_t* desc, const void* z, const void* ids, const void* t,
+                         const float* w, const float* lse, const float* dloss, void* dz, void* stream);
+/* Both in one call for dloss = 1: loss, and dz of the sum of the rows' losses. */
+int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* ids, const void* t,
+                     const float* w, float* loss, void* dz, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

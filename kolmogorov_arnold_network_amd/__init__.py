@@ -16,7 +16,11 @@ from .functional import (kan_forward, kan_forward_static, kan_backward, kan_prep
                          kan_cast_f32_to_bf16, kan_workspace_size, layer_desc, workspace,
                          kan_group_forward, kan_group_backward, kan_group_workspace_size, group_desc,
                          kan_surface_forward, kan_surface_backward, kan_surface_workspace_size,
-                         surface_desc)
+                         surface_desc,
+                         kan_embed_forward, kan_embed_backward, kan_embed_workspace_size, embed_desc,
+                         kan_recur_forward, kan_recur_backward, kan_recur_step, kan_recur_workspace_size,
+                         recur_desc, kan_distill_forward, kan_distill_backward, kan_distill_step,
+                         kan_distill_workspace_size, distill_desc)
 from .modules import (KANLayer, KANNetwork, KANFunction, KANGroupedActivation, KANSurfaceLayer,
                       GroupedFunction, SurfaceFunction)
 
@@ -25,4 +29,8 @@ __all__ = ["kan_forward", "kan_forward_static", "kan_backward", "kan_prepare", "
            "kan_workspace_size", "layer_desc", "workspace", "KANLayer", "KANNetwork", "KANFunction",
            "kan_group_forward", "kan_group_backward", "kan_group_workspace_size", "group_desc",
            "kan_surface_forward", "kan_surface_backward", "kan_surface_workspace_size", "surface_desc",
+           "kan_embed_forward", "kan_embed_backward", "kan_embed_workspace_size", "embed_desc",
+           "kan_recur_forward", "kan_recur_backward", "kan_recur_step", "kan_recur_workspace_size", "recur_desc",
+           "kan_distill_forward", "kan_distill_backward", "kan_distill_step", "kan_distill_workspace_size",
+           "distill_desc",
            "KANGroupedActivation", "KANSurfaceLayer", "GroupedFunction", "SurfaceFunction"]

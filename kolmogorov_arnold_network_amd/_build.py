@@ -16,7 +16,8 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_NAME = "libkan_mi355x.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
-SOURCES = ["kan_api.cpp", "kan_plan.cpp", "kan_gather.hip", "kan_grouped.hip", "kan_mfma.hip", "kan_static.hip"]
+SOURCES = ["kan_api.cpp", "kan_plan.cpp", "kan_gather.hip", "kan_grouped.hip", "kan_mfma.hip", "kan_static.hip",
+           "kan_token_api.cpp", "kan_embed.hip", "kan_recur.hip", "kan_distill.hip"]
 
 # -packed-fp32-ops off: the compiler must not form packed float32 ALU ops.
 HIPCC_FLAGS = [

@@ -34,6 +34,9 @@ KAN_FLAG_PREPARED = 1
 KAN_FLAG_DENSE_FORWARD = 2
 KAN_FLAG_TP_FORWARD = 4
 
+KAN_I32 = 0
+KAN_I64 = 1
+
 KAN_STATIC_SCRATCH_BYTES = 32 << 20     # kan_forward_static's device array
 
 ABI_VERSION = 1
@@ -42,7 +45,10 @@ ABI_VERSION = 1
 EXPORTS = ("kan_abi_version", "kan_status_string", "kan_workspace_size", "kan_prepare",
            "kan_forward", "kan_forward_static", "kan_backward", "kan_basis_eval", "kan_basis_eval_tp", "kan_cast_f32_to_bf16",
            "kan_group_workspace_size", "kan_group_forward", "kan_group_backward",
-           "kan_surface_workspace_size", "kan_surface_forward", "kan_surface_backward")
+           "kan_surface_workspace_size", "kan_surface_forward", "kan_surface_backward",
+           "kan_embed_workspace_size", "kan_embed_forward", "kan_embed_backward",
+           "kan_recur_workspace_size", "kan_recur_forward", "kan_recur_backward", "kan_recur_step",
+           "kan_distill_workspace_size", "kan_distill_forward", "kan_distill_backward", "kan_distill_step")
 
 
 class kan_grid_t(ctypes.Structure):
@@ -64,6 +70,28 @@ class kan_group_desc_t(ctypes.Structure):
 class kan_surface_desc_t(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("P", ctypes.c_int64), ("O", ctypes.c_int64),
                 ("grid", kan_grid_t), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class kan_embed_desc_t(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("row_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class kan_recur_desc_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("x_row", ctypes.c_int64), ("x_seq", ctypes.c_int64),
+                ("g_row", ctypes.c_int64), ("g_seq", ctypes.c_int64),
+                ("dx_row", ctypes.c_int64), ("dx_seq", ctypes.c_int64),
+                ("dg_row", ctypes.c_int64), ("dg_seq", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class kan_distill_desc_t(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("z_row", ctypes.c_int64), ("dz_row", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("teacher_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("tau", ctypes.c_float)]
 
 
 class KanError(RuntimeError):
@@ -120,6 +148,21 @@ def lib():
     L.kan_surface_backward.argtypes = [P(kan_surface_desc_t), _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     L.kan_cast_f32_to_bf16.restype = ctypes.c_int
     L.kan_cast_f32_to_bf16.argtypes = [_vp, _vp, _i64, _vp]
+    for name, desc, forward, backward in (
+            ("embed", kan_embed_desc_t, [_vp] * 4, [_vp] * 4 + [_sz, _vp]),
+            ("recur", kan_recur_desc_t, [_vp] * 7 + [_sz, _vp], [_vp] * 11 + [_sz, _vp]),
+            ("distill", kan_distill_desc_t, [_vp] * 7 + [_sz, _vp], [_vp] * 8)):
+        for fn, args in (("forward", forward), ("backward", backward)):
+            f = getattr(L, "kan_%s_%s" % (name, fn))
+            f.restype = ctypes.c_int
+            f.argtypes = [P(desc)] + args
+        f = getattr(L, "kan_%s_workspace_size" % name)
+        f.restype = _sz
+        f.argtypes = [P(desc)] + ([ctypes.c_int] if name == "recur" else [])
+    L.kan_recur_step.restype = ctypes.c_int
+    L.kan_recur_step.argtypes = [P(kan_recur_desc_t), _i64] + [_vp] * 6
+    L.kan_distill_step.restype = ctypes.c_int
+    L.kan_distill_step.argtypes = [P(kan_distill_desc_t)] + [_vp] * 7 + [_sz, _vp]
     if L.kan_abi_version() != ABI_VERSION:
         raise RuntimeError("libkan ABI version %d, binding expects %d"
                            % (L.kan_abi_version(), ABI_VERSION))

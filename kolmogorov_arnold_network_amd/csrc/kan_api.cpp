@@ -13,24 +13,8 @@ namespace kan {
 
 namespace {
 
-constexpr int64_t kIndexLimit = (int64_t(1) << 31) - 4096;  // keeps 32-bit tile math safe
 constexpr int kMaxG = 125;                                      // K = G + 3 <= 128
 constexpr int64_t kF32SliceTiles = 8;                           // float32 forward: k-tiles per slice
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-    const void* p;
-    size_t n;
-};
-
-bool overlap(const Range& a, const Range& b) {
-    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? KAN_OK : KAN_ERR_HIP; }
 
 // Whether a dense bf16 cubic layer builds a basis operand once in HBM
 // rather than in every workgroup that needs it.  Inside the contraction

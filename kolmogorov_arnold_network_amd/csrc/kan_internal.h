@@ -21,6 +21,24 @@ constexpr int kTileKBytes = 128;
 
 inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
+// Argument checks shared by the entry points.
+constexpr int64_t kIndexLimit = (int64_t(1) << 31) - 4096;  // keeps 32-bit tile math safe
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Range {
+    const void* p;
+    size_t n;
+};
+
+inline bool overlap(const Range& a, const Range& b) {
+    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    return a0 < b0 + b.n && b0 < a0 + a.n;
+}
+
+inline int status_of(hipError_t e) { return e == hipSuccess ? KAN_OK : KAN_ERR_HIP; }
+
 // Block geometry of the vector-ALU kernels, shared with their host plans
 // (kan_plan.cpp).
 constexpr int kGatherFwdOutputs = 64;   // local-gather forward: outputs per block

@@ -1,0 +1,66 @@
+// Launch plans and kernel launchers of the token-side operators: embedding,
+// gated recurrence, distillation.
+#pragma once
+
+#include "kan_internal.h"
+
+namespace kan {
+
+inline int dtype_bytes(int dtype) { return dtype == KAN_F32 ? 4 : 2; }
+
+// ---- embedding ----
+// Gradient: the table is cut into ranges of `width` tokens, a block each, that
+// list their tokens' rows; the listed rows are summed in chunks of
+// kEmbedChunk.
+constexpr int64_t kEmbedMaxN = int64_t(1) << 24, kEmbedMaxV = int64_t(1) << 26, kEmbedMaxD = int64_t(1) << 23;
+constexpr int kEmbedWidth = 512;   // tokens of a range at most
+constexpr int kEmbedChunk = 32;    // listed rows of a chunk
+struct EmbedPlan {
+    int width;
+    int64_t ranges, chunks;
+    size_t off_order, off_token, off_start, off_part, ws;
+};
+EmbedPlan embed_plan(int64_t N, int64_t V, int64_t D);
+
+hipError_t launch_embed_fwd(const kan_embed_desc_t& d, const void* ids, const void* E, void* y, hipStream_t s);
+hipError_t launch_embed_bwd(const kan_embed_desc_t& d, const EmbedPlan& p, const void* ids, const void* dy, float* dE,
+                            char* ws, hipStream_t s);
+
+// ---- gated recurrence ----
+constexpr int64_t kRecurMaxChannels = int64_t(1) << 28;   // B times D, D rounded up to 64
+struct RecurPlan {
+    size_t ws;
+};
+RecurPlan recur_plan(const kan_recur_desc_t& d, int pass);
+
+struct RecurArgs {
+    const void *x, *g;
+    const float *h0, *y, *dy, *dhT;
+    const int32_t* lengths;
+    float *out, *hT, *dh0;     // out: y of the forward
+    void *dx, *dg;
+};
+hipError_t launch_recur_fwd(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s);
+hipError_t launch_recur_bwd(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s);
+hipError_t launch_recur_step(const kan_recur_desc_t& d, int64_t S, const void* x, const void* g, float* state,
+                             const int32_t* slots, float* y, hipStream_t s);
+
+// ---- distillation ----
+constexpr int64_t kDistillMaxN = int64_t(1) << 22;
+constexpr int kDistillMaxK = 1024;   // teacher logits of a row at most
+struct DistillPlan {
+    size_t ws;
+};
+DistillPlan distill_plan(const kan_distill_desc_t& d);
+
+struct DistillArgs {
+    const void *z, *ids, *t;
+    const float *w, *lse_in, *dloss;
+    float *loss, *lse;
+    void* dz;
+};
+hipError_t launch_distill(const kan_distill_desc_t& d, const DistillPlan& p, const DistillArgs& a, char* ws,
+                          hipStream_t s);            // forward (a.lse) or step (a.dz)
+hipError_t launch_distill_bwd(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s);
+
+}  // namespace kan

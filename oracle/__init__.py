@@ -15,10 +15,13 @@ Contents
 ``grouped``  per-channel (grouped) spline activation forward / backward.
 ``surface``  2-D tensor-product spline layer (pairs of inputs) forward /
              backward, and sampled helpers for large shapes.
+``token``    embedding, gated recurrence and distillation, forward and
+             backward (not on the pages; imported as ``oracle.token``).
 
-Every function cites the passage of the pages it follows.  Pinned by the
-``-m "not gpu"`` tests in ``tests/test_oracle.py``, ``test_oracle_grouped.py``
-and ``test_oracle_surface.py``; there is no function here whose parity is
+Every function of the layers cites the passage of the pages it follows.
+Pinned by the ``-m "not gpu"`` tests in ``tests/test_oracle.py``,
+``test_oracle_grouped.py``, ``test_oracle_surface.py`` and
+``test_oracle_token.py``; there is no function here whose parity is
 unpinned.
 """
 
