@@ -14,6 +14,19 @@
 //
 //     del_t = dy_t + c_{t+1},  c_t = del_t - u_t del_t (f >= u), f_t del_t,
 //     dx_t = u_t del_t,  dg_t = f_t u_t (h_{t-1} - x_t) del_t,  dh0 = c_0.
+//
+// A run of steps is h -> h - U h + b with U = 1 - prod f, accumulated as the
+// share that is lost, and two runs compose to one (the earlier first):
+// U = U1 + U2 (1 - U1), b = b2 + b1 - U2 b1.  A block takes 32 channels of a
+// sequence and walks along it in tiles, each read once: lanes hold four
+// channels and R consecutive rows in registers, compose them, the runs of a
+// wave's lanes and of the block's waves are scanned, and each lane goes over
+// its rows again from its start.  Where the sequences have too few channels
+// to fill the GPU they are cut into segments, a block each: a first launch
+// composes every segment's run, and the second starts each segment from the
+// runs before it (its inputs are then read twice).  Memory traffic bounds it;
+// the arithmetic, two transcendentals and about 20 operations an element, is
+// about half of the time that the traffic takes.
 #include "kan_token.h"
 #include "kan_vec.h"
 
@@ -24,22 +37,30 @@ namespace {
 // The shares of x (u = sigmoid(-g)) and of the state (f = sigmoid(g)), each to
 // a few ulp of its own size: the smaller one, the larger one, and whether the
 // state's is the larger.
+// It is held as one word, the smaller share with the sign bit set where x's
+// is the larger.
 struct Gate {
-    float s, l;
-    bool keep;
-    __device__ __forceinline__ explicit Gate(float g) {
-        const float e = __expf(-fabsf(g));
-        l = __builtin_amdgcn_rcpf(1.0f + e);
-        s = e * l;
-        keep = g >= 0.0f;
+    float e;
+    __device__ __forceinline__ static Gate of(float g) {
+        const float v = __expf(-fabsf(g));
+        Gate q;
+        q.e = __builtin_copysignf(v * __builtin_amdgcn_rcpf(1.0f + v), g);
+        return q;
     }
-    __device__ __forceinline__ float u() const { return keep ? s : l; }
+    __device__ __forceinline__ static Gate idle() { return Gate{0.0f}; }   // the state stays
+    __device__ __forceinline__ float s() const { return fabsf(e); }
+    __device__ __forceinline__ bool keep() const { return (int)__float_as_uint(e) >= 0; }
+    __device__ __forceinline__ float u() const { return keep() ? e : 1.0f + e; }
     __device__ __forceinline__ float step(float h, float x) const {
-        const float a = keep ? h : x, b = keep ? x : h;
-        return __builtin_fmaf(s, b - a, a);
+        const float a = keep() ? h : x, b = keep() ? x : h;
+        return __builtin_fmaf(s(), b - a, a);
     }
     __device__ __forceinline__ float back(float del) const {
-        return __builtin_fmaf(keep ? -s : s, del, keep ? del : 0.0f);
+        return __builtin_fmaf(-e, del, keep() ? del : 0.0f);
+    }
+    // 1 - (1 - U) f: the share of a run's start that is lost after this step too
+    __device__ __forceinline__ float lost(float U) const {
+        return __builtin_fmaf(e, 1.0f - U, keep() ? U : 1.0f);
     }
 };
 
@@ -47,109 +68,445 @@ __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, 
     return lengths ? min(max((int64_t)lengths[b], (int64_t)0), T) : T;
 }
 
-// The sequence and the channel of a thread (64 channels of a sequence to a block).
-__device__ __forceinline__ bool channel(const kan_recur_desc_t& d, int64_t& b, int64_t& c) {
-    const unsigned cb = (unsigned)((d.D + 63) / 64);
-    b = blockIdx.x / cb;
-    c = (int64_t)(blockIdx.x % cb) * 64 + threadIdx.x;
-    return c < d.D;
-}
+constexpr int RC = 8;              // lanes along the channels of a tile row
+constexpr int RL = 64 / RC;        // runs of rows of a wave
+constexpr int RW = kRecurWaves;    // waves of a block at most
 
-template <typename TS>
-__global__ void __launch_bounds__(64) recur_fwd_kernel(kan_recur_desc_t d, RecurArgs a) {
-    int64_t b, c;
-    if (!channel(d, b, c)) return;
-    const int64_t len = length_of(a.lengths, b, d.T);
-    const TS* x = static_cast<const TS*>(a.x) + b * d.x_seq + c;
-    const TS* g = static_cast<const TS*>(a.g) + b * d.g_seq + c;
-    float* y = a.out + b * d.T * d.D + c;
-    float h = a.h0 ? a.h0[b * d.D + c] : 0.0f;
-    for (int64_t t = 0; t < len; ++t) {
-        h = Gate(load_f(g, t * d.g_row)).step(h, load_f(x, t * d.x_row));
-        y[t * d.D] = h;
+// What a block works on: channels c .. c + VEC - 1 of sequence b, rows
+// [r0, r1) of segment seg.  Blocks that share cache lines of a row go to the
+// same XCD (blocks are dealt to the 8 XCDs in turn).  A lane whose channels
+// would pass D repeats the last ones (with the same values).
+template <int VEC>
+struct Place {
+    int64_t b, c, r0, r1, len;
+    int seg, cl, tl, w, waves;
+    __device__ __forceinline__ Place(const kan_recur_desc_t& d, const RecurPlan& p, const int32_t* lengths) {
+        const unsigned n = gridDim.x, i = blockIdx.x;
+        unsigned l = n % 8 == 0 ? i % 8 * (n / 8) + i / 8 : i;
+        const unsigned cb = l % p.blocks;
+        l /= p.blocks;
+        seg = (int)(l % p.segs);
+        b = l / p.segs;
+        const int lane = threadIdx.x & 63;
+        cl = lane % RC;
+        tl = lane / RC;
+        w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        waves = blockDim.x >> 6;
+        c = min((int64_t)cb * (RC * VEC) + cl * VEC, d.D - VEC);
+        r0 = seg * p.seg_rows;
+        r1 = min(r0 + p.seg_rows, d.T);
+        len = length_of(lengths, b, d.T);
     }
-    for (int64_t t = len; t < d.T; ++t) y[t * d.D] = 0.0f;
-    if (a.hT) a.hT[b * d.D + c] = h;
-}
+};
 
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = f2bf(v); }
-
-template <typename TS, typename TG>
-__global__ void __launch_bounds__(64) recur_bwd_kernel(kan_recur_desc_t d, RecurArgs a) {
-    int64_t b, c;
-    if (!channel(d, b, c)) return;
-    const int64_t len = length_of(a.lengths, b, d.T);
-    const TS* x = static_cast<const TS*>(a.x) + b * d.x_seq + c;
-    const TS* g = static_cast<const TS*>(a.g) + b * d.g_seq + c;
-    const float* y = a.y + b * d.T * d.D + c;
-    const float* dy = a.dy + b * d.T * d.D + c;
-    TG* dx = a.dx ? static_cast<TG*>(a.dx) + b * d.dx_seq + c : nullptr;
-    TG* dg = a.dx ? static_cast<TG*>(a.dg) + b * d.dg_seq + c : nullptr;
-    float k = a.dhT ? a.dhT[b * d.D + c] : 0.0f;
-    if (dx)
-        for (int64_t t = len; t < d.T; ++t) put(dx + t * d.dx_row, 0.0f), put(dg + t * d.dg_row, 0.0f);
-    for (int64_t t = len - 1; t >= 0; --t) {
-        const Gate q(load_f(g, t * d.g_row));
-        const float del = dy[t * d.D] + k;
-        if (dx) {
-            const float before = t > 0 ? y[(t - 1) * d.D] : a.h0 ? a.h0[b * d.D + c] : 0.0f;
-            put(dx + t * d.dx_row, q.u() * del);
-            put(dg + t * d.dg_row, q.s * q.l * (before - load_f(x, t * d.x_row)) * del);
+// A run (U, b) of VEC channels.
+template <int VEC>
+struct Run {
+    float U[VEC], b[VEC];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) U[i] = b[i] = 0.0f;
+    }
+    // the run of `before`, then this one
+    __device__ __forceinline__ void after(const Run& before) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            b[i] += __builtin_fmaf(-U[i], before.b[i], before.b[i]);
+            U[i] = __builtin_fmaf(U[i], 1.0f - before.U[i], before.U[i]);
         }
-        k = q.back(del);
     }
-    if (a.dh0) a.dh0[b * d.D + c] = k;
+    __device__ __forceinline__ void apply(float (&h)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = __builtin_fmaf(-U[i], h[i], h[i]) + b[i];
+    }
+};
+
+// Scan of the block's runs, in row order (forward) or against it (BACK).
+// `run` is a lane's own; h, the state at the tile's start, becomes the state
+// at its end, and `mine` the state at the start of the lane's rows.
+template <int VEC, bool BACK>
+__device__ __forceinline__ void scan_tile(Run<VEC> run, float (&h)[VEC], float (&mine)[VEC], int cl, int tl, int w,
+                                          int waves, Run<VEC> (*tot)[RC]) {
+    const int at = BACK ? RL - 1 - tl : tl;            // place in the order of the scan
+#pragma unroll
+    for (int k = 1; k < RL; k *= 2) {
+        Run<VEC> o;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            o.U[i] = BACK ? __shfl_down(run.U[i], k * RC, 64) : __shfl_up(run.U[i], k * RC, 64);
+            o.b[i] = BACK ? __shfl_down(run.b[i], k * RC, 64) : __shfl_up(run.b[i], k * RC, 64);
+        }
+        if (at >= k) run.after(o);
+    }
+    if (at == RL - 1) tot[w][cl] = run;
+    Run<VEC> o;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        o.U[i] = BACK ? __shfl_down(run.U[i], RC, 64) : __shfl_up(run.U[i], RC, 64);
+        o.b[i] = BACK ? __shfl_down(run.b[i], RC, 64) : __shfl_up(run.b[i], RC, 64);
+    }
+    if (at == 0) o.clear();
+    __syncthreads();
+    for (int k = 0; k < waves; ++k) {
+        const int q = BACK ? waves - 1 - k : k;
+        if (q == w) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) mine[i] = h[i];
+        }
+        tot[q][cl].apply(h);
+    }
+    o.apply(mine);
 }
 
+// The composition of all of the block's runs of a tile, in every lane.
+template <int VEC, bool BACK>
+__device__ __forceinline__ void block_run(Run<VEC> run, Run<VEC>& out, int cl, int tl, int w, int waves,
+                                          Run<VEC> (*tot)[RC]) {
+    const int at = BACK ? RL - 1 - tl : tl;
+#pragma unroll
+    for (int k = 1; k < RL; k *= 2) {
+        Run<VEC> o;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            o.U[i] = BACK ? __shfl_down(run.U[i], k * RC, 64) : __shfl_up(run.U[i], k * RC, 64);
+            o.b[i] = BACK ? __shfl_down(run.b[i], k * RC, 64) : __shfl_up(run.b[i], k * RC, 64);
+        }
+        if (at >= k) run.after(o);
+    }
+    if (at == RL - 1) tot[w][cl] = run;
+    __syncthreads();
+    out.clear();
+    for (int k = 0; k < waves; ++k) {
+        Run<VEC> o = tot[BACK ? waves - 1 - k : k][cl];
+        o.after(out);
+        out = o;
+    }
+}
+
+// Element i of a row pointer's vector at row t.
+template <typename TS, int VEC>
+__device__ __forceinline__ Raw<TS, VEC> row_at(const TS* p, int64_t t, int64_t stride) {
+    return load_raw<TS, VEC>(p + t * stride);
+}
+
+// The runs of the segments before this one (after it, BACK), from the launch
+// that composed them.
+template <int VEC, bool BACK>
+__device__ __forceinline__ void from_segments(const RecurPlan& p, const Place<VEC>& at, int64_t D, const float* runs,
+                                              float (&h)[VEC]) {
+    const int n = BACK ? p.segs - 1 - at.seg : at.seg;
+    for (int k = 0; k < n; ++k) {
+        const int q = BACK ? p.segs - 1 - k : k;
+        const float* r = runs + ((at.b * p.segs + q) * 2) * D + at.c;
+        const Raw<float, VEC> U = load_raw<float, VEC>(r), bb = load_raw<float, VEC>(r + D);
+        Run<VEC> run;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) run.U[i] = raw_value(U, i), run.b[i] = raw_value(bb, i);
+        run.apply(h);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_run(const RecurPlan& p, const Place<VEC>& at, int64_t D, float* runs,
+                                          const Run<VEC>& run) {
+    float* r = runs + ((at.b * p.segs + at.seg) * 2) * D + at.c;
+    store_vec<VEC>(r, run.U);
+    store_vec<VEC>(r + D, run.b);
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_state(const float* h0, int64_t b, int64_t D, int64_t c, float (&h)[VEC]) {
+    if (h0) {
+        const Raw<float, VEC> r = load_raw<float, VEC>(h0 + b * D + c);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = raw_value(r, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = 0.0f;
+    }
+}
+
+constexpr int RF = kRecurRowsFwd;  // rows of a lane in a tile
+constexpr int RB = kRecurRowsBwd;
+
+// Forward.  COMPOSE: only the segment's run, for the second launch.
+template <typename TS, int VEC, bool COMPOSE>
+__global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
+                                                            float* runs) {
+    __shared__ Run<VEC> tot[2][RW][RC];
+    const Place<VEC> at(d, p, a.lengths);
+    const int64_t D = d.D;
+    const TS* x = static_cast<const TS*>(a.x) + at.b * d.x_seq + at.c;
+    const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
+    float* y = a.out + at.b * d.T * D + at.c;
+    float h[VEC];
+    Run<VEC> all;
+    if (COMPOSE) {
+        all.clear();
+    } else {
+        load_state<VEC>(a.h0, at.b, D, at.c, h);
+        if (p.segs > 1) from_segments<VEC, false>(p, at, D, runs, h);
+    }
+    const int tile = at.waves * RL * RF, first = (at.w * RL + at.tl) * RF;
+    int parity = 0;
+    for (int64_t t0 = at.r0; t0 < at.r1; t0 += tile, parity ^= 1) {
+        const int64_t t = t0 + first;
+        if (t0 >= at.len) {                            // uniform: rows past the length
+            if (COMPOSE) break;
+            const float zero[VEC] = {};
+#pragma unroll
+            for (int r = 0; r < RF; ++r)
+                if (t + r < at.r1) store_vec<VEC>(y + (t + r) * D, zero);
+            continue;
+        }
+        Gate e[RF][VEC];
+        float v[RF][VEC];
+        {
+            Raw<TS, VEC> xr[RF], gr[RF];
+            const bool whole = t0 + tile <= min(at.len, at.r1);    // uniform
+#pragma unroll
+            for (int r = 0; r < RF; ++r) {
+                const int64_t q = whole ? t + r : min(t + r, at.len - 1);
+                gr[r] = row_at<TS, VEC>(g, q, d.g_row);
+                xr[r] = row_at<TS, VEC>(x, q, d.x_row);
+            }
+#pragma unroll
+            for (int r = 0; r < RF; ++r) {
+                const bool in = whole || (t + r < at.len && t + r < at.r1);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    e[r][i] = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
+                    v[r][i] = in ? raw_value(xr[r], i) : 0.0f;
+                }
+            }
+        }
+        Run<VEC> run;
+        run.clear();
+#pragma unroll
+        for (int r = 0; r < RF; ++r)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                run.b[i] = e[r][i].step(run.b[i], v[r][i]);
+                run.U[i] = e[r][i].lost(run.U[i]);
+            }
+        if (COMPOSE) {
+            Run<VEC> tile_run;
+            block_run<VEC, false>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
+            tile_run.after(all);
+            all = tile_run;
+            continue;
+        }
+        float s[VEC];
+        scan_tile<VEC, false>(run, h, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
+#pragma unroll
+        for (int r = 0; r < RF; ++r) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[i] = e[r][i].step(s[i], v[r][i]);
+            if (t + r < at.r1) {
+                float o[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? s[i] : 0.0f;
+                store_vec<VEC>(y + (t + r) * D, o);
+            }
+        }
+    }
+    if (COMPOSE) {
+        if (at.w == 0 && at.tl == 0) store_run<VEC>(p, at, D, runs, all);
+    } else if (a.hT && at.seg == p.segs - 1 && at.w == 0 && at.tl == 0) {
+        store_vec<VEC>(a.hT + at.b * D + at.c, h);
+    }
+}
+
+// Backward: the same, from the last row of a segment to its first.
+template <typename TS, typename TG, int VEC, bool COMPOSE>
+__global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
+                                                            float* runs) {
+    __shared__ Run<VEC> tot[2][RW][RC];
+    const Place<VEC> at(d, p, a.lengths);
+    const int64_t D = d.D;
+    const TS* x = static_cast<const TS*>(a.x) + at.b * d.x_seq + at.c;
+    const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
+    const float* y = a.y + at.b * d.T * D + at.c;
+    const float* dy = a.dy + at.b * d.T * D + at.c;
+    const bool grads = !COMPOSE && a.dx;
+    TG* dx = grads ? static_cast<TG*>(a.dx) + at.b * d.dx_seq + at.c : nullptr;
+    TG* dg = grads ? static_cast<TG*>(a.dg) + at.b * d.dg_seq + at.c : nullptr;
+    float c[VEC], h0[VEC];
+    Run<VEC> all;
+    if (COMPOSE) {
+        all.clear();
+    } else {
+        load_state<VEC>(a.dhT, at.b, D, at.c, c);
+        if (p.segs > 1) from_segments<VEC, true>(p, at, D, runs, c);
+        load_state<VEC>(a.h0, at.b, D, at.c, h0);
+    }
+    const int tile = at.waves * RL * RB, first = (at.w * RL + at.tl) * RB;
+    int parity = 0;
+    const int64_t tiles = (at.r1 - at.r0 + tile - 1) / tile;
+    for (int64_t k = tiles - 1; k >= 0; --k) {
+        const int64_t t0 = at.r0 + k * tile, t = t0 + first;
+        if (t0 >= at.len) {                            // uniform: rows past the length
+            if (!grads) continue;
+            const float zero[VEC] = {};
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                if (t + r < at.r1) {
+                    store_vec<VEC>(dx + (t + r) * d.dx_row, zero);
+                    store_vec<VEC>(dg + (t + r) * d.dg_row, zero);
+                }
+            continue;
+        }
+        Gate e[RB][VEC];
+        float dv[RB][VEC], diff[RB][VEC];              // dy; h_{t-1} - x_t
+        {
+            Raw<TS, VEC> xr[RB], gr[RB];
+            Raw<float, VEC> yr[RB], dr[RB];
+            const bool whole = t0 > 0 && t0 + tile <= min(at.len, at.r1);    // uniform
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int64_t q = whole ? t + r : min(t + r, at.len - 1);
+                gr[r] = row_at<TS, VEC>(g, q, d.g_row);
+                dr[r] = row_at<float, VEC>(dy, q, D);
+                if (grads) {
+                    xr[r] = row_at<TS, VEC>(x, q, d.x_row);
+                    yr[r] = row_at<float, VEC>(y, whole ? q - 1 : max(q - 1, (int64_t)0), D);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const bool in = whole || (t + r < at.len && t + r < at.r1);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    e[r][i] = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
+                    dv[r][i] = in ? raw_value(dr[r], i) : 0.0f;
+                    if (grads) {
+                        const float before = !whole && t + r == 0 ? h0[i] : raw_value(yr[r], i);
+                        diff[r][i] = in ? before - raw_value(xr[r], i) : 0.0f;
+                    }
+                }
+            }
+        }
+        Run<VEC> run;
+        run.clear();
+#pragma unroll
+        for (int r = RB - 1; r >= 0; --r)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                run.b[i] = e[r][i].back(dv[r][i] + run.b[i]);
+                run.U[i] = e[r][i].lost(run.U[i]);
+            }
+        if (COMPOSE) {
+            Run<VEC> tile_run;
+            block_run<VEC, true>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
+            tile_run.after(all);
+            all = tile_run;
+            parity ^= 1;
+            continue;
+        }
+        float s[VEC];
+        scan_tile<VEC, true>(run, c, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
+        parity ^= 1;
+        if (!grads) continue;
+#pragma unroll
+        for (int r = RB - 1; r >= 0; --r) {
+            float ox[VEC], og[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float del = dv[r][i] + s[i], sh = e[r][i].s();
+                ox[i] = e[r][i].u() * del;
+                og[i] = sh * (1.0f - sh) * diff[r][i] * del;
+                s[i] = e[r][i].back(del);
+            }
+            if (t + r < at.r1) {
+                if (t + r >= at.len)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) ox[i] = og[i] = 0.0f;
+                store_vec<VEC>(dx + (t + r) * d.dx_row, ox);
+                store_vec<VEC>(dg + (t + r) * d.dg_row, og);
+            }
+        }
+    }
+    if (COMPOSE) {
+        if (at.w == 0 && at.tl == 0) store_run<VEC>(p, at, D, runs, all);
+    } else if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
+        store_vec<VEC>(a.dh0 + at.b * D + at.c, c);
+    }
+}
+
+// One row of each sequence.  Slots differ, so no two threads share a state
+// element; the last vector of a row is cut, not moved back, because state is
+// read and written.
 template <typename TS>
 __global__ void __launch_bounds__(64) recur_step_kernel(kan_recur_desc_t d, int64_t S, const TS* x, const TS* g,
                                                         float* state, const int32_t* slots, float* y) {
-    int64_t b, c;
-    if (!channel(d, b, c)) return;
+    const unsigned cb = (unsigned)((d.D + 63) / 64);
+    const int64_t b = blockIdx.x / cb, c = (int64_t)(blockIdx.x % cb) * 64 + threadIdx.x;
+    if (c >= d.D) return;
     const int64_t slot = slots ? (int64_t)slots[b] : b;
     if (slot < 0 || slot >= S) {
         y[b * d.D + c] = 0.0f;
         return;
     }
     float* st = state + slot * d.D + c;
-    const float n = Gate(load_f(g, b * d.g_seq + c)).step(*st, load_f(x, b * d.x_seq + c));
+    const float n = Gate::of(load_f(g, b * d.g_seq + c)).step(*st, load_f(x, b * d.x_seq + c));
     *st = n;
     y[b * d.D + c] = n;
 }
 
-dim3 channel_grid(const kan_recur_desc_t& d) { return dim3((unsigned)((d.D + 63) / 64 * d.B)); }
-
-}  // namespace
-
-hipError_t launch_recur_fwd(const kan_recur_desc_t& d, const RecurPlan&, const RecurArgs& a, char*, hipStream_t s) {
-    if (d.dtype == KAN_F32)
-        hipLaunchKernelGGL(recur_fwd_kernel<float>, channel_grid(d), dim3(64), 0, s, d, a);
-    else
-        hipLaunchKernelGGL(recur_fwd_kernel<uint16_t>, channel_grid(d), dim3(64), 0, s, d, a);
+template <typename TS, int VEC>
+hipError_t fwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
+    float* runs = reinterpret_cast<float*>(ws);
+    const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
+    if (p.segs > 1) {
+        hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, true>), grid, block, 0, s, d, p, a, runs);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, false>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
 }
 
-hipError_t launch_recur_bwd(const kan_recur_desc_t& d, const RecurPlan&, const RecurArgs& a, char*, hipStream_t s) {
-    const dim3 grid = channel_grid(d);
-    if (d.dtype == KAN_F32 && d.grad_dtype == KAN_F32)
-        hipLaunchKernelGGL((recur_bwd_kernel<float, float>), grid, dim3(64), 0, s, d, a);
-    else if (d.dtype == KAN_F32)
-        hipLaunchKernelGGL((recur_bwd_kernel<float, uint16_t>), grid, dim3(64), 0, s, d, a);
-    else if (d.grad_dtype == KAN_F32)
-        hipLaunchKernelGGL((recur_bwd_kernel<uint16_t, float>), grid, dim3(64), 0, s, d, a);
-    else
-        hipLaunchKernelGGL((recur_bwd_kernel<uint16_t, uint16_t>), grid, dim3(64), 0, s, d, a);
+template <typename TS, typename TG, int VEC>
+hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
+    float* runs = reinterpret_cast<float*>(ws);
+    const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
+    if (p.segs > 1) {
+        hipLaunchKernelGGL((recur_bwd_kernel<TS, float, VEC, true>), grid, block, 0, s, d, p, a, runs);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, false>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
+}
+
+template <typename TS, typename TG>
+hipError_t bwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
+    return p.vec == 4 ? bwd_t<TS, TG, 4>(d, p, a, ws, s) : bwd_t<TS, TG, 1>(d, p, a, ws, s);
+}
+
+}  // namespace
+
+hipError_t launch_recur_fwd(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws,
+                            hipStream_t s) {
+    if (d.dtype == KAN_F32) return p.vec == 4 ? fwd_t<float, 4>(d, p, a, ws, s) : fwd_t<float, 1>(d, p, a, ws, s);
+    return p.vec == 4 ? fwd_t<uint16_t, 4>(d, p, a, ws, s) : fwd_t<uint16_t, 1>(d, p, a, ws, s);
+}
+
+hipError_t launch_recur_bwd(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws,
+                            hipStream_t s) {
+    if (d.dtype == KAN_F32)
+        return d.grad_dtype == KAN_F32 ? bwd_v<float, float>(d, p, a, ws, s) : bwd_v<float, uint16_t>(d, p, a, ws, s);
+    return d.grad_dtype == KAN_F32 ? bwd_v<uint16_t, float>(d, p, a, ws, s)
+                                   : bwd_v<uint16_t, uint16_t>(d, p, a, ws, s);
 }
 
 hipError_t launch_recur_step(const kan_recur_desc_t& d, int64_t S, const void* x, const void* g, float* state,
                              const int32_t* slots, float* y, hipStream_t s) {
+    const dim3 grid((unsigned)((d.D + 63) / 64 * d.B));
     if (d.dtype == KAN_F32)
-        hipLaunchKernelGGL(recur_step_kernel<float>, channel_grid(d), dim3(64), 0, s, d, S,
+        hipLaunchKernelGGL(recur_step_kernel<float>, grid, dim3(64), 0, s, d, S,
                            static_cast<const float*>(x), static_cast<const float*>(g), state, slots, y);
     else
-        hipLaunchKernelGGL(recur_step_kernel<uint16_t>, channel_grid(d), dim3(64), 0, s, d, S,
+        hipLaunchKernelGGL(recur_step_kernel<uint16_t>, grid, dim3(64), 0, s, d, S,
                            static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(g), state, slots, y);
     return hipGetLastError();
 }

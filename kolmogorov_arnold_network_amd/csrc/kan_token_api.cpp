@@ -136,7 +136,27 @@ EmbedPlan embed_plan(int64_t N, int64_t V, int64_t D) {
     return p;
 }
 
-RecurPlan recur_plan(const kan_recur_desc_t&, int) { return RecurPlan{0}; }
+RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
+    RecurPlan p;
+    p.vec = d.D >= 4 ? 4 : 1;
+    p.blocks = (unsigned)((d.D + 8 * p.vec - 1) / (8 * p.vec));
+    const int wave_rows = 8 * (pass == KAN_PASS_FORWARD ? kRecurRowsFwd : kRecurRowsBwd);
+    p.waves = 1;
+    while (p.waves < kRecurWaves && p.waves * wave_rows < d.T) p.waves *= 2;
+    // Two blocks of 8 waves for each of the 256 compute units; sequences that
+    // give fewer are cut into segments of whole tiles, at least two each.
+    const int64_t have = d.B * p.blocks, tile = p.waves * wave_rows;
+    const int64_t want = have > 0 ? (512 + have - 1) / have : 1;
+    const int64_t segs = std::min<int64_t>(std::min<int64_t>(64, want), d.T / (2 * tile));
+    p.seg_rows = std::max<int64_t>(d.T, 1);
+    p.segs = 1;
+    if (segs > 1) {
+        p.seg_rows = round_up((d.T + segs - 1) / segs, tile);
+        p.segs = (int)((d.T + p.seg_rows - 1) / p.seg_rows);
+    }
+    p.ws = p.segs > 1 ? (size_t)round_up(d.B * p.segs * 2 * d.D * 4, 256) : 0;
+    return p;
+}
 
 DistillPlan distill_plan(const kan_distill_desc_t&) { return DistillPlan{0}; }
 
