@@ -27,6 +27,8 @@
 // runs before it (its inputs are then read twice).  Memory traffic bounds it;
 // the arithmetic, two transcendentals and about 20 operations an element, is
 // about half of the time that the traffic takes.
+#include <type_traits>
+
 #include "kan_token.h"
 #include "kan_vec.h"
 
@@ -68,15 +70,13 @@ __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, 
     return lengths ? min(max((int64_t)lengths[b], (int64_t)0), T) : T;
 }
 
-constexpr int RC = 8;              // lanes along the channels of a tile row
-constexpr int RL = 64 / RC;        // runs of rows of a wave
 constexpr int RW = kRecurWaves;    // waves of a block at most
 
 // What a block works on: channels c .. c + VEC - 1 of sequence b, rows
 // [r0, r1) of segment seg.  Blocks that share cache lines of a row go to the
 // same XCD (blocks are dealt to the 8 XCDs in turn).  A lane whose channels
 // would pass D repeats the last ones (with the same values).
-template <int VEC>
+template <int VEC, int RC>
 struct Place {
     int64_t b, c, r0, r1, len;
     int seg, cl, tl, w, waves;
@@ -124,9 +124,10 @@ struct Run {
 // Scan of the block's runs, in row order (forward) or against it (BACK).
 // `run` is a lane's own; h, the state at the tile's start, becomes the state
 // at its end, and `mine` the state at the start of the lane's rows.
-template <int VEC, bool BACK>
+template <int VEC, int RC, bool BACK>
 __device__ __forceinline__ void scan_tile(Run<VEC> run, float (&h)[VEC], float (&mine)[VEC], int cl, int tl, int w,
                                           int waves, Run<VEC> (*tot)[RC]) {
+    constexpr int RL = 64 / RC;
     const int at = BACK ? RL - 1 - tl : tl;            // place in the order of the scan
 #pragma unroll
     for (int k = 1; k < RL; k *= 2) {
@@ -159,9 +160,10 @@ __device__ __forceinline__ void scan_tile(Run<VEC> run, float (&h)[VEC], float (
 }
 
 // The composition of all of the block's runs of a tile, in every lane.
-template <int VEC, bool BACK>
+template <int VEC, int RC, bool BACK>
 __device__ __forceinline__ void block_run(Run<VEC> run, Run<VEC>& out, int cl, int tl, int w, int waves,
                                           Run<VEC> (*tot)[RC]) {
+    constexpr int RL = 64 / RC;
     const int at = BACK ? RL - 1 - tl : tl;
 #pragma unroll
     for (int k = 1; k < RL; k *= 2) {
@@ -189,24 +191,31 @@ __device__ __forceinline__ Raw<TS, VEC> row_at(const TS* p, int64_t t, int64_t s
     return load_raw<TS, VEC>(p + t * stride);
 }
 
-// The runs of the segments before this one (after it, BACK), from the launch
-// that composed them.
-template <int VEC, bool BACK>
-__device__ __forceinline__ void from_segments(const RecurPlan& p, const Place<VEC>& at, int64_t D, const float* runs,
-                                              float (&h)[VEC]) {
-    const int n = BACK ? p.segs - 1 - at.seg : at.seg;
-    for (int k = 0; k < n; ++k) {
-        const int q = BACK ? p.segs - 1 - k : k;
-        const float* r = runs + ((at.b * p.segs + q) * 2) * D + at.c;
+// h after the runs of the segments before this one (after it, BACK), from the
+// launch that composed them: each of the block's runs of lanes composes a
+// share of them, and the shares are scanned like a tile's.
+template <int VEC, int RC, bool BACK, typename P>
+__device__ __forceinline__ void from_segments(const RecurPlan& p, const P& at, int64_t D, const float* runs,
+                                              float (&h)[VEC], Run<VEC> (*tot)[RC]) {
+    const int groups = at.waves * (64 / RC), g = at.w * (64 / RC) + at.tl;
+    const int n = BACK ? p.segs - 1 - at.seg : at.seg, each = (n + groups - 1) / groups;
+    const int k0 = (BACK ? groups - 1 - g : g) * each, k1 = min(k0 + each, n);
+    Run<VEC> run;
+    run.clear();
+    for (int k = k0; k < k1; ++k) {
+        const float* r = runs + ((at.b * p.segs + (BACK ? p.segs - 1 - k : k)) * 2) * D + at.c;
         const Raw<float, VEC> U = load_raw<float, VEC>(r), bb = load_raw<float, VEC>(r + D);
-        Run<VEC> run;
+        Run<VEC> one;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) run.U[i] = raw_value(U, i), run.b[i] = raw_value(bb, i);
-        run.apply(h);
+        for (int i = 0; i < VEC; ++i) one.U[i] = raw_value(U, i), one.b[i] = raw_value(bb, i);
+        one.after(run);
+        run = one;
     }
+    float mine[VEC];
+    scan_tile<VEC, RC, BACK>(run, h, mine, at.cl, at.tl, at.w, at.waves, tot);
 }
-template <int VEC>
-__device__ __forceinline__ void store_run(const RecurPlan& p, const Place<VEC>& at, int64_t D, float* runs,
+template <int VEC, typename P>
+__device__ __forceinline__ void store_run(const RecurPlan& p, const P& at, int64_t D, float* runs,
                                           const Run<VEC>& run) {
     float* r = runs + ((at.b * p.segs + at.seg) * 2) * D + at.c;
     store_vec<VEC>(r, run.U);
@@ -225,15 +234,15 @@ __device__ __forceinline__ void load_state(const float* h0, int64_t b, int64_t D
     }
 }
 
-constexpr int RF = kRecurRowsFwd;  // rows of a lane in a tile
-constexpr int RB = kRecurRowsBwd;
+constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 
 // Forward.  COMPOSE: only the segment's run, for the second launch.
-template <typename TS, int VEC, bool COMPOSE>
+template <typename TS, int VEC, int RC, bool COMPOSE>
 __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
                                                             float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
-    const Place<VEC> at(d, p, a.lengths);
+    constexpr int RL = 64 / RC;
+    const Place<VEC, RC> at(d, p, a.lengths);
     const int64_t D = d.D;
     const TS* x = static_cast<const TS*>(a.x) + at.b * d.x_seq + at.c;
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
@@ -244,9 +253,29 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
         all.clear();
     } else {
         load_state<VEC>(a.h0, at.b, D, at.c, h);
-        if (p.segs > 1) from_segments<VEC, false>(p, at, D, runs, h);
+        if (p.segs > 1) from_segments<VEC, RC, false>(p, at, D, runs, h, tot[1]);
     }
     const int tile = at.waves * RL * RF, first = (at.w * RL + at.tl) * RF;
+    const int64_t inside = min(at.len, at.r1);
+    Raw<TS, VEC> xr[RF], gr[RF];
+    auto load = [&](int64_t t0) {
+        const int64_t t = t0 + first;
+        if (t0 + tile <= inside) {                     // uniform
+#pragma unroll
+            for (int r = 0; r < RF; ++r) {
+                gr[r] = row_at<TS, VEC>(g, t + r, d.g_row);
+                xr[r] = row_at<TS, VEC>(x, t + r, d.x_row);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < RF; ++r) {
+                const int64_t q = min(t + r, at.len - 1);
+                gr[r] = row_at<TS, VEC>(g, q, d.g_row);
+                xr[r] = row_at<TS, VEC>(x, q, d.x_row);
+            }
+        }
+    };
+    if (at.r0 < inside) load(at.r0);
     int parity = 0;
     for (int64_t t0 = at.r0; t0 < at.r1; t0 += tile, parity ^= 1) {
         const int64_t t = t0 + first;
@@ -258,54 +287,55 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
                 if (t + r < at.r1) store_vec<VEC>(y + (t + r) * D, zero);
             continue;
         }
-        Gate e[RF][VEC];
-        float v[RF][VEC];
-        {
-            Raw<TS, VEC> xr[RF], gr[RF];
-            const bool whole = t0 + tile <= min(at.len, at.r1);    // uniform
+        const bool whole = t0 + tile <= inside;        // uniform
+        // U and b of the lane's rows up to each row: from them a row's state is
+        // two operations once the state before the lane's rows is known
+        Run<VEC> run, upto[RF];
+        run.clear();
+        auto compose = [&](auto checked) {
 #pragma unroll
             for (int r = 0; r < RF; ++r) {
-                const int64_t q = whole ? t + r : min(t + r, at.len - 1);
-                gr[r] = row_at<TS, VEC>(g, q, d.g_row);
-                xr[r] = row_at<TS, VEC>(x, q, d.x_row);
-            }
-#pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                const bool in = whole || (t + r < at.len && t + r < at.r1);
+                const bool in = !checked.value || (t + r < at.len && t + r < at.r1);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    e[r][i] = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
-                    v[r][i] = in ? raw_value(xr[r], i) : 0.0f;
+                    const Gate e = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
+                    run.b[i] = e.step(run.b[i], in ? raw_value(xr[r], i) : 0.0f);
+                    run.U[i] = e.lost(run.U[i]);
                 }
+                upto[r] = run;
             }
-        }
-        Run<VEC> run;
-        run.clear();
-#pragma unroll
-        for (int r = 0; r < RF; ++r)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                run.b[i] = e[r][i].step(run.b[i], v[r][i]);
-                run.U[i] = e[r][i].lost(run.U[i]);
-            }
+        };
+        if (whole) compose(std::false_type());
+        else compose(std::true_type());
+        if (t0 + tile < inside) load(t0 + tile);       // arrives during the scan and the stores
         if (COMPOSE) {
             Run<VEC> tile_run;
-            block_run<VEC, false>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
+            block_run<VEC, RC, false>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
             tile_run.after(all);
             all = tile_run;
             continue;
         }
         float s[VEC];
-        scan_tile<VEC, false>(run, h, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
+        scan_tile<VEC, RC, false>(run, h, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
+        if (whole) {
 #pragma unroll
-        for (int r = 0; r < RF; ++r) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s[i] = e[r][i].step(s[i], v[r][i]);
-            if (t + r < at.r1) {
+            for (int r = 0; r < RF; ++r) {
                 float o[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? s[i] : 0.0f;
+                for (int i = 0; i < VEC; ++i) o[i] = s[i];
+                upto[r].apply(o);
                 store_vec<VEC>(y + (t + r) * D, o);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < RF; ++r) {
+                float o[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] = s[i];
+                upto[r].apply(o);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? o[i] : 0.0f;
+                if (t + r < at.r1) store_vec<VEC>(y + (t + r) * D, o);
             }
         }
     }
@@ -317,11 +347,12 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
 }
 
 // Backward: the same, from the last row of a segment to its first.
-template <typename TS, typename TG, int VEC, bool COMPOSE>
+template <typename TS, typename TG, int VEC, int RC, bool COMPOSE>
 __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
                                                             float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
-    const Place<VEC> at(d, p, a.lengths);
+    constexpr int RL = 64 / RC;
+    const Place<VEC, RC> at(d, p, a.lengths);
     const int64_t D = d.D;
     const TS* x = static_cast<const TS*>(a.x) + at.b * d.x_seq + at.c;
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
@@ -336,7 +367,7 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
         all.clear();
     } else {
         load_state<VEC>(a.dhT, at.b, D, at.c, c);
-        if (p.segs > 1) from_segments<VEC, true>(p, at, D, runs, c);
+        if (p.segs > 1) from_segments<VEC, RC, true>(p, at, D, runs, c, tot[1]);
         load_state<VEC>(a.h0, at.b, D, at.c, h0);
     }
     const int tile = at.waves * RL * RB, first = (at.w * RL + at.tl) * RB;
@@ -357,34 +388,36 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
         }
         Gate e[RB][VEC];
         float dv[RB][VEC], diff[RB][VEC];              // dy; h_{t-1} - x_t
-        {
+        const bool whole = t0 > 0 && t0 + tile <= min(at.len, at.r1);    // uniform
+        auto load = [&](auto checked) {
             Raw<TS, VEC> xr[RB], gr[RB];
             Raw<float, VEC> yr[RB], dr[RB];
-            const bool whole = t0 > 0 && t0 + tile <= min(at.len, at.r1);    // uniform
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                const int64_t q = whole ? t + r : min(t + r, at.len - 1);
+                const int64_t q = checked.value ? min(t + r, at.len - 1) : t + r;
                 gr[r] = row_at<TS, VEC>(g, q, d.g_row);
                 dr[r] = row_at<float, VEC>(dy, q, D);
                 if (grads) {
                     xr[r] = row_at<TS, VEC>(x, q, d.x_row);
-                    yr[r] = row_at<float, VEC>(y, whole ? q - 1 : max(q - 1, (int64_t)0), D);
+                    yr[r] = row_at<float, VEC>(y, checked.value ? max(q - 1, (int64_t)0) : q - 1, D);
                 }
             }
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                const bool in = whole || (t + r < at.len && t + r < at.r1);
+                const bool in = !checked.value || (t + r < at.len && t + r < at.r1);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     e[r][i] = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
                     dv[r][i] = in ? raw_value(dr[r], i) : 0.0f;
                     if (grads) {
-                        const float before = !whole && t + r == 0 ? h0[i] : raw_value(yr[r], i);
+                        const float before = checked.value && t + r == 0 ? h0[i] : raw_value(yr[r], i);
                         diff[r][i] = in ? before - raw_value(xr[r], i) : 0.0f;
                     }
                 }
             }
-        }
+        };
+        if (whole) load(std::false_type());
+        else load(std::true_type());
         Run<VEC> run;
         run.clear();
 #pragma unroll
@@ -396,14 +429,14 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
             }
         if (COMPOSE) {
             Run<VEC> tile_run;
-            block_run<VEC, true>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
+            block_run<VEC, RC, true>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
             tile_run.after(all);
             all = tile_run;
             parity ^= 1;
             continue;
         }
         float s[VEC];
-        scan_tile<VEC, true>(run, c, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
+        scan_tile<VEC, RC, true>(run, c, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
         parity ^= 1;
         if (!grads) continue;
 #pragma unroll
@@ -452,43 +485,51 @@ __global__ void __launch_bounds__(64) recur_step_kernel(kan_recur_desc_t d, int6
     y[b * d.D + c] = n;
 }
 
-template <typename TS, int VEC>
+template <typename TS, int VEC, int RC>
 hipError_t fwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, true>), grid, block, 0, s, d, p, a, runs);
+        hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, true>), grid, block, 0, s, d, p, a, runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, false>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, false>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
 }
 
-template <typename TS, typename TG, int VEC>
+template <typename TS, typename TG, int VEC, int RC>
 hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_bwd_kernel<TS, float, VEC, true>), grid, block, 0, s, d, p, a, runs);
+        hipLaunchKernelGGL((recur_bwd_kernel<TS, float, VEC, RC, true>), grid, block, 0, s, d, p, a, runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, false>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, false>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
+}
+
+template <typename TS>
+hipError_t fwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
+    if (p.vec == 1) return fwd_t<TS, 1, 4>(d, p, a, ws, s);
+    return p.lanes == 16 ? fwd_t<TS, 4, 16>(d, p, a, ws, s)
+                         : p.lanes == 8 ? fwd_t<TS, 4, 8>(d, p, a, ws, s) : fwd_t<TS, 4, 4>(d, p, a, ws, s);
 }
 
 template <typename TS, typename TG>
 hipError_t bwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
-    return p.vec == 4 ? bwd_t<TS, TG, 4>(d, p, a, ws, s) : bwd_t<TS, TG, 1>(d, p, a, ws, s);
+    if (p.vec == 1) return bwd_t<TS, TG, 1, 4>(d, p, a, ws, s);
+    return p.lanes == 16 ? bwd_t<TS, TG, 4, 16>(d, p, a, ws, s)
+                         : p.lanes == 8 ? bwd_t<TS, TG, 4, 8>(d, p, a, ws, s) : bwd_t<TS, TG, 4, 4>(d, p, a, ws, s);
 }
 
 }  // namespace
 
 hipError_t launch_recur_fwd(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws,
                             hipStream_t s) {
-    if (d.dtype == KAN_F32) return p.vec == 4 ? fwd_t<float, 4>(d, p, a, ws, s) : fwd_t<float, 1>(d, p, a, ws, s);
-    return p.vec == 4 ? fwd_t<uint16_t, 4>(d, p, a, ws, s) : fwd_t<uint16_t, 1>(d, p, a, ws, s);
+    return d.dtype == KAN_F32 ? fwd_v<float>(d, p, a, ws, s) : fwd_v<uint16_t>(d, p, a, ws, s);
 }
 
 hipError_t launch_recur_bwd(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws,

@@ -136,24 +136,46 @@ EmbedPlan embed_plan(int64_t N, int64_t V, int64_t D) {
     return p;
 }
 
-RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
+RecurPlan recur_plan(const kan_recur_desc_t& d) {
+    // A block's time goes with its tiles, and the launch's with the most
+    // blocks that a compute unit gets.  Narrow blocks (fewer lanes along the
+    // channels) make more and shorter columns, at 32 or 64 bytes of a bf16 row
+    // a tile row; measured, that costs about 1.25 and 1.6 times as much an
+    // element.  Segments read x and g (g and dy) twice and take a launch more,
+    // about three tiles' time.
+    constexpr int64_t kCUs = 256;
     RecurPlan p;
     p.vec = d.D >= 4 ? 4 : 1;
-    p.blocks = (unsigned)((d.D + 8 * p.vec - 1) / (8 * p.vec));
-    const int wave_rows = 8 * (pass == KAN_PASS_FORWARD ? kRecurRowsFwd : kRecurRowsBwd);
-    p.waves = 1;
-    while (p.waves < kRecurWaves && p.waves * wave_rows < d.T) p.waves *= 2;
-    // Two blocks of 8 waves for each of the 256 compute units; sequences that
-    // give fewer are cut into segments of whole tiles, at least two each.
-    const int64_t have = d.B * p.blocks, tile = p.waves * wave_rows;
-    const int64_t want = have > 0 ? (512 + have - 1) / have : 1;
-    const int64_t segs = std::min<int64_t>(std::min<int64_t>(64, want), d.T / (2 * tile));
-    p.seg_rows = std::max<int64_t>(d.T, 1);
-    p.segs = 1;
-    if (segs > 1) {
-        p.seg_rows = round_up((d.T + segs - 1) / segs, tile);
-        p.segs = (int)((d.T + p.seg_rows - 1) / p.seg_rows);
+    const int64_t T = std::max<int64_t>(d.T, 1);
+    double least = 0;
+    auto weigh = [&](int lanes, int64_t segs) {
+        const int64_t tile = kRecurWaves * kRecurRows * (64 / lanes);
+        const int64_t blocks = (d.D + lanes * p.vec - 1) / (lanes * p.vec);
+        const int64_t rows = segs > 1 ? round_up((T + segs - 1) / segs, tile) : T;
+        segs = (T + rows - 1) / rows;
+        const double narrow = lanes == 16 ? 1.0 : lanes == 8 ? 1.25 : 1.6;
+        const double most = (double)((d.B * blocks * segs + kCUs - 1) / kCUs), tiles = (double)((rows + tile - 1) / tile);
+        const double est = most * tiles * narrow * (segs > 1 ? 1.6 : 1.0) + (segs > 1 ? 3.0 : 0.0);
+        if (least > 0 && est >= least) return;
+        least = est;
+        p.lanes = lanes;
+        p.segs = (int)segs;
+        p.seg_rows = rows;
+        p.blocks = (unsigned)blocks;
+    };
+    if (p.vec == 1) {
+        weigh(4, 1);
+    } else {
+        for (int lanes : {16, 8, 4}) weigh(lanes, 1);
     }
+    const int lanes = p.vec == 1 ? 4 : 16;
+    const int64_t tile = kRecurWaves * kRecurRows * (64 / lanes);
+    const int64_t have = std::max<int64_t>(1, d.B * ((d.D + lanes * p.vec - 1) / (lanes * p.vec)));
+    const int64_t segs = std::min<int64_t>(std::min<int64_t>(256, kCUs / have), T / (2 * tile));
+    if (segs > 1) weigh(lanes, segs);
+    const int wave_rows = kRecurRows * (64 / p.lanes);
+    p.waves = 1;
+    while (p.waves < kRecurWaves && p.waves * wave_rows < p.seg_rows) p.waves *= 2;
     p.ws = p.segs > 1 ? (size_t)round_up(d.B * p.segs * 2 * d.D * 4, 256) : 0;
     return p;
 }
@@ -207,7 +229,7 @@ int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void
 
 size_t kan_recur_workspace_size(const kan_recur_desc_t* desc, int pass) {
     if (recur_check(desc) != KAN_OK || (pass != KAN_PASS_FORWARD && pass != KAN_PASS_BACKWARD)) return SIZE_MAX;
-    return desc->B == 0 || desc->T == 0 ? 0 : recur_plan(*desc, pass).ws;
+    return desc->B == 0 || desc->T == 0 ? 0 : recur_plan(*desc).ws;
 }
 
 int kan_recur_forward(const kan_recur_desc_t* desc, const void* x, const void* g, const float* h0,
@@ -230,7 +252,7 @@ int kan_recur_forward(const kan_recur_desc_t* desc, const void* x, const void* g
     RecurArgs a = {};
     a.x = x, a.g = g, a.h0 = h0, a.lengths = lengths, a.out = y, a.hT = hT;
     (void)hipGetLastError();
-    return status_of(launch_recur_fwd(*desc, recur_plan(*desc, KAN_PASS_FORWARD), a, static_cast<char*>(ws),
+    return status_of(launch_recur_fwd(*desc, recur_plan(*desc), a, static_cast<char*>(ws),
                                       (hipStream_t)stream));
 }
 
@@ -285,7 +307,7 @@ int kan_recur_backward(const kan_recur_desc_t* desc, const void* x, const void* 
     a.x = x, a.g = g, a.h0 = h0, a.lengths = lengths, a.y = y, a.dy = dy, a.dhT = dhT, a.dx = dx, a.dg = dg,
     a.dh0 = dh0;
     (void)hipGetLastError();
-    return status_of(launch_recur_bwd(*desc, recur_plan(*desc, KAN_PASS_BACKWARD), a, static_cast<char*>(ws),
+    return status_of(launch_recur_bwd(*desc, recur_plan(*desc), a, static_cast<char*>(ws),
                                       (hipStream_t)stream));
 }
 
