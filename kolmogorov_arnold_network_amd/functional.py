@@ -314,85 +314,122 @@ def kan_cast_f32_to_bf16(t, out=None):
 
 
 # ---- token rows, sequence mixing and distillation -------------------------------
+#
+# These are called once a token when serving, so their host side is kept short:
+# tensors are checked through their device number, addresses and the stream go
+# to the library as plain integers.
 
 _INDEX = {torch.int32: L.KAN_I32, torch.int64: L.KAN_I64}
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_NO_WS = ctypes.c_size_t(-1).value
 
 
-def _check_device(t, name, dtypes, device=None):
-    """As ``_check_tensor``, for a tensor whose rows may be strided."""
+def _dev(t, name):
+    """The device number of a call's first tensor."""
+    k = t.get_device()
+    if k < 0:
+        raise ValueError("%s must be a device tensor" % name)
+    return k
+
+
+def _rows(t, name, dtypes, dev, shape=None):
+    """Checks a tensor whose last dimension alone must be contiguous (None passes)."""
     if t is None:
         return
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on device %d, is on %s" % (name, dev, t.device))
     if t.dtype not in dtypes:
         raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, tuple(dtypes)))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("the last dimension of %s must be contiguous" % name)
-
-
-def _check_shape(t, name, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _sized_ws(ws, n, device):
-    """The caller's workspace, or a fresh one of ``n`` bytes (none for an invalid
-    description, which the entry point itself refuses with its status)."""
-    if n == ctypes.c_size_t(-1).value:
+def _whole(t, name, dtypes, dev, shape=None):
+    """Checks a contiguous tensor (None passes)."""
+    if t is None:
+        return
+    _rows(t, name, dtypes, dev, shape)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _sized_ws(ws, n, t):
+    """The caller's workspace, or a fresh one of ``n`` bytes on ``t``'s device
+    (none for an invalid description, which the entry point itself refuses)."""
+    if ws is not None:
+        return _check_ws(ws, t.device)
+    if n == 0 or n == _NO_WS:
         return None, 0
-    if ws is None:
-        return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), int(n)
-    return _check_ws(ws, device)
+    return torch.empty(n, dtype=torch.uint8, device=t.device), n
 
 
-def kan_embed_workspace_size(desc):
-    n = L.lib().kan_embed_workspace_size(ctypes.byref(desc))
-    if n == ctypes.c_size_t(-1).value:
-        raise ValueError("invalid embedding description")
+def _valid_size(n, what):
+    if n == _NO_WS:
+        raise ValueError("invalid %s description" % what)
     return int(n)
 
 
 def embed_desc(n, V, D, table_dtype, row_dtype, id_dtype, scale):
     """``kan_embed_desc_t`` of ``n`` tokens over a table ``[V, D]``."""
-    return L.kan_embed_desc_t(int(n), int(V), int(D), _DTYPES[table_dtype], _DTYPES[row_dtype], _INDEX[id_dtype],
-                              float(scale))
+    return L.kan_embed_desc_t(n, V, D, _DTYPES[table_dtype], _DTYPES[row_dtype], _INDEX[id_dtype], scale)
+
+
+def kan_embed_workspace_size(desc):
+    return _valid_size(L.lib().kan_embed_workspace_size(desc), "embedding")
 
 
 def kan_embed_forward(ids, table, scale=1.0, row_dtype=None, out=None):
     """``y [*ids.shape, D] = scale * table[ids]``, rounded once to ``row_dtype``
     (default: the table's); the rows of ids outside the table are zero."""
-    _check_tensor(ids, "ids", _INDEX)
-    _check_tensor(table, "table", _DTYPES, ids.device)
+    dev = _dev(ids, "ids")
+    _whole(ids, "ids", _INDEX, dev)
+    _whole(table, "table", _DTYPES, dev)
     if table.dim() != 2:
         raise ValueError("table must be [V, D]")
     V, D = table.shape
-    row_dtype = row_dtype or (out.dtype if out is not None else table.dtype)
+    row_dtype = row_dtype or (table.dtype if out is None else out.dtype)
     if row_dtype not in _DTYPES:
         raise ValueError("row_dtype must be one of %s" % (tuple(_DTYPES),))
-    y = out if out is not None else torch.empty((*ids.shape, D), dtype=row_dtype, device=ids.device)
-    _check_tensor(y, "y", (row_dtype,), ids.device)
-    _check_shape(y, "y", (*ids.shape, D))
+    if out is None:
+        y = table.new_empty((*ids.shape, D), dtype=row_dtype)
+    else:
+        y = out
+        _whole(y, "y", (row_dtype,), dev, (*ids.shape, D))
     desc = embed_desc(ids.numel(), V, D, table.dtype, row_dtype, ids.dtype, scale)
-    L.check(L.lib().kan_embed_forward(ctypes.byref(desc), _ptr(ids), _ptr(table), _ptr(y), _stream(ids)),
+    L.check(L.lib().kan_embed_forward(desc, ids.data_ptr(), table.data_ptr(), y.data_ptr(), _raw_stream(dev)),
             "kan_embed_forward")
     return y
 
 
 def kan_embed_backward(ids, dy, num_rows, scale=1.0, ws=None, out=None):
     """``dE [num_rows, D]`` float32 of the lookup, from ``dy [*ids.shape, D]``."""
-    _check_tensor(ids, "ids", _INDEX)
-    _check_tensor(dy, "dy", _DTYPES, ids.device)
-    if dy.dim() < 1 or tuple(dy.shape[:-1]) != tuple(ids.shape):
+    dev = _dev(ids, "ids")
+    _whole(ids, "ids", _INDEX, dev)
+    _whole(dy, "dy", _DTYPES, dev)
+    if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
         raise ValueError("dy must be [*ids.shape, D], got %s" % (tuple(dy.shape),))
     D = dy.shape[-1]
-    dE = out if out is not None else torch.empty((num_rows, D), dtype=torch.float32, device=ids.device)
-    _check_out(dE, "dE", (num_rows, D), ids.device)
+    if out is None:
+        dE = dy.new_empty((num_rows, D), dtype=torch.float32)
+    else:
+        dE = out
+        _whole(dE, "dE", _F32, dev, (num_rows, D))
     desc = embed_desc(ids.numel(), num_rows, D, torch.float32, dy.dtype, ids.dtype, scale)
-    buf, n = _sized_ws(ws, L.lib().kan_embed_workspace_size(ctypes.byref(desc)), ids.device)
-    L.check(L.lib().kan_embed_backward(ctypes.byref(desc), _ptr(ids), _ptr(dy), _ptr(dE), _ptr(buf), n,
-                                       _stream(ids)), "kan_embed_backward")
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_embed_workspace_size(desc), dy)
+    L.check(lib.kan_embed_backward(desc, ids.data_ptr(), dy.data_ptr(), dE.data_ptr(), _addr(buf), n,
+                                   _raw_stream(dev)), "kan_embed_backward")
     return dE
 
 
@@ -401,50 +438,52 @@ def recur_desc(x, g, dx=None, dg=None):
     ``dg``, all ``[B, T, D]`` with any strides between rows and sequences."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D], got %s" % (tuple(x.shape),))
-    _check_shape(g, "g", x.shape)
+    if g.shape != x.shape:
+        raise ValueError("g must be %s, got %s" % (tuple(x.shape), tuple(g.shape)))
     if x.dtype != g.dtype:
         raise ValueError("x and g must share one dtype")
-    d = L.kan_recur_desc_t()
-    d.B, d.T, d.D = x.shape
-    for name, t in (("x", x), ("g", g), ("dx", dx), ("dg", dg)):
-        if t is not None:
-            setattr(d, name + "_row", t.stride(1))
-            setattr(d, name + "_seq", t.stride(0))
-    d.dtype = _DTYPES[x.dtype]
-    d.grad_dtype = _DTYPES[dx.dtype] if dx is not None else L.KAN_F32
-    return d
+    xs, gs = x.stride(), g.stride()
+    if dx is None:
+        return L.kan_recur_desc_t(*x.shape, xs[1], xs[0], gs[1], gs[0], 0, 0, 0, 0, _DTYPES[x.dtype], L.KAN_F32)
+    ds, es = dx.stride(), dg.stride()
+    return L.kan_recur_desc_t(*x.shape, xs[1], xs[0], gs[1], gs[0], ds[1], ds[0], es[1], es[0], _DTYPES[x.dtype],
+                              _DTYPES[dx.dtype])
 
 
 def kan_recur_workspace_size(desc, pass_):
-    n = L.lib().kan_recur_workspace_size(ctypes.byref(desc), int(pass_))
-    if n == ctypes.c_size_t(-1).value:
-        raise ValueError("invalid recurrence description")
-    return int(n)
+    return _valid_size(L.lib().kan_recur_workspace_size(desc, int(pass_)), "recurrence")
 
 
-def _recur_common(x, g, h0, lengths):
-    _check_device(x, "x", _DTYPES)
-    _check_device(g, "g", _DTYPES, x.device)
-    _check_tensor(h0, "h0", (torch.float32,), x.device)
-    _check_tensor(lengths, "lengths", (torch.int32,), x.device)
+def _recur_inputs(x, g, h0, lengths):
+    dev = _dev(x, "x")
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D], got %s" % (tuple(x.shape),))
-    _check_shape(h0, "h0", (x.shape[0], x.shape[2]))
-    _check_shape(lengths, "lengths", (x.shape[0],))
+    _rows(x, "x", _DTYPES, dev)
+    _rows(g, "g", _DTYPES, dev)
+    if h0 is not None:
+        _whole(h0, "h0", _F32, dev, (x.shape[0], x.shape[2]))
+    if lengths is not None:
+        _whole(lengths, "lengths", _I32, dev, x.shape[:1])
+    return dev
 
 
 def kan_recur_forward(x, g, h0=None, lengths=None, ws=None, out=None):
     """``(y [B, T, D], hT [B, D])`` float32 of the gated recurrence
     ``h_t = sigmoid(g_t) h_{t-1} + sigmoid(-g_t) x_t``.  ``h0 [B, D]`` float32
     (default 0), ``lengths [B]`` int32 (default T); ``y`` is 0 past a length."""
-    _recur_common(x, g, h0, lengths)
+    dev = _recur_inputs(x, g, h0, lengths)
     desc = recur_desc(x, g)
-    y = out if out is not None else torch.empty(x.shape, dtype=torch.float32, device=x.device)
-    _check_out(y, "y", x.shape, x.device)
-    hT = torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)
-    buf, n = _sized_ws(ws, L.lib().kan_recur_workspace_size(ctypes.byref(desc), L.KAN_PASS_FORWARD), x.device)
-    L.check(L.lib().kan_recur_forward(ctypes.byref(desc), _ptr(x), _ptr(g), _ptr(h0), _ptr(lengths), _ptr(y),
-                                      _ptr(hT), _ptr(buf), n, _stream(x)), "kan_recur_forward")
+    B, T, D = x.shape
+    if out is None:
+        y = x.new_empty((B, T, D), dtype=torch.float32)
+    else:
+        y = out
+        _whole(y, "y", _F32, dev, x.shape)
+    hT = y.new_empty((B, D))
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_recur_workspace_size(desc, L.KAN_PASS_FORWARD), x)
+    L.check(lib.kan_recur_forward(desc, x.data_ptr(), g.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
+                                  hT.data_ptr(), _addr(buf), n, _raw_stream(dev)), "kan_recur_forward")
     return y, hT
 
 
@@ -454,25 +493,26 @@ def kan_recur_backward(x, g, y, dy, h0=None, lengths=None, dhT=None, need_dh0=No
     ``dhT [B, D]``).  ``dx`` and ``dg`` are written into the given tensors (any
     row and sequence strides, for instance the halves of one array) or into
     new ones of ``grad_dtype``; ``dh0 [B, D]`` float32 (default: with ``h0``)."""
-    _recur_common(x, g, h0, lengths)
-    for t, name in ((y, "y"), (dy, "dy")):
-        _check_out(t, name, x.shape, x.device)
-    _check_tensor(dhT, "dhT", (torch.float32,), x.device)
-    _check_shape(dhT, "dhT", (x.shape[0], x.shape[2]))
+    dev = _recur_inputs(x, g, h0, lengths)
+    shape = x.shape
+    _whole(y, "y", _F32, dev, shape)
+    _whole(dy, "dy", _F32, dev, shape)
+    if dhT is not None:
+        _whole(dhT, "dhT", _F32, dev, (shape[0], shape[2]))
     if (dx is None) != (dg is None):
         raise ValueError("give both dx and dg or neither")
     if dx is None:
-        dx, dg = torch.empty((2, *x.shape), dtype=grad_dtype, device=x.device)
-    for t, name in ((dx, "dx"), (dg, "dg")):
-        _check_device(t, name, (dx.dtype,) if dx.dtype in _DTYPES else _DTYPES, x.device)
-        _check_shape(t, name, x.shape)
+        dx, dg = x.new_empty((2, *shape), dtype=grad_dtype).unbind(0)
+    _rows(dx, "dx", _DTYPES, dev, shape)
+    _rows(dg, "dg", (dx.dtype,), dev, shape)
     desc = recur_desc(x, g, dx, dg)
     need_dh0 = h0 is not None if need_dh0 is None else need_dh0
-    dh0 = torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device) if need_dh0 else None
-    buf, n = _sized_ws(ws, L.lib().kan_recur_workspace_size(ctypes.byref(desc), L.KAN_PASS_BACKWARD), x.device)
-    L.check(L.lib().kan_recur_backward(ctypes.byref(desc), _ptr(x), _ptr(g), _ptr(h0), _ptr(lengths), _ptr(y),
-                                       _ptr(dy), _ptr(dhT), _ptr(dx), _ptr(dg), _ptr(dh0), _ptr(buf), n,
-                                       _stream(x)), "kan_recur_backward")
+    dh0 = y.new_empty((shape[0], shape[2])) if need_dh0 else None
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_recur_workspace_size(desc, L.KAN_PASS_BACKWARD), x)
+    L.check(lib.kan_recur_backward(desc, x.data_ptr(), g.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
+                                   dy.data_ptr(), _addr(dhT), dx.data_ptr(), dg.data_ptr(), _addr(dh0), _addr(buf),
+                                   n, _raw_stream(dev)), "kan_recur_backward")
     return dx, dg, dh0
 
 
@@ -480,61 +520,66 @@ def kan_recur_step(x, g, state, slots=None, out=None):
     """One row of each sequence: ``state [S, D]`` float32 is read and replaced in
     rows ``slots [B]`` (int32, all different; default ``0 .. B-1``) and the new
     rows are returned as ``y [B, D]``; a slot outside the pool is skipped."""
-    _check_device(x, "x", _DTYPES)
-    _check_device(g, "g", _DTYPES, x.device)
-    _check_tensor(state, "state", (torch.float32,), x.device)
-    _check_tensor(slots, "slots", (torch.int32,), x.device)
+    dev = _dev(x, "x")
     if x.dim() != 2 or state.dim() != 2 or state.shape[1] != x.shape[1]:
         raise ValueError("x must be [B, D] and state [S, D]")
-    _check_shape(slots, "slots", x.shape[:1])
-    desc = recur_desc(x.unsqueeze(1), g.unsqueeze(1))
-    y = out if out is not None else torch.empty(x.shape, dtype=torch.float32, device=x.device)
-    _check_out(y, "y", x.shape, x.device)
-    L.check(L.lib().kan_recur_step(ctypes.byref(desc), state.shape[0], _ptr(x), _ptr(g), _ptr(state), _ptr(slots),
-                                   _ptr(y), _stream(x)), "kan_recur_step")
+    shape = x.shape
+    _rows(x, "x", _DTYPES, dev)
+    _rows(g, "g", (x.dtype,), dev, shape)
+    _whole(state, "state", _F32, dev)
+    if slots is not None:
+        _whole(slots, "slots", _I32, dev, shape[:1])
+    B, D = shape
+    xs, gs = x.stride(0), g.stride(0)
+    desc = L.kan_recur_desc_t(B, 1, D, xs, xs, gs, gs, 0, 0, 0, 0, _DTYPES[x.dtype], L.KAN_F32)
+    if out is None:
+        y = state.new_empty((B, D))
+    else:
+        y = out
+        _whole(y, "y", _F32, dev, shape)
+    L.check(L.lib().kan_recur_step(desc, state.shape[0], x.data_ptr(), g.data_ptr(), state.data_ptr(), _addr(slots),
+                                   y.data_ptr(), _raw_stream(dev)), "kan_recur_step")
     return y
+
+
+def _row_stride(t):
+    """The stride between the rows of ``[N, V]`` (a single row's stride is free)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def distill_desc(z, ids, t, tau, dz=None, grad_dtype=torch.float32):
     """``kan_distill_desc_t`` of ``z [N, V]`` (any row stride) and ``ids``, ``t [N, K]``."""
     if z.dim() != 2 or ids.dim() != 2 or ids.shape[0] != z.shape[0]:
         raise ValueError("z must be [N, V] and ids [N, K]")
-    _check_shape(t, "t", ids.shape)
-    d = L.kan_distill_desc_t()
-    d.N, d.V = z.shape
-    d.K = ids.shape[1]
-    d.z_row = z.stride(0) if z.shape[0] > 1 else max(z.stride(0), z.shape[1])
-    d.dz_row = d.V
-    if dz is not None:
-        d.dz_row = dz.stride(0) if dz.shape[0] > 1 else max(dz.stride(0), dz.shape[1])
-    d.dtype, d.teacher_dtype, d.id_dtype = _DTYPES[z.dtype], _DTYPES[t.dtype], _INDEX[ids.dtype]
-    d.grad_dtype = _DTYPES[dz.dtype if dz is not None else grad_dtype]
-    d.tau = float(tau)
-    return d
+    if t.shape != ids.shape:
+        raise ValueError("t must be %s, got %s" % (tuple(ids.shape), tuple(t.shape)))
+    N, V = z.shape
+    return L.kan_distill_desc_t(N, V, ids.shape[1], _row_stride(z), V if dz is None else _row_stride(dz),
+                                _DTYPES[z.dtype], _DTYPES[t.dtype], _INDEX[ids.dtype],
+                                _DTYPES[grad_dtype if dz is None else dz.dtype], tau)
 
 
 def kan_distill_workspace_size(desc):
-    n = L.lib().kan_distill_workspace_size(ctypes.byref(desc))
-    if n == ctypes.c_size_t(-1).value:
-        raise ValueError("invalid distillation description")
-    return int(n)
+    return _valid_size(L.lib().kan_distill_workspace_size(desc), "distillation")
 
 
-def _distill_common(z, ids, t, weight):
-    _check_device(z, "z", _DTYPES)
-    _check_tensor(ids, "ids", _INDEX, z.device)
-    _check_tensor(t, "t", _DTYPES, z.device)
-    _check_tensor(weight, "weight", (torch.float32,), z.device)
+def _distill_inputs(z, ids, t, weight):
+    dev = _dev(z, "z")
     if z.dim() != 2:
         raise ValueError("z must be [N, V], got %s" % (tuple(z.shape),))
-    _check_shape(weight, "weight", z.shape[:1])
+    _rows(z, "z", _DTYPES, dev)
+    _whole(ids, "ids", _INDEX, dev)
+    _whole(t, "t", _DTYPES, dev)
+    if weight is not None:
+        _whole(weight, "weight", _F32, dev, z.shape[:1])
+    return dev
 
 
-def _distill_out(z, out, grad_dtype):
-    dz = out if out is not None else torch.empty(z.shape, dtype=grad_dtype, device=z.device)
-    _check_device(dz, "dz", _DTYPES, z.device)
-    _check_shape(dz, "dz", z.shape)
-    return dz
+def _distill_grad(z, out, grad_dtype, dev):
+    if out is None:
+        return z.new_empty(z.shape, dtype=grad_dtype)
+    _rows(out, "dz", _DTYPES, dev, z.shape)
+    return out
 
 
 def kan_distill_forward(z, ids, t, temperature=1.0, weight=None, ws=None):
@@ -542,37 +587,41 @@ def kan_distill_forward(z, ids, t, temperature=1.0, weight=None, ws=None):
     divergence of the student's distribution ``softmax(z_b / tau)`` from the
     teacher's, the softmax of its top logits ``t [N, K] / tau`` over the tokens
     ``ids [N, K]`` (int32 or int64; ids outside ``[0, V)`` are absent)."""
-    _distill_common(z, ids, t, weight)
+    dev = _distill_inputs(z, ids, t, weight)
     desc = distill_desc(z, ids, t, temperature)
-    loss = torch.empty((z.shape[0],), dtype=torch.float32, device=z.device)
+    loss = z.new_empty(z.shape[:1], dtype=torch.float32)
     lse = torch.empty_like(loss)
-    buf, n = _sized_ws(ws, L.lib().kan_distill_workspace_size(ctypes.byref(desc)), z.device)
-    L.check(L.lib().kan_distill_forward(ctypes.byref(desc), _ptr(z), _ptr(ids), _ptr(t), _ptr(weight), _ptr(loss),
-                                        _ptr(lse), _ptr(buf), n, _stream(z)), "kan_distill_forward")
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_distill_workspace_size(desc), z)
+    L.check(lib.kan_distill_forward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
+                                    loss.data_ptr(), lse.data_ptr(), _addr(buf), n, _raw_stream(dev)),
+            "kan_distill_forward")
     return loss, lse
 
 
 def kan_distill_backward(z, ids, t, lse, dloss, temperature=1.0, weight=None, grad_dtype=torch.float32, out=None):
     """``dz [N, V]`` in ``grad_dtype`` of the loss, from the forward's ``lse`` and
     the gradients ``dloss [N]`` of the rows' losses."""
-    _distill_common(z, ids, t, weight)
-    for v, name in ((lse, "lse"), (dloss, "dloss")):
-        _check_out(v, name, z.shape[:1], z.device)
-    dz = _distill_out(z, out, grad_dtype)
+    dev = _distill_inputs(z, ids, t, weight)
+    _whole(lse, "lse", _F32, dev, z.shape[:1])
+    _whole(dloss, "dloss", _F32, dev, z.shape[:1])
+    dz = _distill_grad(z, out, grad_dtype, dev)
     desc = distill_desc(z, ids, t, temperature, dz)
-    L.check(L.lib().kan_distill_backward(ctypes.byref(desc), _ptr(z), _ptr(ids), _ptr(t), _ptr(weight), _ptr(lse),
-                                         _ptr(dloss), _ptr(dz), _stream(z)), "kan_distill_backward")
+    L.check(L.lib().kan_distill_backward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
+                                         lse.data_ptr(), dloss.data_ptr(), dz.data_ptr(), _raw_stream(dev)),
+            "kan_distill_backward")
     return dz
 
 
 def kan_distill_step(z, ids, t, temperature=1.0, weight=None, grad_dtype=torch.float32, out=None, ws=None):
     """``(loss [N], dz [N, V])`` in one call: the rows' losses and the gradient of
     their sum (put the mean's 1/N into ``weight``)."""
-    _distill_common(z, ids, t, weight)
-    dz = _distill_out(z, out, grad_dtype)
+    dev = _distill_inputs(z, ids, t, weight)
+    dz = _distill_grad(z, out, grad_dtype, dev)
     desc = distill_desc(z, ids, t, temperature, dz)
-    loss = torch.empty((z.shape[0],), dtype=torch.float32, device=z.device)
-    buf, n = _sized_ws(ws, L.lib().kan_distill_workspace_size(ctypes.byref(desc)), z.device)
-    L.check(L.lib().kan_distill_step(ctypes.byref(desc), _ptr(z), _ptr(ids), _ptr(t), _ptr(weight), _ptr(loss),
-                                     _ptr(dz), _ptr(buf), n, _stream(z)), "kan_distill_step")
+    loss = z.new_empty(z.shape[:1], dtype=torch.float32)
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_distill_workspace_size(desc), z)
+    L.check(lib.kan_distill_step(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight), loss.data_ptr(),
+                                 dz.data_ptr(), _addr(buf), n, _raw_stream(dev)), "kan_distill_step")
     return loss, dz
