@@ -480,7 +480,7 @@ int kan_recur_step(const kan_recur_desc_t* desc, int64_t S, const void* x, const
  * stride dz_row; ids [N, K] (id_dtype), t [N, K] in `teacher_dtype`; w (NULL:
  * all 1), loss, lse, dloss [N] float32. */
 typedef struct {
-    int64_t N;              /* rows, 0 .. 2^22 */
+    int64_t N;              /* rows, 0 .. 2^21 */
     int64_t V;              /* student logits of a row, >= 1 */
     int64_t K;              /* teacher logits of a row, 1 .. 1024 */
     int64_t z_row;          /* stride of z, >= V */

@@ -51,7 +51,7 @@ hipError_t launch_recur_step(const kan_recur_desc_t& d, int64_t S, const void* x
                              const int32_t* slots, float* y, hipStream_t s);
 
 // ---- distillation ----
-constexpr int64_t kDistillMaxN = int64_t(1) << 22;
+constexpr int64_t kDistillMaxN = int64_t(1) << 21;
 constexpr int kDistillMaxK = 1024;   // teacher logits of a row at most
 struct DistillPlan {
     size_t ws;
