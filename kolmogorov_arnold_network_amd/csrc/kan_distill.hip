@@ -15,7 +15,8 @@
 // longer row is read again from the caches), so z is read once though its
 // gradient needs m and s first; the forward streams the row with a running
 // maximum and sum.  The teacher's part is done while the row's loads are in
-// flight.
+// flight.  The step's stores are plain: streamed ones gained 2% at 8192 x 65536
+// and lost 4% at 4096 x 50021.
 #include "kan_token.h"
 #include "kan_vec.h"
 
@@ -24,6 +25,10 @@ namespace kan {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+// 2^x by the hardware's instruction; results below 2^-126 become 0, which no sum
+// here would see.
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
+
 constexpr int DU = 4;             // vectors that a streaming thread loads together
 
 // Reductions over a block, one barrier each; every call has its own slots.
@@ -75,93 +80,85 @@ struct Teacher {
     __device__ __forceinline__ void finish(const kan_distill_desc_t& d, float* slots, int* ids, float* ps) {
         const float m = block_max<NT>(t, slots);       // a NaN shows in the sum
         t = (t - (m == -INFINITY ? 0.0f : m)) / d.tau;
-        p = id >= 0 ? exp2f(t * kLog2e) : 0.0f;
+        p = id >= 0 ? exp2_raw(t * kLog2e) : 0.0f;
         float none = 0.0f;
         sum = p;
         block_sum2<NT>(sum, none, slots + NT / 64);
         p = id >= 0 ? p / sum : 0.0f;
-        if ((int)threadIdx.x < d.K) ids[threadIdx.x] = id, ps[threadIdx.x] = p;
+        // entries past K, up to a multiple of 4, are absent
+        if ((int)threadIdx.x < ((d.K + 3) & ~3)) ids[threadIdx.x] = id, ps[threadIdx.x] = p;
         __syncthreads();
     }
     // p becomes the sum over the entries of the same id, at the first of them;
-    // the others drop out (id -1)
+    // the others drop out (id -1).  Only the waves that hold entries look, at
+    // four others a read: with all of 16 waves looking at one each, 128 entries
+    // took longer than the row.
     __device__ __forceinline__ void join_equal(const kan_distill_desc_t& d, const int* ids, const float* ps) {
+        if ((int)threadIdx.x >= d.K) return;
         bool first = true;
         float s = 0.0f;
-        for (int j = 0; j < d.K; ++j) {
-            const bool same = ids[j] == id;
-            first = first && !(same && j < (int)threadIdx.x);
-            s += same ? ps[j] : 0.0f;
+        for (int j = 0; j < d.K; j += 4) {
+            const int4 i = *reinterpret_cast<const int4*>(ids + j);
+            const float4 q = *reinterpret_cast<const float4*>(ps + j);
+            const int of[4] = {i.x, i.y, i.z, i.w};
+            const float pr[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool same = of[k] == id;
+                first = first && !(same && j + k < (int)threadIdx.x);
+                s += same ? pr[k] : 0.0f;
+            }
         }
         if (!first) id = -1;
         p = s;
     }
 };
 
-// VE elements of a row from element v: -inf past its end.
-template <typename TS>
-struct Piece {
-    static constexpr int VE = 16 / (int)sizeof(TS);
-    Raw<TS, VE> r;
-    __device__ __forceinline__ void load(const TS* z, int64_t v, int64_t V) {
-        if (v + VE <= V) {
-            r = load_raw<TS, VE>(z + v);
-            return;
-        }
-        constexpr uint32_t fill = sizeof(TS) == 4 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.w[i] = fill;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            if (v + i >= V) continue;
-            if constexpr (sizeof(TS) == 4) r.w[i] = __float_as_uint(z[v + i]);
-            else r.w[i / 2] = i & 1 ? (r.w[i / 2] & 0xffffu) | ((uint32_t)z[v + i] << 16)
-                                    : (r.w[i / 2] & 0xffff0000u) | z[v + i];
-        }
-    }
-    __device__ __forceinline__ float operator[](int i) const { return raw_value(r, i); }
-    __device__ __forceinline__ float max() const {
-        float m = (*this)[0];
-#pragma unroll
-        for (int i = 1; i < VE; ++i) m = fmaxf(m, (*this)[i]);
-        return m;
-    }
-};
-
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put1(uint16_t* p, float v) { *p = f2bf(v); }
 
-template <typename TG, int VE>
-__device__ __forceinline__ void put(TG* dz, int64_t v, int64_t V, const float (&o)[VE]) {
-    if (v + VE <= V) {
-        if constexpr (sizeof(TG) == 4 && VE == 8) {
-            const float lo[4] = {o[0], o[1], o[2], o[3]}, hi[4] = {o[4], o[5], o[6], o[7]};
-            store_vec<4>(dz + v, lo);
-            store_vec<4>(dz + v + 4, hi);
-        } else {
-            store_vec<VE>(dz + v, o);
-        }
-        return;
-    }
+template <typename TS, int N>
+__device__ __forceinline__ float max_of(const Raw<TS, N>& r) {
+    float m = raw_value(r, 0);
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-        if (v + i < V) put1(dz + v + i, o[i]);
+    for (int i = 1; i < N; ++i) m = fmaxf(m, raw_value(r, i));
+    return m;
 }
 
-// All of a row's (or, from v0 to v1, a part's) gradient zero.
-template <typename TG, int NT, int VE>
+constexpr int VE = 4;             // elements of a vector, of either type
+
+// A row is a head of single elements up to the first cache line of what is
+// written (of z, where nothing is), vectors, and a tail of fewer elements than
+// a vector.  Rows of an odd length start anywhere; lines cut between lanes and
+// waves cost 20% of a step with 50021 bf16 logits (241 us against 204 at 50024).
+// Thread i takes element i of the head and of the tail.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int64_t V) {
+    const int n = (int)((128 - (reinterpret_cast<uintptr_t>(p) & 127)) & 127) / (int)sizeof(T);
+    return (int)min((int64_t)n, V);
+}
+
+// All of a row's gradient, or of its elements [v0, v1), zero.
+template <typename TG, int NT>
 __device__ __forceinline__ void zeros(TG* dz, int64_t v0, int64_t v1) {
     const float zero[VE] = {};
-    for (int64_t v = v0 + threadIdx.x * VE; v < v1; v += NT * VE) put<TG, VE>(dz, v, v1, zero);
+    dz += v0;
+    const int64_t n = v1 - v0;
+    const int head = head_of(dz, n);
+    const int64_t tail = n - (n - head) % VE;
+    for (int64_t v = head + (int64_t)threadIdx.x * VE; v + VE <= n; v += NT * VE) store_vec<VE>(dz + v, zero);
+    for (int v = threadIdx.x; v < head; v += NT) put1(dz + v, 0.0f);
+    if (tail + threadIdx.x < n) put1(dz + tail + threadIdx.x, 0.0f);
 }
 
 // Forward (STEP false) and step.  NV vectors of a thread are held in registers.
-template <typename TS, typename TG, int NT, int NV, bool STEP>
+template <typename TS, typename TG, int NT, int NV, bool STEP, bool STREAM>
 __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, DistillArgs a) {
-    constexpr int VE = Piece<TS>::VE, W = NT / 64;
+    constexpr int W = NT / 64;
+    typedef Raw<TS, VE> Vec;
     __shared__ float slots[6 * W];
-    __shared__ int ids[kDistillMaxK];
-    __shared__ float ps[kDistillMaxK];
+    __shared__ __attribute__((aligned(16))) int ids[NT];
+    __shared__ __attribute__((aligned(16))) float ps[NT];
     const int64_t row = blockIdx.x, V = d.V;
     const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
     TG* dz = STEP ? static_cast<TG*>(a.dz) + row * d.dz_row : nullptr;
@@ -171,58 +168,82 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
             a.loss[row] = 0.0f;
             if (!STEP) a.lse[row] = 0.0f;
         }
-        if (STEP) zeros<TG, NT, VE>(dz, 0, V);
+        if (STEP) zeros<TG, NT>(dz, 0, V);
         return;
     }
     const float inv = 1.0f / d.tau, c = kLog2e * inv;
     Teacher<NT> te;
     te.load(d, a, row);
-    const int mine = threadIdx.x * VE;
-    Piece<TS> keep[NV ? NV : 1];
+    const int head = STEP ? head_of(dz, V) : head_of(z, V);
+    const int64_t body = head + (int64_t)threadIdx.x * VE, tail = V - (V - head) % VE + threadIdx.x;
+    constexpr int64_t STRIDE = NT * VE;                // elements of a vector of every thread
+    float hz = -INFINITY, tz = -INFINITY;
+    if ((int)threadIdx.x < head) hz = load_f(z, threadIdx.x);
+    if (tail < V) tz = load_f(z, tail);
+    Vec keep[NV ? NV : 1];
     float m = -INFINITY, s = 0.0f;
     if (NV) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if ((int64_t)v * NT * VE < V) keep[v].load(z, (int64_t)v * NT * VE + mine, V);    // uniform
+        for (int v = 0; v < NV; ++v) {
+            if (head + v * STRIDE >= V) break;         // uniform
+            if (body + v * STRIDE + VE <= V) {
+                keep[v] = load_raw<TS, VE>(z + body + v * STRIDE);
+            } else {
+#pragma unroll
+                for (int i = 0; i < Vec::W; ++i) keep[v].w[i] = sizeof(TS) == 4 ? 0xff800000u : 0xff80ff80u;
+            }
+        }
     }
     te.finish(d, slots, ids, ps);
     if (STEP) te.join_equal(d, ids, ps);
     // a running maximum and sum over what registers do not hold
-    for (int64_t v = (int64_t)NV * NT * VE + mine; v < V; v += (int64_t)NT * VE * DU) {
-        Piece<TS> q[DU];
+    for (int64_t v = body + NV * STRIDE; v + VE <= V; v += STRIDE * DU) {
+        Vec q[DU];
 #pragma unroll
-        for (int u = 0; u < DU; ++u) q[u].load(z, v + (int64_t)u * NT * VE, V);
+        for (int u = 0; u < DU; ++u) {
+            const int64_t at = v + u * STRIDE;         // past the end: the first again, not counted
+            const TS* from = z + (at + VE <= V ? at : v);
+            q[u] = STREAM ? load_once<TS, VE>(from) : load_raw<TS, VE>(from);
+        }
         float g = m;
 #pragma unroll
-        for (int u = 0; u < DU; ++u) g = fmaxf(g, q[u].max());
+        for (int u = 0; u < DU; ++u) g = fmaxf(g, max_of<TS, VE>(q[u]));
         const float g0 = g == -INFINITY ? 0.0f : g;
-        s *= exp2f((m - g0) * c);
+        s *= exp2_raw((m - g0) * c);
         m = g;
 #pragma unroll
-        for (int u = 0; u < DU; ++u)
+        for (int u = 0; u < DU; ++u) {
+            if (v + u * STRIDE + VE > V) continue;
 #pragma unroll
-            for (int i = 0; i < VE; ++i) s += exp2f((q[u][i] - g0) * c);
+            for (int i = 0; i < VE; ++i) s += exp2_raw((raw_value(q[u], i) - g0) * c);
+        }
     }
     const float m_stream = m;
+    m = fmaxf(m, fmaxf(hz, tz));
     if (NV) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if ((int64_t)v * NT * VE < V) m = fmaxf(m, keep[v].max());
+        for (int v = 0; v < NV; ++v) {
+            if (head + v * STRIDE >= V) break;
+            m = fmaxf(m, max_of<TS, VE>(keep[v]));
+        }
     }
     m = block_max<NT>(m, slots + 3 * W);
     const float m0 = m == -INFINITY ? 0.0f : m;
-    s *= exp2f((m_stream - m0) * c);
+    s *= exp2_raw((m_stream - m0) * c);
+    hz = exp2_raw((hz - m0) * c);
+    tz = exp2_raw((tz - m0) * c);
+    s += hz + tz;
     if (NV) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if ((int64_t)v * NT * VE < V) {
+        for (int v = 0; v < NV; ++v) {
+            if (head + v * STRIDE >= V) break;
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const float e = exp2f((keep[v][i] - m0) * c);
-                    s += e;
-                    if constexpr (STEP && sizeof(TS) == 4) keep[v].r.w[i] = __float_as_uint(e);
-                }
+            for (int i = 0; i < VE; ++i) {
+                const float e = exp2_raw((raw_value(keep[v], i) - m0) * c);
+                s += e;
+                if constexpr (STEP && sizeof(TS) == 4) keep[v].w[i] = __float_as_uint(e);
             }
+        }
     }
     // sum_k p_k (log p_k + log(teacher's sum) - (z_k - m) / tau); the logs of the sums come after it
     float l = 0.0f, zk = -INFINITY;
@@ -239,87 +260,106 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
     }
     if (!STEP) return;
     if (empty) {
-        zeros<TG, NT, VE>(dz, 0, V);
+        zeros<TG, NT>(dz, 0, V);
         return;
     }
     const float f = w * d.tau, fs = f / s;
+    if ((int)threadIdx.x < head) put1(dz + threadIdx.x, fs * hz);
+    if (tail < V) put1(dz + tail, fs * tz);
     if (NV) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if ((int64_t)v * NT * VE < V) {
-                float o[VE];
-#pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    o[i] = fs * (sizeof(TS) == 4 ? keep[v][i] : exp2f((keep[v][i] - m0) * c));
-                const int64_t at = (int64_t)v * NT * VE + mine;
-                if (at < V) put<TG, VE>(dz, at, V, o);
-            }
-    }
-    for (int64_t v = (int64_t)NV * NT * VE + mine; v < V; v += (int64_t)NT * VE * DU) {
-        Piece<TS> q[DU];
-#pragma unroll
-        for (int u = 0; u < DU; ++u) q[u].load(z, v + (int64_t)u * NT * VE, V);
-#pragma unroll
-        for (int u = 0; u < DU; ++u) {
+        for (int v = 0; v < NV; ++v) {
+            if (head + v * STRIDE >= V) break;
+            if (body + v * STRIDE + VE > V) break;
             float o[VE];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) o[i] = fs * exp2f((q[u][i] - m0) * c);
-            const int64_t at = v + (int64_t)u * NT * VE;
-            if (at < V) put<TG, VE>(dz, at, V, o);
+            for (int i = 0; i < VE; ++i) {
+                const float e = raw_value(keep[v], i);
+                o[i] = fs * (sizeof(TS) == 4 ? e : exp2_raw((e - m0) * c));
+            }
+            store_vec<VE>(dz + body + v * STRIDE, o);
+        }
+    }
+    for (int64_t v = body + NV * STRIDE; v + VE <= V; v += STRIDE * DU) {
+        Vec q[DU];
+#pragma unroll
+        for (int u = 0; u < DU; ++u) {
+            const int64_t at = v + u * STRIDE;
+            q[u] = load_raw<TS, VE>(z + (at + VE <= V ? at : v));
+        }
+#pragma unroll
+        for (int u = 0; u < DU; ++u) {
+            if (v + u * STRIDE + VE > V) continue;
+            float o[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) o[i] = fs * exp2_raw((raw_value(q[u], i) - m0) * c);
+            store_vec<VE>(dz + v + u * STRIDE, o);
         }
     }
     // the teacher's entries again, now with their p taken off
     __syncthreads();
-    if (te.id >= 0) put1(dz + te.id, fs * exp2f((zk - m0) * c) - f * te.p);
+    if (te.id >= 0) put1(dz + te.id, fs * exp2_raw((zk - m0) * c) - f * te.p);
 }
 
-// Backward: block (row, part) writes elements [v0, v1) of a row.
-template <typename TS, typename TG, int NT>
+// Backward: block (row, p) writes part p of a row's vectors, the first block the
+// head too and the last the tail.
+template <typename TS, typename TG, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, DistillArgs a, int parts,
                                                          int64_t part) {
-    constexpr int VE = Piece<TS>::VE, W = NT / 64;
+    constexpr int W = NT / 64;
     __shared__ float slots[3 * W];
-    __shared__ int ids[kDistillMaxK];
-    __shared__ float ps[kDistillMaxK];
-    const int64_t row = blockIdx.x / (unsigned)parts, v0 = (blockIdx.x % (unsigned)parts) * part;
-    const int64_t v1 = min(v0 + part, d.V);
+    __shared__ __attribute__((aligned(16))) int ids[NT];
+    __shared__ __attribute__((aligned(16))) float ps[NT];
+    const int64_t row = blockIdx.x / (unsigned)parts, V = d.V;
+    const int p = (int)(blockIdx.x % (unsigned)parts);
     const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
     TG* dz = static_cast<TG*>(a.dz) + row * d.dz_row;
+    const int head = head_of(dz, V);
+    const int64_t v0 = p ? min(head + p * part, V) : 0, v1 = p == parts - 1 ? V : min(head + (p + 1) * part, V);
     const float w = a.w ? a.w[row] : 1.0f, lse = w != 0.0f ? a.lse_in[row] : 0.0f;
     if (w == 0.0f || lse == -INFINITY) {
-        zeros<TG, NT, VE>(dz, v0, v1);
+        zeros<TG, NT>(dz, v0, v1);
         return;
     }
     Teacher<NT> te;
     te.load(d, a, row);
     te.finish(d, slots, ids, ps);
     if (te.sum == 0.0f) {
-        zeros<TG, NT, VE>(dz, v0, v1);
+        zeros<TG, NT>(dz, v0, v1);
         return;
     }
     te.join_equal(d, ids, ps);
     const float f = w * d.tau * a.dloss[row], inv = 1.0f / d.tau;
-    auto q = [&](float x) { return exp2f(__builtin_fmaf(x, inv, -lse) * kLog2e); };
-    for (int64_t v = v0 + threadIdx.x * VE; v < v1; v += (int64_t)NT * VE * DU) {
-        Piece<TS> x[DU];
-#pragma unroll
-        for (int u = 0; u < DU; ++u) x[u].load(z, v + (int64_t)u * NT * VE, v1);
+    auto q = [&](float x) { return exp2_raw(__builtin_fmaf(x, inv, -lse) * kLog2e); };
+    constexpr int64_t STRIDE = NT * VE;
+    for (int64_t v = head + p * part + (int64_t)threadIdx.x * VE; v + VE <= v1; v += STRIDE * DU) {
+        Raw<TS, VE> x[DU];
 #pragma unroll
         for (int u = 0; u < DU; ++u) {
+            const int64_t at = v + u * STRIDE;
+            x[u] = load_raw<TS, VE>(z + (at + VE <= v1 ? at : v));
+        }
+#pragma unroll
+        for (int u = 0; u < DU; ++u) {
+            if (v + u * STRIDE + VE > v1) continue;
             float o[VE];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) o[i] = f * q(x[u][i]);
-            const int64_t at = v + (int64_t)u * NT * VE;
-            if (at < v1) put<TG, VE>(dz, at, v1, o);
+            for (int i = 0; i < VE; ++i) o[i] = f * q(raw_value(x[u], i));
+            store_vec<VE, STREAM>(dz + v + u * STRIDE, o);
         }
+    }
+    if (p == 0 && (int)threadIdx.x < head) put1(dz + threadIdx.x, f * q(load_f(z, threadIdx.x)));
+    if (p == parts - 1) {
+        const int64_t tail = V - (V - head) % VE + threadIdx.x;
+        if (tail < V) put1(dz + tail, f * q(load_f(z, tail)));
     }
     __syncthreads();
     if (te.id >= v0 && te.id < v1) put1(dz + te.id, f * (q(load_f(z, te.id)) - te.p));
 }
 
-template <typename TS, typename TG, int NT, int NV, bool STEP>
+template <typename TS, typename TG, int NT, int NV, bool STEP, bool STREAM>
 hipError_t row_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((distill_row_kernel<TS, TG, NT, NV, STEP>), dim3((unsigned)d.N), dim3(NT), 0, s, d, a);
+    hipLaunchKernelGGL((distill_row_kernel<TS, TG, NT, NV, STEP, STREAM>), dim3((unsigned)d.N), dim3(NT), 0, s, d, a);
     return hipGetLastError();
 }
 
@@ -327,29 +367,41 @@ hipError_t row_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t 
 // the teacher's entries.
 template <typename TS, typename TG>
 hipError_t step_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    const int64_t per = 16 * Piece<TS>::VE;            // elements that a thread holds
+    constexpr int NV = 256 / (VE * (int)sizeof(TS));   // 64 registers
+    constexpr int64_t per = NV * VE;
     const int64_t threads = std::max((d.V + per - 1) / per, d.K);
-    if (threads <= 64) return row_t<TS, TG, 64, 16, true>(d, a, s);
-    if (threads <= 256) return row_t<TS, TG, 256, 16, true>(d, a, s);
-    if (threads <= 512) return row_t<TS, TG, 512, 16, true>(d, a, s);
-    return row_t<TS, TG, 1024, 16, true>(d, a, s);
+    if (threads <= 64) return row_t<TS, TG, 64, NV, true, false>(d, a, s);
+    if (threads <= 256) return row_t<TS, TG, 256, NV, true, false>(d, a, s);
+    if (threads <= 512) return row_t<TS, TG, 512, NV, true, false>(d, a, s);
+    return row_t<TS, TG, 1024, NV, true, false>(d, a, s);
 }
 
+template <typename TS, bool STREAM>
+hipError_t fwd_s(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
+    if (d.K > 256) return row_t<TS, TS, 1024, 0, false, STREAM>(d, a, s);
+    if (d.K > 64 || d.V > 64 * 64) return row_t<TS, TS, 256, 0, false, STREAM>(d, a, s);
+    return row_t<TS, TS, 64, 0, false, STREAM>(d, a, s);
+}
+// Past kStreamBytes the logits cannot stay in the caches for the backward pass
+// and are read as streamed data (4096 x 50021 float32: 133 -> 119 us).
 template <typename TS>
 hipError_t fwd_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    if (d.K > 256) return row_t<TS, float, 1024, 0, false>(d, a, s);
-    if (d.K > 64 || d.V > 64 * 16 * Piece<TS>::VE) return row_t<TS, float, 256, 0, false>(d, a, s);
-    return row_t<TS, float, 64, 0, false>(d, a, s);
+    return d.N * d.V * (int64_t)sizeof(TS) >= kStreamBytes ? fwd_s<TS, true>(d, a, s) : fwd_s<TS, false>(d, a, s);
 }
 
 template <typename TS, typename TG, int NT>
 hipError_t bwd_n(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    constexpr int VE = Piece<TS>::VE;
+    constexpr int64_t round = NT * VE;
     // a few thousand blocks, of at least one round of loads each
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((2048 + d.N - 1) / d.N, d.V / (NT * VE * DU)));
-    const int64_t part = round_up((d.V + parts - 1) / parts, NT * VE), n = (d.V + part - 1) / part;
-    hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT>), dim3((unsigned)(d.N * n)), dim3(NT), 0, s, d, a, (int)n,
-                       part);
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((2048 + d.N - 1) / d.N, d.V / (round * DU)));
+    const int64_t part = round_up((d.V + parts - 1) / parts, round), n = (d.V + part - 1) / part;
+    // streamed stores past kStreamBytes: 4096 x 50021 bf16 197 -> 170 us, float32 372 -> 331
+    if (d.N * d.V * (int64_t)sizeof(TG) >= kStreamBytes)
+        hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, true>), dim3((unsigned)(d.N * n)), dim3(NT), 0, s, d, a,
+                           (int)n, part);
+    else
+        hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, false>), dim3((unsigned)(d.N * n)), dim3(NT), 0, s, d, a,
+                           (int)n, part);
     return hipGetLastError();
 }
 template <typename TS, typename TG>

@@ -6,6 +6,10 @@
 
 namespace kan {
 
+// An array of half the 256 MB cache or more is gone from it before the next
+// operator reads it.
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
 inline int dtype_bytes(int dtype) { return dtype == KAN_F32 ? 4 : 2; }
 
 // ---- embedding ----

@@ -52,21 +52,43 @@ __device__ __forceinline__ Raw<TS, VEC> load_raw(const TS* p) {
     return r;
 }
 
+// The same, for data that is read once: the caches keep it no longer than needed.
+template <typename TS, int VEC>
+__device__ __forceinline__ Raw<TS, VEC> load_once(const TS* p) {
+    static_assert(sizeof(TS) * VEC > 2, "a vector");
+    Raw<TS, VEC> r;
+    typedef typename words<(int)sizeof(TS) * VEC>::type W;
+    typedef W Wu __attribute__((aligned(sizeof(TS))));
+    const W v = __builtin_nontemporal_load(reinterpret_cast<const Wu*>(p));
+    __builtin_memcpy(r.w, &v, sizeof(v));
+    return r;
+}
+
 template <typename TS, int VEC>
 __device__ __forceinline__ float raw_value(const Raw<TS, VEC>& r, int i) {
     if constexpr (sizeof(TS) == 4) return __uint_as_float(r.w[i]);
     else return __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
 }
 
-template <int VEC>
+// STREAM: the caches keep what is written no longer than needed.
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
     typedef typename words<4 * VEC>::type W;
     typedef W Wu __attribute__((aligned(4)));
     W w;
     __builtin_memcpy(&w, v, sizeof(w));
-    *reinterpret_cast<Wu*>(p) = w;
+    if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<Wu*>(p));
+    else *reinterpret_cast<Wu*>(p) = w;
 }
-template <int VEC>
+// Two floats rounded to nearest even bf16, in one instruction (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 f = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+}
+
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC]) {
     if constexpr (VEC == 1) {
         *p = f2bf(v[0]);
@@ -75,10 +97,11 @@ __device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[VEC]) {
         typedef W Wu __attribute__((aligned(2)));
         uint32_t u[VEC / 2];
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) u[i] = (uint32_t)f2bf(v[2 * i]) | ((uint32_t)f2bf(v[2 * i + 1]) << 16);
+        for (int i = 0; i < VEC / 2; ++i) u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
         W w;
         __builtin_memcpy(&w, u, sizeof(w));
-        *reinterpret_cast<Wu*>(p) = w;
+        if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<Wu*>(p));
+        else *reinterpret_cast<Wu*>(p) = w;
     }
 }
 
