@@ -237,7 +237,7 @@ __device__ __forceinline__ void load_state(const float* h0, int64_t b, int64_t D
 constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 
 // Forward.  COMPOSE: only the segment's run, for the second launch.
-template <typename TS, int VEC, int RC, bool COMPOSE>
+template <typename TS, int VEC, int RC, bool COMPOSE, bool STREAM>
 __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
                                                             float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
             const float zero[VEC] = {};
 #pragma unroll
             for (int r = 0; r < RF; ++r)
-                if (t + r < at.r1) store_vec<VEC>(y + (t + r) * D, zero);
+                if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, zero);
             continue;
         }
         const bool whole = t0 + tile <= inside;        // uniform
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] = s[i];
                 upto[r].apply(o);
-                store_vec<VEC>(y + (t + r) * D, o);
+                store_vec<VEC, STREAM>(y + (t + r) * D, o);
             }
         } else {
 #pragma unroll
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
                 upto[r].apply(o);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? o[i] : 0.0f;
-                if (t + r < at.r1) store_vec<VEC>(y + (t + r) * D, o);
+                if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, o);
             }
         }
     }
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
 }
 
 // Backward: the same, from the last row of a segment to its first.
-template <typename TS, typename TG, int VEC, int RC, bool COMPOSE>
+template <typename TS, typename TG, int VEC, int RC, bool COMPOSE, bool STREAM>
 __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
                                                             float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
 #pragma unroll
             for (int r = 0; r < RB; ++r)
                 if (t + r < at.r1) {
-                    store_vec<VEC>(dx + (t + r) * d.dx_row, zero);
-                    store_vec<VEC>(dg + (t + r) * d.dg_row, zero);
+                    store_vec<VEC, STREAM>(dx + (t + r) * d.dx_row, zero);
+                    store_vec<VEC, STREAM>(dg + (t + r) * d.dg_row, zero);
                 }
             continue;
         }
@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
                 if (t + r >= at.len)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) ox[i] = og[i] = 0.0f;
-                store_vec<VEC>(dx + (t + r) * d.dx_row, ox);
-                store_vec<VEC>(dg + (t + r) * d.dg_row, og);
+                store_vec<VEC, STREAM>(dx + (t + r) * d.dx_row, ox);
+                store_vec<VEC, STREAM>(dg + (t + r) * d.dg_row, og);
             }
         }
     }
@@ -485,35 +485,38 @@ __global__ void __launch_bounds__(64) recur_step_kernel(kan_recur_desc_t d, int6
     y[b * d.D + c] = n;
 }
 
-template <typename TS, int VEC, int RC>
+template <typename TS, int VEC, int RC, bool STREAM = false>
 hipError_t fwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, true>), grid, block, 0, s, d, p, a, runs);
+        hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, true, false>), grid, block, 0, s, d, p, a, runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, false>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, false, STREAM>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
 }
 
-template <typename TS, typename TG, int VEC, int RC>
+template <typename TS, typename TG, int VEC, int RC, bool STREAM = false>
 hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_bwd_kernel<TS, float, VEC, RC, true>), grid, block, 0, s, d, p, a, runs);
+        hipLaunchKernelGGL((recur_bwd_kernel<TS, float, VEC, RC, true, false>), grid, block, 0, s, d, p, a, runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, false>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, false, STREAM>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
 }
 
+// Large outputs are stored as streamed data (8 x 4096 x 2048: bf16 forward 106.5 ->
+// 104 us, float32 backward 327 -> 315.5).
 template <typename TS>
 hipError_t fwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     if (p.vec == 1) return fwd_t<TS, 1, 4>(d, p, a, ws, s);
+    if (p.lanes == 16 && d.B * d.T * d.D * 4 >= kStreamBytes) return fwd_t<TS, 4, 16, true>(d, p, a, ws, s);
     return p.lanes == 16 ? fwd_t<TS, 4, 16>(d, p, a, ws, s)
                          : p.lanes == 8 ? fwd_t<TS, 4, 8>(d, p, a, ws, s) : fwd_t<TS, 4, 4>(d, p, a, ws, s);
 }
@@ -521,6 +524,8 @@ hipError_t fwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs&
 template <typename TS, typename TG>
 hipError_t bwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     if (p.vec == 1) return bwd_t<TS, TG, 1, 4>(d, p, a, ws, s);
+    if (p.lanes == 16 && d.B * d.T * d.D * (int64_t)sizeof(TG) >= kStreamBytes)
+        return bwd_t<TS, TG, 4, 16, true>(d, p, a, ws, s);
     return p.lanes == 16 ? bwd_t<TS, TG, 4, 16>(d, p, a, ws, s)
                          : p.lanes == 8 ? bwd_t<TS, TG, 4, 8>(d, p, a, ws, s) : bwd_t<TS, TG, 4, 4>(d, p, a, ws, s);
 }
