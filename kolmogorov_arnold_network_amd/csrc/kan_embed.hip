@@ -3,11 +3,14 @@
 //
 // Both move rows and do one operation an element, so HBM traffic bounds them
 // (and launches, with few tokens).  The gradient adds no float atomics: a
-// first launch lists the rows of every token in ascending order, a second
-// adds the listed rows in chunks of 32 - every dy row is read once, every
-// dE row written once, whatever the tokens' frequencies - and writes zeros
-// for tokens that do not occur, and a third joins tokens that span chunks.
-// The order of every sum depends on the ids alone.
+// first launch lists the rows of every token in ascending order and, in other
+// blocks, fills dE with zeros; a second adds the listed rows in chunks - every
+// dy row is read once, whatever the tokens' frequencies - and writes the rows
+// of the tokens that occur; a third joins tokens that span chunks.  The order
+// of every sum depends on the ids alone.  Listing is latency (38 us for 32768
+// ids when it ran alone), the fill is bandwidth, so they share a launch; rows
+// that occur are written twice, but a fill alone runs at 6.8 TB/s where reads
+// and writes mixed run at 5.
 #include "kan_token.h"
 #include "kan_vec.h"
 
@@ -18,13 +21,14 @@ namespace {
 constexpr int EB_T = 256;         // threads of a lookup / summing block
 constexpr int ES_W = 16;          // waves of a listing block
 constexpr int ES_T = 64 * ES_W;
-constexpr int ES_U = 4;           // ids a listing lane loads together
+constexpr int ES_U = 8;           // ids a listing lane loads together
+constexpr int EZ_V = 16;          // vectors of zeros that a filling thread writes
 
 // ---- lookup -------------------------------------------------------------------
 // Block: 256 / tpr rows at a time, UNR times, tpr lanes of VEC columns to a
 // row.  With at least VEC columns the last vector of a row ends at its end
 // (it repeats columns of its neighbour, with the same values).
-template <typename TE, typename TY, typename TI, int VEC, int UNR>
+template <typename TE, typename TY, typename TI, int VEC, int UNR, bool STREAM>
 __global__ void __launch_bounds__(EB_T) embed_fwd_kernel(const TI* __restrict__ ids, const TE* __restrict__ E,
                                                          TY* __restrict__ y, int64_t N, int64_t V, int64_t D,
                                                          int tpr, float scale) {
@@ -52,29 +56,60 @@ __global__ void __launch_bounds__(EB_T) embed_fwd_kernel(const TI* __restrict__ 
         float v[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = id[q] >= 0 ? raw_value(r[q], i) * scale : 0.0f;
-        if (n < N) store_vec<VEC>(y + n * D + c, v);
+        if (n < N) store_vec<VEC, STREAM>(y + n * D + c, v);
     }
 }
 
 // ---- listing ------------------------------------------------------------------
-// Block r lists the tokens [r width, (r + 1) width): it reads every id once to
-// count its tokens' rows (per wave of the block, each of which takes a
-// contiguous share of the ids) and the rows of smaller tokens, which is where
-// its own part of the list begins, and a second time to place the rows:
-// place = the token's first + rows of it in earlier waves + earlier in this
-// wave.  All sums are of integers and every row's place is fixed by the ids.
-// Each block reads all ids, from L2 (N <= 32768: 256 KB): no other block's
-// counts are waited for, so one launch is enough.
-template <typename TI>
-__global__ void __launch_bounds__(ES_T) embed_list_kernel(const TI* __restrict__ ids, int N, int64_t V, int width,
-                                                          int bits, int* __restrict__ order,
-                                                          int* __restrict__ token, int* __restrict__ start) {
+// Block r lists the tokens of range r: it reads every id once to count its
+// tokens' rows (per wave of the block, each of which takes a contiguous share
+// of the ids) and the rows of smaller tokens, which is where its own part of
+// the list begins, and a second time to place the rows: place = the token's
+// first + rows of it in earlier waves + earlier in this wave.  All sums are of
+// integers and every row's place is fixed by the ids.  Each block reads all
+// ids, from L2 (N <= 32768: 256 KB): no other block's counts are waited for,
+// so one launch is enough.
+//
+// The ranges are 16 to a doubling of the token, at most kEmbedWidth wide:
+// vocabularies are commonly in the order of frequency, about 1 / rank, and a
+// block's time goes with the rows that it places.  With equal ranges the first
+// one had half of all rows and took 38 us for 32768 of them.
+__device__ __forceinline__ void range_of(int r, int64_t& lo, int& width) {
+    constexpr int N = kEmbedPerDoubling;
+    const int doubling = r < N ? 0 : r / N - 1;
+    if (doubling < kEmbedDoublings) {
+        width = 1 << doubling;
+        lo = r < N ? r : (int64_t)(N + r % N) << doubling;
+    } else {
+        width = kEmbedWidth;
+        lo = ((int64_t)N << kEmbedDoublings) + (int64_t)(r - N * (kEmbedDoublings + 1)) * kEmbedWidth;
+    }
+}
+
+//
+// Blocks past the ranges fill dE, `total` floats, with zeros.
+template <typename TI, bool STREAM>
+__global__ void __launch_bounds__(ES_T) embed_list_kernel(const TI* __restrict__ ids, int N, int64_t V,
+                                                          int2* __restrict__ list, int* __restrict__ start, int ranges, float* __restrict__ dE, int64_t total) {
     __shared__ int hist[ES_W][kEmbedWidth];
     __shared__ int sums[ES_W];
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int64_t lo = (int64_t)blockIdx.x * width;
+    if ((int)blockIdx.x >= ranges) {                   // uniform
+        const float zero[4] = {};
+        int64_t at = ((int64_t)(blockIdx.x - ranges) * (ES_T * EZ_V) + t) * 4;
+#pragma unroll
+        for (int i = 0; i < EZ_V; ++i, at += ES_T * 4) {
+            if (at + 4 <= total) store_vec<4, STREAM>(dE + at, zero);
+            else
+                for (int64_t k = at; k < total; ++k) dE[k] = 0.0f;
+        }
+        return;
+    }
+    int64_t lo;
+    int width;
+    range_of(blockIdx.x, lo, width);
     const int n_tok = (int)min((int64_t)width, V - lo);
-    for (int i = t; i < ES_W * kEmbedWidth; i += ES_T) (&hist[0][0])[i] = 0;
+    for (int i = lane; i < n_tok; i += 64) hist[w][i] = 0;
     __syncthreads();
     const int share = ((N + ES_W - 1) / ES_W + 63) / 64 * 64;
     const int a = min((int64_t)w * share, (int64_t)N), b = min((int64_t)a + share, (int64_t)N);
@@ -88,9 +123,8 @@ __global__ void __launch_bounds__(ES_T) embed_list_kernel(const TI* __restrict__
         }
 #pragma unroll
         for (int q = 0; q < ES_U; ++q) {
-            const int64_t k = id[q] - lo;
-            below += id[q] >= 0 && k < 0;
-            if (k >= 0 && k < n_tok) atomicAdd(&hist[w][k], 1);
+            below += id[q] >= 0 && id[q] < lo;
+            if (id[q] >= lo && id[q] < lo + n_tok) atomicAdd(&hist[w][(int)(id[q] - lo)], 1);
         }
     }
 #pragma unroll
@@ -134,20 +168,24 @@ __global__ void __launch_bounds__(ES_T) embed_list_kernel(const TI* __restrict__
         }
 #pragma unroll
         for (int q = 0; q < ES_U; ++q) {
-            const int64_t k = id[q] - lo;
-            const bool in = id[q] >= 0 && k >= 0 && k < n_tok;
+            const bool in = id[q] >= lo && id[q] < lo + n_tok;
             unsigned long long same = __ballot(in);
             if (same == 0) continue;                   // uniform across the wave
-            for (int bit = 0; bit < bits; ++bit) {
-                const unsigned long long set = __ballot(in && ((k >> bit) & 1));
-                same &= ((k >> bit) & 1) ? set : ~set;
+            const int k = in ? (int)(id[q] - lo) : 0;
+            // lanes of the same token: those that agree in every bit of k
+            uint32_t s0 = (uint32_t)same, s1 = (uint32_t)(same >> 32);
+            for (int bit = 0; (1 << bit) < width; ++bit) {
+                const int m = (int)((uint32_t)k << (31 - bit)) >> 31;      // the bit, in every place
+                const unsigned long long set = __ballot(m != 0);
+                s0 &= ~((uint32_t)set ^ (uint32_t)m);
+                s1 &= ~((uint32_t)(set >> 32) ^ (uint32_t)m);
             }
+            same = ((unsigned long long)s1 << 32) | s0;
             if (in) {
                 const int rank = __popcll(same & ((1ull << lane) - 1));
                 int* h = &hist[w][k];
                 const int at = __hip_atomic_load(h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) + rank;
-                order[at] = n0 + q * 64 + lane;
-                token[at] = (int)id[q];
+                list[at] = make_int2((int)id[q], n0 + q * 64 + lane);
                 // the last lane of the token leaves the next place; a wave's
                 // LDS operations are done in order
                 if ((same >> lane) == 1)
@@ -164,13 +202,12 @@ __global__ void __launch_bounds__(ES_T) embed_list_kernel(const TI* __restrict__
 // part[chunk][0], one that ends in a later chunk to part[chunk][1].
 constexpr int EQ = 8;             // rows loaded together
 template <typename TY, int VEC>
-__device__ __forceinline__ void sum_chunk(int64_t chunk, int64_t c, const TY* dy, int64_t D, const int* order,
-                                          const int* token, int total, float scale, float* dE, float* part) {
-    const int p0 = (int)(chunk * kEmbedChunk);
-    if (p0 >= total) return;
-    const int p1 = min(p0 + kEmbedChunk, total);
-    int cur = token[p0];
-    bool head = p0 > 0 && token[p0 - 1] == cur;
+__device__ __forceinline__ void sum_chunk(int64_t chunk, int size, int64_t c, const TY* dy, int64_t D,
+                                          const int2* list, int total, float scale, float* dE, float* part) {
+    if (chunk * size >= total) return;
+    const int p0 = (int)chunk * size, p1 = min(p0 + size, total);
+    int cur = list[p0].x;                              // {token, row}
+    bool head = p0 > 0 && list[p0 - 1].x == cur;
     float acc[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
@@ -187,8 +224,9 @@ __device__ __forceinline__ void sum_chunk(int64_t chunk, int64_t c, const TY* dy
 #pragma unroll
         for (int q = 0; q < EQ; ++q) {
             const int at = min(p + q, p1 - 1);
-            tok[q] = token[at];
-            r[q] = load_raw<TY, VEC>(dy + (int64_t)order[at] * D + c);
+            const int2 e = list[at];
+            tok[q] = e.x;
+            r[q] = load_raw<TY, VEC>(dy + (int64_t)e.y * D + c);
         }
 #pragma unroll
         for (int q = 0; q < EQ; ++q) {
@@ -202,35 +240,23 @@ __device__ __forceinline__ void sum_chunk(int64_t chunk, int64_t c, const TY* dy
             for (int i = 0; i < VEC; ++i) acc[i] += raw_value(r[q], i);
         }
     }
-    const bool tail = p1 < total && token[p1] == cur;
+    const bool tail = p1 < total && list[p1].x == cur;
     if (head) put(part0, 1.0f);
     else if (tail) put(part0 + D, 1.0f);
     else put(dE + (int64_t)cur * D, scale);
 }
 
-// Blocks [0, sum_blocks): 256 / tpr chunks each, tpr lanes of VEC columns
-// (blockIdx.y: further columns).  The rest: zero rows, `zrows` tokens each.
+// 256 / tpr chunks to a block, tpr lanes of VEC columns (blockIdx.y: further columns).
 template <typename TY, int VEC>
-__global__ void __launch_bounds__(EB_T) embed_sum_kernel(const TY* __restrict__ dy, int64_t V, int64_t D, int tpr,
-                                                         int64_t sum_blocks, int zrows,
-                                                         const int* __restrict__ order,
-                                                         const int* __restrict__ token,
+__global__ void __launch_bounds__(EB_T) embed_sum_kernel(const TY* __restrict__ dy, int64_t V, int64_t D, int tpr, int size,
+                                                         const int2* __restrict__ list,
                                                          const int* __restrict__ start, float scale,
                                                          float* __restrict__ dE, float* __restrict__ part) {
     const int lane = threadIdx.x % tpr, sub = threadIdx.x / tpr, rows = EB_T / tpr;
     const int64_t c0 = ((int64_t)blockIdx.y * tpr + lane) * VEC;
     if (c0 >= D) return;
     const int64_t c = c0 + VEC > D ? D - VEC : c0;
-    if ((int64_t)blockIdx.x < sum_blocks) {
-        sum_chunk<TY, VEC>((int64_t)blockIdx.x * rows + sub, c, dy, D, order, token, start[V], scale, dE, part);
-        return;
-    }
-    const int64_t v0 = ((int64_t)blockIdx.x - sum_blocks) * zrows;
-    for (int64_t v = v0 + sub; v < min(v0 + zrows, V); v += rows) {
-        if (start[v] != start[v + 1]) continue;
-        const float zero[VEC] = {};
-        store_vec<VEC>(dE + v * D + c, zero);
-    }
+    sum_chunk<TY, VEC>((int64_t)blockIdx.x * rows + sub, size, c, dy, D, list, start[V], scale, dE, part);
 }
 
 // A token that spans chunks: the sum of its chunks' sums.  Block b looks at
@@ -239,17 +265,17 @@ __global__ void __launch_bounds__(EB_T) embed_sum_kernel(const TY* __restrict__ 
 // then the quarters are added in order.
 constexpr int EJ_W = 4;
 template <int VEC>
-__global__ void __launch_bounds__(64 * EJ_W) embed_join_kernel(int64_t V, int64_t D, const int* __restrict__ token,
+__global__ void __launch_bounds__(64 * EJ_W) embed_join_kernel(int64_t V, int64_t D, int size, const int2* __restrict__ list,
                                                                const int* __restrict__ start, float scale,
                                                                float* __restrict__ dE,
                                                                const float* __restrict__ part) {
     __shared__ float quarter[EJ_W][64][VEC];
     const int64_t b = blockIdx.x;
-    const int p = (int)((b + 1) * kEmbedChunk);
+    const int p = (int)((b + 1) * size);
     if (p >= start[V]) return;                         // uniform across the block, as the next one
-    const int tok = token[p];
-    const int first = start[tok], last = (start[tok + 1] - 1) / kEmbedChunk;
-    if (first >= p || first < p - kEmbedChunk) return;
+    const int tok = list[p].x;
+    const int first = start[tok], last = (start[tok + 1] - 1) / size;
+    if (first >= p || first < p - size) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     // pieces: part[b][1], part[b + 1][0], ..., part[last][0]
     const int n = last - (int)b + 1, each = (n + EJ_W - 1) / EJ_W;
@@ -299,14 +325,14 @@ hipError_t fwd_t(const kan_embed_desc_t& d, const void* ids, const void* E, void
     // four rows to a lane once one row each would fill the GPU's waves several times over
     const bool many = d.N / rows * gy >= 4096;
     const unsigned gx = (unsigned)((d.N + rows * (many ? 4 : 1) - 1) / (rows * (many ? 4 : 1)));
-    if (many)
-        hipLaunchKernelGGL((embed_fwd_kernel<TE, TY, TI, VEC, 4>), dim3(gx, gy), dim3(EB_T), 0, s,
-                           static_cast<const TI*>(ids), static_cast<const TE*>(E), static_cast<TY*>(y), d.N, d.V, d.D,
-                           tpr, d.scale);
-    else
-        hipLaunchKernelGGL((embed_fwd_kernel<TE, TY, TI, VEC, 1>), dim3(gx, gy), dim3(EB_T), 0, s,
-                           static_cast<const TI*>(ids), static_cast<const TE*>(E), static_cast<TY*>(y), d.N, d.V, d.D,
-                           tpr, d.scale);
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(gx, gy), dim3(EB_T), 0, s, static_cast<const TI*>(ids),
+                           static_cast<const TE*>(E), static_cast<TY*>(y), d.N, d.V, d.D, tpr, d.scale);
+    };
+    // large outputs as streamed data: 32768 x 2048 bf16 36.6 -> 31.3 us
+    if (!many) run(embed_fwd_kernel<TE, TY, TI, VEC, 1, false>);
+    else if (d.N * d.D * (int64_t)sizeof(TY) < kStreamBytes) run(embed_fwd_kernel<TE, TY, TI, VEC, 4, false>);
+    else run(embed_fwd_kernel<TE, TY, TI, VEC, 4, true>);
     return hipGetLastError();
 }
 
@@ -323,33 +349,36 @@ template <typename TY, int VEC>
 hipError_t bwd_t(const kan_embed_desc_t& d, const EmbedPlan& p, const void* dy, float* dE, char* ws, hipStream_t s) {
     const int tpr = lanes_per_row(d.D, VEC), rows = EB_T / tpr;
     const unsigned gy = (unsigned)((d.D + (int64_t)tpr * VEC - 1) / ((int64_t)tpr * VEC));
-    const int64_t sum_blocks = (p.chunks + rows - 1) / rows;
-    const int zrows = rows * 8;
-    const int64_t blocks = sum_blocks + (d.V + zrows - 1) / zrows;
-    int* order = reinterpret_cast<int*>(ws + p.off_order);
-    int* token = reinterpret_cast<int*>(ws + p.off_token);
+    const int64_t blocks = (p.chunks + rows - 1) / rows;
+    int2* list = reinterpret_cast<int2*>(ws + p.off_list);
     int* start = reinterpret_cast<int*>(ws + p.off_start);
     float* part = reinterpret_cast<float*>(ws + p.off_part);
     hipLaunchKernelGGL((embed_sum_kernel<TY, VEC>), dim3((unsigned)blocks, gy), dim3(EB_T), 0, s,
-                       static_cast<const TY*>(dy), d.V, d.D, tpr, sum_blocks, zrows, order, token, start, d.scale, dE,
-                       part);
+                       static_cast<const TY*>(dy), d.V, d.D, tpr, p.chunk, list, start, d.scale, dE, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.chunks == 1) return e;
     const unsigned jy = (unsigned)((d.D + 64 * VEC - 1) / (64 * VEC));
-    hipLaunchKernelGGL((embed_join_kernel<VEC>), dim3((unsigned)(p.chunks - 1), jy), dim3(64 * EJ_W), 0, s, d.V, d.D,
-                       token, start, d.scale, dE, part);
+    hipLaunchKernelGGL((embed_join_kernel<VEC>), dim3((unsigned)(p.chunks - 1), jy), dim3(64 * EJ_W), 0, s, d.V, d.D, p.chunk,
+                       list, start, d.scale, dE, part);
     return hipGetLastError();
 }
 
-template <typename TI>
-hipError_t list_t(const kan_embed_desc_t& d, const EmbedPlan& p, const void* ids, char* ws, hipStream_t s) {
-    int bits = 0;
-    while ((1 << bits) < p.width) ++bits;
-    hipLaunchKernelGGL((embed_list_kernel<TI>), dim3((unsigned)p.ranges), dim3(ES_T), 0, s,
-                       static_cast<const TI*>(ids), (int)d.N, d.V, p.width, bits,
-                       reinterpret_cast<int*>(ws + p.off_order), reinterpret_cast<int*>(ws + p.off_token),
-                       reinterpret_cast<int*>(ws + p.off_start));
+template <typename TI, bool STREAM>
+hipError_t list_t(const kan_embed_desc_t& d, const EmbedPlan& p, const void* ids, float* dE, char* ws,
+                  hipStream_t s) {
+    const int64_t total = d.V * d.D, fill = (total + ES_T * EZ_V * 4 - 1) / (ES_T * EZ_V * 4);
+    hipLaunchKernelGGL((embed_list_kernel<TI, STREAM>), dim3((unsigned)(p.ranges + fill)), dim3(ES_T), 0, s,
+                       static_cast<const TI*>(ids), (int)d.N, d.V,
+                       reinterpret_cast<int2*>(ws + p.off_list), reinterpret_cast<int*>(ws + p.off_start), (int)p.ranges, dE, total);
     return hipGetLastError();
+}
+// A large dE is filled past the caches (537 MB: 207 -> 180 us for the whole
+// pass), a small one in them (98 MB: 32 -> 27 us).
+template <typename TI>
+hipError_t list_s(const kan_embed_desc_t& d, const EmbedPlan& p, const void* ids, float* dE, char* ws,
+                  hipStream_t s) {
+    return d.V * d.D * 4 >= kStreamBytes ? list_t<TI, true>(d, p, ids, dE, ws, s)
+                                         : list_t<TI, false>(d, p, ids, dE, ws, s);
 }
 
 }  // namespace
@@ -364,7 +393,8 @@ hipError_t launch_embed_fwd(const kan_embed_desc_t& d, const void* ids, const vo
 
 hipError_t launch_embed_bwd(const kan_embed_desc_t& d, const EmbedPlan& p, const void* ids, const void* dy, float* dE,
                             char* ws, hipStream_t s) {
-    const hipError_t e = d.id_dtype == KAN_I32 ? list_t<int32_t>(d, p, ids, ws, s) : list_t<int64_t>(d, p, ids, ws, s);
+    const hipError_t e = d.id_dtype == KAN_I32 ? list_s<int32_t>(d, p, ids, dE, ws, s)
+                                                   : list_s<int64_t>(d, p, ids, dE, ws, s);
     if (e != hipSuccess) return e;
     if (d.row_dtype == KAN_F32)
         return d.D < 4 ? bwd_t<float, 1>(d, p, dy, dE, ws, s) : bwd_t<float, 4>(d, p, dy, dE, ws, s);

@@ -13,16 +13,17 @@ constexpr int64_t kStreamBytes = int64_t(128) << 20;
 inline int dtype_bytes(int dtype) { return dtype == KAN_F32 ? 4 : 2; }
 
 // ---- embedding ----
-// Gradient: the table is cut into ranges of `width` tokens, a block each, that
-// list their tokens' rows; the listed rows are summed in chunks of
-// kEmbedChunk.
+// Gradient: the table is cut into ranges of tokens, a block each, that list
+// their tokens' rows; the listed rows are summed in chunks.  The ranges are
+// kEmbedPerDoubling to a doubling of the token, kEmbedDoublings times, then
+// kEmbedWidth tokens each.
 constexpr int64_t kEmbedMaxN = int64_t(1) << 24, kEmbedMaxV = int64_t(1) << 26, kEmbedMaxD = int64_t(1) << 23;
-constexpr int kEmbedWidth = 512;   // tokens of a range at most
-constexpr int kEmbedChunk = 32;    // listed rows of a chunk
+constexpr int kEmbedPerDoubling = 16, kEmbedDoublings = 9;
+constexpr int kEmbedWidth = 1 << kEmbedDoublings;
 struct EmbedPlan {
-    int width;
+    int chunk;               // listed rows of a chunk
     int64_t ranges, chunks;
-    size_t off_order, off_token, off_start, off_part, ws;
+    size_t off_list, off_start, off_part, ws;
 };
 EmbedPlan embed_plan(int64_t N, int64_t V, int64_t D);
 
