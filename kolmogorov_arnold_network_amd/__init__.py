@@ -6,7 +6,9 @@ extended knot grid, and its training backward (dx, dC, dW_base).  All of it
 runs in hand-written HIP kernels behind the C ABI of ``include/kan.h``; so
 does the grouped (per-channel) spline activation ``y[b, i] = phi_{g(i)}(x[b, i])``
 and its backward, and the 2-D tensor-product spline layer over pairs of
-inputs.  This
+inputs.  Around the layers, for models over tokens: an embedding with its
+gradient by sorted tokens, a gated linear recurrence over the rows of a
+sequence, and distillation from a teacher's top logits.  This
 package binds that ABI (``functional``) and wraps it as torch modules
 (``modules``).
 """
@@ -22,7 +24,8 @@ from .functional import (kan_forward, kan_forward_static, kan_backward, kan_prep
                          recur_desc, kan_distill_forward, kan_distill_backward, kan_distill_step,
                          kan_distill_workspace_size, distill_desc)
 from .modules import (KANLayer, KANNetwork, KANFunction, KANGroupedActivation, KANSurfaceLayer,
-                      GroupedFunction, SurfaceFunction)
+                      GroupedFunction, SurfaceFunction, KANEmbedding, KANRecurrence, KANDistillLoss,
+                      EmbedFunction, RecurFunction, DistillFunction)
 
 __all__ = ["kan_forward", "kan_forward_static", "kan_backward", "kan_prepare", "kan_basis_eval", "kan_basis_eval_tp",
            "kan_cast_f32_to_bf16",
@@ -33,4 +36,5 @@ __all__ = ["kan_forward", "kan_forward_static", "kan_backward", "kan_prepare", "
            "kan_recur_forward", "kan_recur_backward", "kan_recur_step", "kan_recur_workspace_size", "recur_desc",
            "kan_distill_forward", "kan_distill_backward", "kan_distill_step", "kan_distill_workspace_size",
            "distill_desc",
-           "KANGroupedActivation", "KANSurfaceLayer", "GroupedFunction", "SurfaceFunction"]
+           "KANGroupedActivation", "KANSurfaceLayer", "GroupedFunction", "SurfaceFunction",
+           "KANEmbedding", "KANRecurrence", "KANDistillLoss", "EmbedFunction", "RecurFunction", "DistillFunction"]

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
         }
         float s[VEC];
         scan_tile<VEC, RC, false>(run, h, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
-        if (whole) {
+        if (whole && t0 + tile < at.len) {
 #pragma unroll
             for (int r = 0; r < RF; ++r) {
                 float o[VEC];
@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] = s[i];
                 upto[r].apply(o);
+                if (a.hT && t + r == at.len - 1) store_vec<VEC>(a.hT + at.b * D + at.c, o);     // the bits of y
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? o[i] : 0.0f;
                 if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, o);
@@ -341,8 +342,8 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
     }
     if (COMPOSE) {
         if (at.w == 0 && at.tl == 0) store_run<VEC>(p, at, D, runs, all);
-    } else if (a.hT && at.seg == p.segs - 1 && at.w == 0 && at.tl == 0) {
-        store_vec<VEC>(a.hT + at.b * D + at.c, h);
+    } else if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
+        store_vec<VEC>(a.hT + at.b * D + at.c, h);     // h0
     }
 }
 

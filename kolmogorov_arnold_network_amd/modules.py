@@ -1,4 +1,5 @@
-"""``KANLayer`` / ``KANNetwork`` / ``KANGroupedActivation`` / ``KANSurfaceLayer``:
+"""``KANLayer`` / ``KANNetwork`` / ``KANGroupedActivation`` / ``KANSurfaceLayer``, and
+for models over tokens ``KANEmbedding`` / ``KANRecurrence`` / ``KANDistillLoss``:
 torch modules over the HIP library.
 
 "KANLayer(in, out) replaces nn.Linear(in, out). Same interface, same
@@ -219,3 +220,139 @@ class KANSurfaceLayer(torch.nn.Module):
         return "in=%d (pairs=%d), out=%d, grid_size=%d, range=%s, dtype=%s" % (
             self.in_features, self.in_features // 2, self.out_features, self.grid_size, self.grid_range,
             self.coef.dtype)
+
+
+class EmbedFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, scale, row_dtype):
+        ctx.scale = scale
+        ctx.rows = table.shape[0]
+        ctx.table_dtype = table.dtype
+        ctx.save_for_backward(ids)
+        return F.kan_embed_forward(ids, table, scale, row_dtype)
+
+    @staticmethod
+    def backward(ctx, dy):
+        (ids,) = ctx.saved_tensors
+        dE = F.kan_embed_backward(ids, dy.contiguous(), ctx.rows, ctx.scale)
+        return None, dE if ctx.table_dtype == torch.float32 else dE.to(ctx.table_dtype), None, None
+
+
+class KANEmbedding(torch.nn.Module):
+    """Token rows: ``scale * table[ids]`` (default scale ``sqrt(features)``, for a
+    table of standard deviation ``1 / sqrt(features)``); ids outside the table
+    (padding) give zero rows.  The gradient is summed by token without atomics.
+    Parameter ``table [num_tokens, features]`` in ``dtype``; rows in
+    ``row_dtype`` (default ``dtype``)."""
+
+    def __init__(self, num_tokens, features, scale=None, dtype=torch.float32, row_dtype=None, device=None):
+        super().__init__()
+        self.num_tokens = int(num_tokens)
+        self.features = int(features)
+        self.scale = math.sqrt(features) if scale is None else float(scale)
+        self.row_dtype = row_dtype or dtype
+        self.table = torch.nn.Parameter(
+            torch.randn(num_tokens, features, dtype=dtype, device=device) / math.sqrt(features))
+
+    def forward(self, ids):
+        return EmbedFunction.apply(ids.contiguous(), self.table, self.scale, self.row_dtype)
+
+    def extra_repr(self):
+        return "tokens=%d, features=%d, scale=%g, dtype=%s, rows=%s" % (
+            self.num_tokens, self.features, self.scale, self.table.dtype, self.row_dtype)
+
+
+class RecurFunction(torch.autograd.Function):
+    """The recurrence over ``p [B, T, 2 D]``, whose halves are x and g."""
+
+    @staticmethod
+    def forward(ctx, p, h0, lengths):
+        D = p.shape[2] // 2
+        y, hT = F.kan_recur_forward(p[..., :D], p[..., D:], h0, lengths)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(p, h0, lengths, y)
+        return y, hT
+
+    @staticmethod
+    def backward(ctx, dy, dhT):
+        p, h0, lengths, y = ctx.saved_tensors
+        D = p.shape[2] // 2
+        dy = torch.zeros_like(y) if dy is None else dy.contiguous()
+        dp = torch.empty(p.shape, dtype=p.dtype, device=p.device)
+        dh0 = F.kan_recur_backward(p[..., :D], p[..., D:], y, dy, h0, lengths, None if dhT is None else dhT.contiguous(),
+                                   need_dh0=ctx.needs_input_grad[1], dx=dp[..., :D], dg=dp[..., D:])[2]
+        return dp, dh0, None
+
+
+class KANRecurrence(torch.nn.Module):
+    """Mixes the rows of a sequence: a ``KANLayer`` of twice the width makes a
+    value x and a gate g of every row, and each channel follows
+    ``h_t = sigmoid(g_t) h_{t-1} + sigmoid(-g_t) x_t``.
+
+    ``forward(x [B, T, in], h0 [B, out], lengths [B])`` returns the rows ``y [B, T,
+    out]`` and the last states ``[B, out]``, float32; ``step(x [B, in], state [S,
+    out], slots [B])`` takes one row of each of B sequences and replaces their
+    states in the pool."""
+
+    def __init__(self, in_features, out_features, **kw):
+        super().__init__()
+        self.in_features = int(in_features)
+        self.out_features = int(out_features)
+        self.layer = KANLayer(in_features, 2 * out_features, **kw)
+
+    def forward(self, x, h0=None, lengths=None):
+        return RecurFunction.apply(self.layer(x), h0, lengths)
+
+    @torch.no_grad()
+    def step(self, x, state, slots=None):
+        p = self.layer(x)
+        return F.kan_recur_step(p[:, :self.out_features], p[:, self.out_features:], state, slots)
+
+    def extra_repr(self):
+        return "in=%d, out=%d" % (self.in_features, self.out_features)
+
+
+class DistillFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, z, ids, t, temperature, weight):
+        loss, lse = F.kan_distill_forward(z, ids, t, temperature, weight)
+        ctx.temperature = temperature
+        ctx.save_for_backward(z, ids, t, lse, weight)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        z, ids, t, lse, weight = ctx.saved_tensors
+        dz = F.kan_distill_backward(z, ids, t, lse, dloss.contiguous().float(), ctx.temperature, weight,
+                                    grad_dtype=z.dtype)
+        return dz, None, None, None, None
+
+
+class KANDistillLoss(torch.nn.Module):
+    """``tau^2`` times the divergence of a student's logits ``z [..., V]`` from a
+    teacher's top logits ``t [..., K]`` of the tokens ``ids [..., K]``, both
+    softened by the temperature ``tau``.  ``weight [...]`` (float32) scales rows;
+    rows of weight 0 (padding) are not read.  ``reduction``: ``mean`` over all
+    rows, ``sum`` or ``none``."""
+
+    def __init__(self, temperature=1.0, reduction="mean"):
+        super().__init__()
+        if reduction not in ("mean", "sum", "none"):
+            raise ValueError("reduction must be mean, sum or none")
+        self.temperature = float(temperature)
+        self.reduction = reduction
+
+    def forward(self, z, ids, t, weight=None):
+        lead = z.shape[:-1]
+        if ids.shape[:-1] != lead or t.shape != ids.shape or (weight is not None and weight.shape != lead):
+            raise ValueError("z, ids, t and weight must share their leading dimensions")
+        K = ids.shape[-1]
+        loss = DistillFunction.apply(z.reshape(-1, z.shape[-1]), ids.reshape(-1, K).contiguous(),
+                                     t.reshape(-1, K).contiguous(), self.temperature,
+                                     None if weight is None else weight.reshape(-1).contiguous())
+        if self.reduction == "none":
+            return loss.reshape(lead)
+        return loss.mean() if self.reduction == "mean" else loss.sum()
+
+    def extra_repr(self):
+        return "temperature=%g, reduction=%s" % (self.temperature, self.reduction)
