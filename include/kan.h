@@ -394,7 +394,7 @@ typedef enum { KAN_I32 = 0, KAN_I64 = 1 } kan_index_t;
 typedef struct {
     int64_t N;          /* tokens, 0 .. 2^24 */
     int64_t V;          /* table rows, 1 .. 2^26 */
-    int64_t D;          /* row width, 1 .. 2^23 */
+    int64_t D;          /* row width, 1 .. 2^23; N D and V D at most 2^37 */
     int32_t dtype;      /* kan_dtype_t: storage of E */
     int32_t row_dtype;  /* kan_dtype_t: storage of y and dy */
     int32_t id_dtype;   /* kan_index_t: storage of ids */

@@ -18,6 +18,7 @@ inline int dtype_bytes(int dtype) { return dtype == KAN_F32 ? 4 : 2; }
 // kEmbedPerDoubling to a doubling of the token, kEmbedDoublings times, then
 // kEmbedWidth tokens each.
 constexpr int64_t kEmbedMaxN = int64_t(1) << 24, kEmbedMaxV = int64_t(1) << 26, kEmbedMaxD = int64_t(1) << 23;
+constexpr int64_t kEmbedMaxElements = int64_t(1) << 37;     // of the table and of the rows
 constexpr int kEmbedPerDoubling = 16, kEmbedDoublings = 9;
 constexpr int kEmbedWidth = 1 << kEmbedDoublings;
 struct EmbedPlan {

@@ -68,6 +68,7 @@ int embed_check(const kan_embed_desc_t* d) {
     if (!d) return KAN_ERR_NULL;
     if (d->N < 0 || d->N > kEmbedMaxN || d->V < 1 || d->V > kEmbedMaxV || d->D < 1 || d->D > kEmbedMaxD)
         return KAN_ERR_SHAPE;
+    if (d->N > kEmbedMaxElements / d->D || d->V > kEmbedMaxElements / d->D) return KAN_ERR_SHAPE;
     if (!dtype_ok(d->dtype) || !dtype_ok(d->row_dtype) || !index_ok(d->id_dtype)) return KAN_ERR_DTYPE;
     if (!isfinite(d->scale)) return KAN_ERR_UNSUPPORTED;
     return KAN_OK;
