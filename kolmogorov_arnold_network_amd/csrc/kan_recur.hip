@@ -23,8 +23,8 @@
 // wave's lanes and of the block's waves are scanned, and each lane goes over
 // its rows again from its start.  Where the sequences have too few channels
 // to fill the GPU they are cut into segments, a block each: a first launch
-// composes every segment's run, and the second starts each segment from the
-// runs before it (its inputs are then read twice).  Memory traffic bounds it;
+// composes every segment's run, from as many of its rows as still count at
+// its end, and the second starts each segment from the runs before it.  Memory traffic bounds it;
 // the arithmetic, two transcendentals and about 20 operations an element, is
 // about half of the time that the traffic takes.
 #include <type_traits>
@@ -236,10 +236,82 @@ __device__ __forceinline__ void load_state(const float* h0, int64_t b, int64_t D
 
 constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 
-// Forward.  COMPOSE: only the segment's run, for the second launch.
-template <typename TS, int VEC, int RC, bool COMPOSE, bool STREAM>
+// The runs of the segments, for the launch that starts each segment from them:
+// of h from x and g, or (BACK) of c from dy and g.  A segment's run is composed
+// from the end that counts most, the one where it hands its state on, and ends
+// where the share that is left of what comes before is at most 2^-25 in every
+// channel of the block: the rest of the segment would change the state by less
+// than its last place.  Common gates forget in a tile or two (128 or 256 rows);
+// gates that do not are read to the segment's start.
+template <typename TS, typename TV, int VEC, int RC, bool BACK>
+__global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d, RecurPlan p, const TS* g, const TV* v,
+                                                             int64_t v_row, int64_t v_seq, const int32_t* lengths,
+                                                             float* runs) {
+    __shared__ Run<VEC> tot[2][RW][RC];
+    constexpr int RL = 64 / RC;
+    const Place<VEC, RC> at(d, p, lengths);
+    g += at.b * d.g_seq + at.c;
+    v += at.b * v_seq + at.c;
+    const int tile = at.waves * RL * RF, first = (at.w * RL + at.tl) * RF;
+    const int64_t inside = min(at.len, at.r1), tiles = max((int64_t)0, (inside - at.r0 + tile - 1) / tile);
+    Raw<TS, VEC> gr[RF];
+    Raw<TV, VEC> vr[RF];
+    auto load = [&](int64_t t0) {                      // rows past the length repeat its last one
+#pragma unroll
+        for (int r = 0; r < RF; ++r) {
+            const int64_t q = min(t0 + first + r, at.len - 1);
+            gr[r] = row_at<TS, VEC>(g, q, d.g_row);
+            vr[r] = row_at<TV, VEC>(v, q, v_row);
+        }
+    };
+    auto start = [&](int64_t k) { return at.r0 + (BACK ? k : tiles - 1 - k) * tile; };
+    Run<VEC> all;
+    all.clear();
+    float left[VEC];                                   // 1 - all.U, with the digits of small values
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) left[i] = 1.0f;
+    if (tiles > 0) load(start(0));
+    for (int64_t k = 0; k < tiles; ++k) {
+        const int64_t t = start(k) + first;
+        Run<VEC> run, whole;
+        run.clear();
+#pragma unroll
+        for (int j = 0; j < RF; ++j) {
+            const int r = BACK ? RF - 1 - j : j;
+            const bool in = t + r < inside;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const Gate e = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
+                const float x = in ? raw_value(vr[r], i) : 0.0f;
+                run.b[i] = BACK ? e.back(x + run.b[i]) : e.step(run.b[i], x);
+                run.U[i] = e.lost(run.U[i]);
+            }
+        }
+        if (k + 1 < tiles) load(start(k + 1));
+        block_run<VEC, RC, BACK>(run, whole, at.cl, at.tl, at.w, at.waves, tot[k & 1]);
+        bool done = true;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            all.b[i] = __builtin_fmaf(left[i], whole.b[i], all.b[i]);
+            all.U[i] = __builtin_fmaf(all.U[i], 1.0f - whole.U[i], whole.U[i]);
+            left[i] *= 1.0f - whole.U[i];
+            done = done && left[i] <= 0x1p-25f;
+        }
+        // a wave has all of the block's channels and the same runs of them as
+        // every other wave: they leave together
+        if (__all(done)) break;
+    }
+    if (at.w != 0 || at.tl != 0) return;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        if (left[i] < 0.5f) all.U[i] = 1.0f - left[i];
+    store_run<VEC>(p, at, d.D, runs, all);
+}
+
+// Forward.
+template <typename TS, int VEC, int RC, bool STREAM>
 __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
-                                                            float* runs) {
+                                                            const float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
     const Place<VEC, RC> at(d, p, a.lengths);
@@ -248,13 +320,8 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
     float* y = a.out + at.b * d.T * D + at.c;
     float h[VEC];
-    Run<VEC> all;
-    if (COMPOSE) {
-        all.clear();
-    } else {
-        load_state<VEC>(a.h0, at.b, D, at.c, h);
-        if (p.segs > 1) from_segments<VEC, RC, false>(p, at, D, runs, h, tot[1]);
-    }
+    load_state<VEC>(a.h0, at.b, D, at.c, h);
+    if (p.segs > 1) from_segments<VEC, RC, false>(p, at, D, runs, h, tot[1]);
     const int tile = at.waves * RL * RF, first = (at.w * RL + at.tl) * RF;
     const int64_t inside = min(at.len, at.r1);
     Raw<TS, VEC> xr[RF], gr[RF];
@@ -280,7 +347,6 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
     for (int64_t t0 = at.r0; t0 < at.r1; t0 += tile, parity ^= 1) {
         const int64_t t = t0 + first;
         if (t0 >= at.len) {                            // uniform: rows past the length
-            if (COMPOSE) break;
             const float zero[VEC] = {};
 #pragma unroll
             for (int r = 0; r < RF; ++r)
@@ -308,13 +374,6 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
         if (whole) compose(std::false_type());
         else compose(std::true_type());
         if (t0 + tile < inside) load(t0 + tile);       // arrives during the scan and the stores
-        if (COMPOSE) {
-            Run<VEC> tile_run;
-            block_run<VEC, RC, false>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
-            tile_run.after(all);
-            all = tile_run;
-            continue;
-        }
         float s[VEC];
         scan_tile<VEC, RC, false>(run, h, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
         if (whole && t0 + tile < at.len) {
@@ -340,17 +399,15 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
             }
         }
     }
-    if (COMPOSE) {
-        if (at.w == 0 && at.tl == 0) store_run<VEC>(p, at, D, runs, all);
-    } else if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
+    if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
         store_vec<VEC>(a.hT + at.b * D + at.c, h);     // h0
     }
 }
 
 // Backward: the same, from the last row of a segment to its first.
-template <typename TS, typename TG, int VEC, int RC, bool COMPOSE, bool STREAM>
+template <typename TS, typename TG, int VEC, int RC, bool STREAM>
 __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
-                                                            float* runs) {
+                                                            const float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
     const Place<VEC, RC> at(d, p, a.lengths);
@@ -359,18 +416,13 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
     const float* y = a.y + at.b * d.T * D + at.c;
     const float* dy = a.dy + at.b * d.T * D + at.c;
-    const bool grads = !COMPOSE && a.dx;
+    const bool grads = a.dx;
     TG* dx = grads ? static_cast<TG*>(a.dx) + at.b * d.dx_seq + at.c : nullptr;
     TG* dg = grads ? static_cast<TG*>(a.dg) + at.b * d.dg_seq + at.c : nullptr;
     float c[VEC], h0[VEC];
-    Run<VEC> all;
-    if (COMPOSE) {
-        all.clear();
-    } else {
-        load_state<VEC>(a.dhT, at.b, D, at.c, c);
-        if (p.segs > 1) from_segments<VEC, RC, true>(p, at, D, runs, c, tot[1]);
-        load_state<VEC>(a.h0, at.b, D, at.c, h0);
-    }
+    load_state<VEC>(a.dhT, at.b, D, at.c, c);
+    if (p.segs > 1) from_segments<VEC, RC, true>(p, at, D, runs, c, tot[1]);
+    load_state<VEC>(a.h0, at.b, D, at.c, h0);
     const int tile = at.waves * RL * RB, first = (at.w * RL + at.tl) * RB;
     int parity = 0;
     const int64_t tiles = (at.r1 - at.r0 + tile - 1) / tile;
@@ -428,14 +480,6 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
                 run.b[i] = e[r][i].back(dv[r][i] + run.b[i]);
                 run.U[i] = e[r][i].lost(run.U[i]);
             }
-        if (COMPOSE) {
-            Run<VEC> tile_run;
-            block_run<VEC, RC, true>(run, tile_run, at.cl, at.tl, at.w, at.waves, tot[parity]);
-            tile_run.after(all);
-            all = tile_run;
-            parity ^= 1;
-            continue;
-        }
         float s[VEC];
         scan_tile<VEC, RC, true>(run, c, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
         parity ^= 1;
@@ -459,9 +503,7 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
             }
         }
     }
-    if (COMPOSE) {
-        if (at.w == 0 && at.tl == 0) store_run<VEC>(p, at, D, runs, all);
-    } else if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
+    if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
         store_vec<VEC>(a.dh0 + at.b * D + at.c, c);
     }
 }
@@ -491,11 +533,13 @@ hipError_t fwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs&
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, true, false>), grid, block, 0, s, d, p, a, runs);
+        hipLaunchKernelGGL((recur_runs_kernel<TS, TS, VEC, RC, false>), grid, block, 0, s, d, p,
+                           static_cast<const TS*>(a.g), static_cast<const TS*>(a.x), d.x_row, d.x_seq, a.lengths,
+                           runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, false, STREAM>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, STREAM>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
 }
 
@@ -504,11 +548,12 @@ hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs&
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_bwd_kernel<TS, float, VEC, RC, true, false>), grid, block, 0, s, d, p, a, runs);
+        hipLaunchKernelGGL((recur_runs_kernel<TS, float, VEC, RC, true>), grid, block, 0, s, d, p,
+                           static_cast<const TS*>(a.g), a.dy, d.D, d.T * d.D, a.lengths, runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, false, STREAM>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, STREAM>), grid, block, 0, s, d, p, a, runs);
     return hipGetLastError();
 }
 
