@@ -557,23 +557,35 @@ hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs&
     return hipGetLastError();
 }
 
-// Large outputs are stored as streamed data (8 x 4096 x 2048: bf16 forward 106.5 ->
-// 104 us, float32 backward 327 -> 315.5).
+// Large outputs are stored as streamed data where rows start on cache lines (8 x
+// 4096 x 2048: bf16 forward 106.5 -> 104 us, float32 backward 327 -> 315.5); cut
+// lines make streamed stores slower (70 x 1531 x 770 backward: 529 -> 581).
+bool streamed(const kan_recur_desc_t& d, const RecurPlan& p, int64_t bytes) {
+    return p.on_lines && d.B * d.T * d.D * bytes >= kStreamBytes;
+}
+
 template <typename TS>
 hipError_t fwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     if (p.vec == 1) return fwd_t<TS, 1, 4>(d, p, a, ws, s);
-    if (p.lanes == 16 && d.B * d.T * d.D * 4 >= kStreamBytes) return fwd_t<TS, 4, 16, true>(d, p, a, ws, s);
-    return p.lanes == 16 ? fwd_t<TS, 4, 16>(d, p, a, ws, s)
-                         : p.lanes == 8 ? fwd_t<TS, 4, 8>(d, p, a, ws, s) : fwd_t<TS, 4, 4>(d, p, a, ws, s);
+    const bool st = streamed(d, p, 4);
+    switch (p.lanes) {
+        case 32: return st ? fwd_t<TS, 4, 32, true>(d, p, a, ws, s) : fwd_t<TS, 4, 32>(d, p, a, ws, s);
+        case 16: return st ? fwd_t<TS, 4, 16, true>(d, p, a, ws, s) : fwd_t<TS, 4, 16>(d, p, a, ws, s);
+        case 8: return fwd_t<TS, 4, 8>(d, p, a, ws, s);
+        default: return fwd_t<TS, 4, 4>(d, p, a, ws, s);
+    }
 }
 
 template <typename TS, typename TG>
 hipError_t bwd_v(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     if (p.vec == 1) return bwd_t<TS, TG, 1, 4>(d, p, a, ws, s);
-    if (p.lanes == 16 && d.B * d.T * d.D * (int64_t)sizeof(TG) >= kStreamBytes)
-        return bwd_t<TS, TG, 4, 16, true>(d, p, a, ws, s);
-    return p.lanes == 16 ? bwd_t<TS, TG, 4, 16>(d, p, a, ws, s)
-                         : p.lanes == 8 ? bwd_t<TS, TG, 4, 8>(d, p, a, ws, s) : bwd_t<TS, TG, 4, 4>(d, p, a, ws, s);
+    const bool st = streamed(d, p, sizeof(TG));
+    switch (p.lanes) {
+        case 32: return st ? bwd_t<TS, TG, 4, 32, true>(d, p, a, ws, s) : bwd_t<TS, TG, 4, 32>(d, p, a, ws, s);
+        case 16: return st ? bwd_t<TS, TG, 4, 16, true>(d, p, a, ws, s) : bwd_t<TS, TG, 4, 16>(d, p, a, ws, s);
+        case 8: return bwd_t<TS, TG, 4, 8>(d, p, a, ws, s);
+        default: return bwd_t<TS, TG, 4, 4>(d, p, a, ws, s);
+    }
 }
 
 }  // namespace

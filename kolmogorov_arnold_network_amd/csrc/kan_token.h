@@ -35,14 +35,16 @@ hipError_t launch_embed_bwd(const kan_embed_desc_t& d, const EmbedPlan& p, const
 // ---- gated recurrence ----
 constexpr int64_t kRecurMaxChannels = int64_t(1) << 28;   // B times D, D rounded up to 64
 constexpr int kRecurWaves = 8;       // waves of a block at most
+constexpr int kRecurMaxSegs = 256;   // segments of a sequence at most
 constexpr int kRecurRows = 4;        // rows of a lane in a tile; a wave has 64 / lanes runs of them
 struct RecurPlan {
     int vec, lanes, waves, segs;     // channels of a lane, lanes along the channels, waves of a block, segments
+    bool on_lines;                   // rows start on cache lines
     unsigned blocks;                 // channel blocks
     int64_t seg_rows;
     size_t ws;                       // runs of the segments: [B][segs][2][D] float
 };
-RecurPlan recur_plan(const kan_recur_desc_t& d);
+RecurPlan recur_plan(const kan_recur_desc_t& d, int pass);
 
 struct RecurArgs {
     const void *x, *g;

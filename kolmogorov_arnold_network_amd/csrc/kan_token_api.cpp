@@ -142,27 +142,56 @@ EmbedPlan embed_plan(int64_t N, int64_t V, int64_t D) {
     return p;
 }
 
-RecurPlan recur_plan(const kan_recur_desc_t& d) {
-    // A block's time goes with its tiles, and the launch's with the most
-    // blocks that a compute unit gets.  Narrow blocks (fewer lanes along the
-    // channels) make more and shorter columns, at 32 or 64 bytes of a bf16 row
-    // a tile row; measured, that costs about 1.25 and 1.6 times as much an
-    // element.  Segments read x and g (g and dy) twice and take a launch more,
-    // about three tiles' time.
+RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
+    // Time is counted in tiles of 128 rows by 64 channels, of which 256, one for
+    // each compute unit, take about as long as their memory traffic.  A launch
+    // takes as many as the longest block has, 1.4 times that where a unit holds
+    // two blocks, and no less than its traffic.  Blocks with fewer lanes along
+    // the channels make more and shorter columns, but touch more cache lines
+    // for their bytes, above all where rows do not start on a line; measured,
+    // time goes with the lines to the power 0.75 or so (8 x 4096 x 2048 bf16
+    // forward: 106 us with 16 lanes, 126 with 8; 70 x 1531 x 770 bf16 backward:
+    // 461 with 32, 529 with 16, 364 with 16 at 768 channels).  Segments read a
+    // little twice and take a launch more (1 x 65536 x 1024 float32 forward:
+    // 644 us whole, 152 in segments).
     constexpr int64_t kCUs = 256;
+    const bool forward = pass == KAN_PASS_FORWARD;
     RecurPlan p;
     p.vec = d.D >= 4 ? 4 : 1;
+    const int es = dtype_bytes(d.dtype);
+    p.on_lines = (d.D * 4) % 128 == 0 && (d.x_row * es) % 128 == 0 && (d.g_row * es) % 128 == 0;
+    if (!forward)
+        p.on_lines = p.on_lines && (d.dx_row * dtype_bytes(d.grad_dtype)) % 128 == 0 &&
+                     (d.dg_row * dtype_bytes(d.grad_dtype)) % 128 == 0;
     const int64_t T = std::max<int64_t>(d.T, 1);
-    double least = 0;
-    auto weigh = [&](int lanes, int64_t segs) {
+    // cache lines that a block's row touches in its arrays, over the least that
+    // its bytes need
+    auto lines = [&](int lanes) {
+        double touched = 0, least = 0;
+        auto array = [&](int bytes, int count) {
+            const double own = lanes * p.vec * bytes / 128.0;
+            touched += count * (p.on_lines ? std::max(own, 1.0) : own + 1.0);
+            least += count * own;
+        };
+        array(es, 2);
+        array(4, forward ? 1 : 2);
+        if (!forward) array(dtype_bytes(d.grad_dtype), 2);
+        return pow(touched / least, 0.75);
+    };
+    double least = -1.0;
+    auto weigh = [&](int lanes, int64_t want) {        // want: blocks, in segments (0: whole)
         const int64_t tile = kRecurWaves * kRecurRows * (64 / lanes);
-        const int64_t blocks = (d.D + lanes * p.vec - 1) / (lanes * p.vec);
+        const int64_t blocks = (d.D + lanes * p.vec - 1) / (lanes * p.vec), have = std::max<int64_t>(1, d.B * blocks);
+        int64_t segs = std::min<int64_t>(std::min<int64_t>(kRecurMaxSegs, want / have), T / tile);
+        if (want > 0 && segs < 2) return;
         const int64_t rows = segs > 1 ? round_up((T + segs - 1) / segs, tile) : T;
         segs = (T + rows - 1) / rows;
-        const double narrow = lanes == 16 ? 1.0 : lanes == 8 ? 1.25 : 1.6;
-        const double most = (double)((d.B * blocks * segs + kCUs - 1) / kCUs), tiles = (double)((rows + tile - 1) / tile);
-        const double est = most * tiles * narrow * (segs > 1 ? 1.6 : 1.0) + (segs > 1 ? 3.0 : 0.0);
-        if (least > 0 && est >= least) return;
+        const int64_t n = have * segs;
+        const double most = n <= kCUs ? 1.0 : 1.4 * (double)((n + 2 * kCUs - 1) / (2 * kCUs));
+        const double tiles = (double)((rows + tile - 1) / tile);
+        const double traffic = (double)d.B * (double)T * (double)d.D / (128.0 * 64.0 * kCUs);
+        const double est = std::max(most * tiles, traffic) * lines(lanes) * (segs > 1 ? 1.1 : 1.0) + (segs > 1 ? 3.0 : 0.0);
+        if (least >= 0.0 && est >= least) return;
         least = est;
         p.lanes = lanes;
         p.segs = (int)segs;
@@ -170,15 +199,12 @@ RecurPlan recur_plan(const kan_recur_desc_t& d) {
         p.blocks = (unsigned)blocks;
     };
     if (p.vec == 1) {
-        weigh(4, 1);
+        weigh(4, 0);
+        weigh(4, kCUs);
     } else {
-        for (int lanes : {16, 8, 4}) weigh(lanes, 1);
+        for (int lanes : {32, 16, 8, 4}) weigh(lanes, 0);
+        for (int lanes : {32, 16, 8}) weigh(lanes, kCUs), weigh(lanes, 2 * kCUs);
     }
-    const int lanes = p.vec == 1 ? 4 : 16;
-    const int64_t tile = kRecurWaves * kRecurRows * (64 / lanes);
-    const int64_t have = std::max<int64_t>(1, d.B * ((d.D + lanes * p.vec - 1) / (lanes * p.vec)));
-    const int64_t segs = std::min<int64_t>(std::min<int64_t>(256, kCUs / have), T / (2 * tile));
-    if (segs > 1) weigh(lanes, segs);
     const int wave_rows = kRecurRows * (64 / p.lanes);
     p.waves = 1;
     while (p.waves < kRecurWaves && p.waves * wave_rows < p.seg_rows) p.waves *= 2;
@@ -235,7 +261,7 @@ int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void
 
 size_t kan_recur_workspace_size(const kan_recur_desc_t* desc, int pass) {
     if (recur_check(desc) != KAN_OK || (pass != KAN_PASS_FORWARD && pass != KAN_PASS_BACKWARD)) return SIZE_MAX;
-    return desc->B == 0 || desc->T == 0 ? 0 : recur_plan(*desc).ws;
+    return desc->B == 0 || desc->T == 0 ? 0 : recur_plan(*desc, pass).ws;
 }
 
 int kan_recur_forward(const kan_recur_desc_t* desc, const void* x, const void* g, const float* h0,
@@ -258,7 +284,7 @@ int kan_recur_forward(const kan_recur_desc_t* desc, const void* x, const void* g
     RecurArgs a = {};
     a.x = x, a.g = g, a.h0 = h0, a.lengths = lengths, a.out = y, a.hT = hT;
     (void)hipGetLastError();
-    return status_of(launch_recur_fwd(*desc, recur_plan(*desc), a, static_cast<char*>(ws),
+    return status_of(launch_recur_fwd(*desc, recur_plan(*desc, KAN_PASS_FORWARD), a, static_cast<char*>(ws),
                                       (hipStream_t)stream));
 }
 
@@ -313,7 +339,7 @@ int kan_recur_backward(const kan_recur_desc_t* desc, const void* x, const void* 
     a.x = x, a.g = g, a.h0 = h0, a.lengths = lengths, a.y = y, a.dy = dy, a.dhT = dhT, a.dx = dx, a.dg = dg,
     a.dh0 = dh0;
     (void)hipGetLastError();
-    return status_of(launch_recur_bwd(*desc, recur_plan(*desc), a, static_cast<char*>(ws),
+    return status_of(launch_recur_bwd(*desc, recur_plan(*desc, KAN_PASS_BACKWARD), a, static_cast<char*>(ws),
                                       (hipStream_t)stream));
 }
 

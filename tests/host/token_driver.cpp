@@ -60,7 +60,7 @@ hipError_t launch_embed_bwd(const kan_embed_desc_t& d, const EmbedPlan& p, const
 }
 static void recur(const kan_recur_desc_t& d, const RecurPlan& p, const char* ws) {
     need(d.B > 0 && d.D > 0, "recurrence shape");
-    need(p.vec == (d.D >= 4 ? 4 : 1) && (p.lanes == 4 || p.lanes == 8 || p.lanes == 16), "channels of a block");
+    need(p.vec == (d.D >= 4 ? 4 : 1) && (p.lanes == 4 || p.lanes == 8 || p.lanes == 16 || p.lanes == 32), "channels of a block");
     need(p.waves >= 1 && p.waves <= kRecurWaves, "waves");
     need((int64_t)p.blocks * p.lanes * p.vec >= d.D && (int64_t)(p.blocks - 1) * p.lanes * p.vec < d.D, "blocks");
     need(p.segs >= 1 && p.segs * p.seg_rows >= d.T && (p.segs == 1 || (p.segs - 1) * p.seg_rows < d.T), "segments");
@@ -135,11 +135,14 @@ int main() {
             for (int64_t D : {1, 2, 3, 4, 5, 16, 63, 64, 65, 770, 2048, 4096}) {
                 kan_recur_desc_t d{B, T, D, 2 * D, 2 * D * T, D, D * T, 2 * D, 2 * D * T, 2 * D, 2 * D * T, 0, 1};
                 ws_bytes = kan_recur_workspace_size(&d, KAN_PASS_FORWARD);
-                need(ws_bytes == kan_recur_workspace_size(&d, KAN_PASS_BACKWARD) && ws_bytes < big, "recurrence workspace");
+                need(ws_bytes < big, "recurrence workspace");
                 void* ws = ws_bytes ? at(12) : nullptr;
                 need(kan_recur_forward(&d, at(0), at(1), at<float>(2), at<int32_t>(3), at<float>(4), at<float>(5), ws,
                                        ws_bytes, nullptr) == KAN_OK,
                      "recurrence forward call");
+                ws_bytes = kan_recur_workspace_size(&d, KAN_PASS_BACKWARD);
+                need(ws_bytes < big, "recurrence workspace");
+                ws = ws_bytes ? at(12) : nullptr;
                 need(kan_recur_backward(&d, at(0), at(1), at<float>(2), at<int32_t>(3), at<float>(4), at<float>(5),
                                         at<float>(6), at(7), reinterpret_cast<char*>(at(7)) + 2 * D, at<float>(9), ws,
                                         ws_bytes, nullptr) == KAN_OK,
