@@ -163,12 +163,9 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
     const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
     TG* dz = STEP ? static_cast<TG*>(a.dz) + row * d.dz_row : nullptr;
     const float w = a.w ? a.w[row] : 1.0f;
-    if (w == 0.0f) {
-        if (threadIdx.x == 0) {
-            a.loss[row] = 0.0f;
-            if (!STEP) a.lse[row] = 0.0f;
-        }
-        if (STEP) zeros<TG, NT>(dz, 0, V);
+    if (STEP && w == 0.0f) {                           // the forward's lse is due for every row
+        if (threadIdx.x == 0) a.loss[row] = 0.0f;
+        zeros<TG, NT>(dz, 0, V);
         return;
     }
     const float inv = 1.0f / d.tau, c = kLog2e * inv;
@@ -253,7 +250,7 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
         if (ps[k] != 0.0f) l = ps[k] * (te.t - (zk - m0) * inv);
     }
     block_sum2<NT>(s, l, slots + 4 * W);
-    const bool empty = te.sum == 0.0f || s == 0.0f;
+    const bool empty = w == 0.0f || te.sum == 0.0f || s == 0.0f;
     if (threadIdx.x == 0) {
         a.loss[row] = empty ? 0.0f : w * d.tau * d.tau * (l - logf(te.sum) + logf(s));
         if (!STEP) a.lse[row] = m0 * inv + logf(s);

@@ -83,14 +83,14 @@ def _row(z, ids, t, tau):
 
 
 def distill(z, ids, t, tau, weight=None, dloss=None):
-    """``(loss, lse, dz)``; ``lse`` of a row of weight 0 is 0."""
+    """``(loss, lse, dz)``; a row of weight 0 has its ``lse`` all the same."""
     N, V = z.shape
     loss, lse, dz = np.zeros(N), np.zeros(N), np.zeros((N, V))
     for b in range(N):
         w = 1.0 if weight is None else float(weight[b])
-        if w == 0.0:
-            continue
         lq, lse[b], entries = _row(z[b], ids[b], t[b], tau)
+        if w == 0.0 and lq is not None:
+            continue
         if lq is None:
             if lse[b] != -np.inf:
                 s = z[b].astype(np.float64) / tau
