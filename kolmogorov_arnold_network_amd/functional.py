@@ -334,22 +334,24 @@ def _dev(t, name):
 
 
 def _rows(t, name, dtypes, dev, shape=None):
-    """Checks a tensor whose last dimension alone must be contiguous (None passes)."""
-    if t is None:
+    """Checks a tensor whose last dimension alone must be contiguous."""
+    if (t.get_device() == dev and t.dtype in dtypes and (t.is_contiguous() or t.stride(-1) == 1)
+            and (shape is None or t.shape == shape)):
         return
     if t.get_device() != dev:
         raise ValueError("%s must be on device %d, is on %s" % (name, dev, t.device))
     if t.dtype not in dtypes:
         raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, tuple(dtypes)))
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("the last dimension of %s must be contiguous" % name)
     if shape is not None and t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
 
 
 def _whole(t, name, dtypes, dev, shape=None):
-    """Checks a contiguous tensor (None passes)."""
-    if t is None:
+    """Checks a contiguous tensor."""
+    if (t.get_device() == dev and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
         return
     _rows(t, name, dtypes, dev, shape)
     if not t.is_contiguous():
