@@ -57,6 +57,17 @@ __device__ __forceinline__ void block_sum2(float& a, float& b, float* slots) {
     for (int i = 1; i < NT / 64; ++i) a += slots[i], b += slots[NT / 64 + i];
 }
 
+// LDS of a row's teacher: ids (-1: absent) and p of its entries, and a table of
+// the ids that occur, twice as large as a block has entries: the id of a slot,
+// how many entries have it, and the first of them.
+template <int NT>
+struct TeacherShared {
+    int ids[NT];
+    float ps[NT];
+    int key[2 * NT], count[2 * NT], first[2 * NT];
+    float slots[3 * (NT / 64)];
+};
+
 // A row's teacher.  Thread k holds entry k (a block has at least K threads):
 // the id (-1: absent or t = -inf), (t - max t) / tau and, after `finish`, p.
 template <int NT>
@@ -76,41 +87,48 @@ struct Teacher {
                                                    : load_f(static_cast<const uint16_t*>(a.t), at);
         if (v >= 0 && v < d.V && x != -INFINITY) id = (int)v, t = x;
     }
-    // ids and p of the row to LDS, p in place
-    __device__ __forceinline__ void finish(const kan_distill_desc_t& d, float* slots, int* ids, float* ps) {
-        const float m = block_max<NT>(t, slots);       // a NaN shows in the sum
+    // ids and p of the row to LDS, p in place; TABLE: an empty table of ids
+    template <bool TABLE>
+    __device__ __forceinline__ void finish(const kan_distill_desc_t& d, TeacherShared<NT>& sh) {
+        const float m = block_max<NT>(t, sh.slots);    // a NaN shows in the sum
         t = (t - (m == -INFINITY ? 0.0f : m)) / d.tau;
         p = id >= 0 ? exp2_raw(t * kLog2e) : 0.0f;
         float none = 0.0f;
         sum = p;
-        block_sum2<NT>(sum, none, slots + NT / 64);
+        block_sum2<NT>(sum, none, sh.slots + NT / 64);
         p = id >= 0 ? p / sum : 0.0f;
-        // entries past K, up to a multiple of 4, are absent
-        if ((int)threadIdx.x < ((d.K + 3) & ~3)) ids[threadIdx.x] = id, ps[threadIdx.x] = p;
+        sh.ids[threadIdx.x] = id;
+        sh.ps[threadIdx.x] = p;
+        if (TABLE) {
+#pragma unroll
+            for (int i = threadIdx.x; i < 2 * NT; i += NT) sh.key[i] = -1, sh.count[i] = 0, sh.first[i] = NT;
+        }
         __syncthreads();
     }
     // p becomes the sum over the entries of the same id, at the first of them;
-    // the others drop out (id -1).  Only the waves that hold entries look, at
-    // four others a read: with all of 16 waves looking at one each, 128 entries
-    // took longer than the row.
-    __device__ __forceinline__ void join_equal(const kan_distill_desc_t& d, const int* ids, const float* ps) {
-        if ((int)threadIdx.x >= d.K) return;
-        bool first = true;
-        float s = 0.0f;
-        for (int j = 0; j < d.K; j += 4) {
-            const int4 i = *reinterpret_cast<const int4*>(ids + j);
-            const float4 q = *reinterpret_cast<const float4*>(ps + j);
-            const int of[4] = {i.x, i.y, i.z, i.w};
-            const float pr[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool same = of[k] == id;
-                first = first && !(same && j + k < (int)threadIdx.x);
-                s += same ? pr[k] : 0.0f;
+    // the others drop out (id -1).  The table finds the ids that occur more than
+    // once, whose entries alone are gone through (a comparison of every pair
+    // took 4 us a row with 256 entries).
+    __device__ __forceinline__ void join_equal(const kan_distill_desc_t& d, TeacherShared<NT>& sh) {
+        int slot = 0;
+        if (id >= 0) {
+            slot = (int)(((uint32_t)id * 2654435769u) >> 16) & (2 * NT - 1);
+            for (;;) {                                 // ends: at most NT ids in 2 NT slots
+                const int was = atomicCAS(&sh.key[slot], -1, id);
+                if (was == -1 || was == id) break;
+                slot = (slot + 1) & (2 * NT - 1);
             }
+            atomicAdd(&sh.count[slot], 1);
+            atomicMin(&sh.first[slot], (int)threadIdx.x);
         }
-        if (!first) id = -1;
-        p = s;
+        __syncthreads();
+        if (id < 0 || sh.count[slot] == 1) return;
+        if (sh.first[slot] == (int)threadIdx.x) {
+            p = 0.0f;
+            for (int j = 0; j < d.K; ++j) p += sh.ids[j] == id ? sh.ps[j] : 0.0f;
+        } else {
+            id = -1;
+        }
     }
 };
 
@@ -156,9 +174,8 @@ template <typename TS, typename TG, int NT, int NV, bool STEP, bool STREAM>
 __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, DistillArgs a) {
     constexpr int W = NT / 64;
     typedef Raw<TS, VE> Vec;
-    __shared__ float slots[6 * W];
-    __shared__ __attribute__((aligned(16))) int ids[NT];
-    __shared__ __attribute__((aligned(16))) float ps[NT];
+    __shared__ TeacherShared<NT> sh;
+    __shared__ float slots[3 * W];
     const int64_t row = blockIdx.x, V = d.V;
     const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
     TG* dz = STEP ? static_cast<TG*>(a.dz) + row * d.dz_row : nullptr;
@@ -191,8 +208,7 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
             }
         }
     }
-    te.finish(d, slots, ids, ps);
-    if (STEP) te.join_equal(d, ids, ps);
+    te.template finish<STEP>(d, sh);
     // a running maximum and sum over what registers do not hold
     for (int64_t v = body + NV * STRIDE; v + VE <= V; v += STRIDE * DU) {
         Vec q[DU];
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
             m = fmaxf(m, max_of<TS, VE>(keep[v]));
         }
     }
-    m = block_max<NT>(m, slots + 3 * W);
+    m = block_max<NT>(m, slots);
     const float m0 = m == -INFINITY ? 0.0f : m;
     s *= exp2_raw((m_stream - m0) * c);
     hz = exp2_raw((hz - m0) * c);
@@ -244,12 +260,12 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
     }
     // sum_k p_k (log p_k + log(teacher's sum) - (z_k - m) / tau); the logs of the sums come after it
     float l = 0.0f, zk = -INFINITY;
-    const int k = threadIdx.x;
-    if (k < d.K && ids[k] >= 0) {
-        zk = load_f(z, ids[k]);
-        if (ps[k] != 0.0f) l = ps[k] * (te.t - (zk - m0) * inv);
+    if (te.id >= 0) {
+        zk = load_f(z, te.id);
+        if (te.p != 0.0f) l = te.p * (te.t - (zk - m0) * inv);
     }
-    block_sum2<NT>(s, l, slots + 4 * W);
+    if (STEP) te.join_equal(d, sh);
+    block_sum2<NT>(s, l, slots + W);
     const bool empty = w == 0.0f || te.sum == 0.0f || s == 0.0f;
     if (threadIdx.x == 0) {
         a.loss[row] = empty ? 0.0f : w * d.tau * d.tau * (l - logf(te.sum) + logf(s));
@@ -303,10 +319,7 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
 template <typename TS, typename TG, int NT, int VE, bool STREAM>
 __global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, DistillArgs a, int parts,
                                                          int64_t part) {
-    constexpr int W = NT / 64;
-    __shared__ float slots[3 * W];
-    __shared__ __attribute__((aligned(16))) int ids[NT];
-    __shared__ __attribute__((aligned(16))) float ps[NT];
+    __shared__ TeacherShared<NT> sh;
     const int64_t row = blockIdx.x / (unsigned)parts, V = d.V;
     const int p = (int)(blockIdx.x % (unsigned)parts);
     const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
@@ -320,12 +333,12 @@ __global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, D
     }
     Teacher<NT> te;
     te.load(d, a, row);
-    te.finish(d, slots, ids, ps);
+    te.template finish<true>(d, sh);
     if (te.sum == 0.0f) {
         zeros<TG, NT>(dz, v0, v1);
         return;
     }
-    te.join_equal(d, ids, ps);
+    te.join_equal(d, sh);
     const float f = w * d.tau * a.dloss[row], inv = 1.0f / d.tau;
     auto q = [&](float x) { return exp2_raw(__builtin_fmaf(x, inv, -lse) * kLog2e); };
     constexpr int64_t STRIDE = NT * VE;
@@ -373,9 +386,11 @@ hipError_t step_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t
     return row_t<TS, TG, 1024, NV, true, false>(d, a, s);
 }
 
+// Few long rows take a block of 1024 threads each (64 x 131072 float32: 23 us with
+// 256), many rows one of 256 (16384 x 4000 bf16: 47 us, 87 with 512).
 template <typename TS, bool STREAM>
 hipError_t fwd_s(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    if (d.K > 256) return row_t<TS, TS, 1024, 0, false, STREAM>(d, a, s);
+    if (d.K > 256 || (d.N <= 512 && d.V >= 8192)) return row_t<TS, TS, 1024, 0, false, STREAM>(d, a, s);
     if (d.K > 64 || d.V > 64 * 64) return row_t<TS, TS, 256, 0, false, STREAM>(d, a, s);
     return row_t<TS, TS, 64, 0, false, STREAM>(d, a, s);
 }
@@ -406,7 +421,8 @@ hipError_t bwd_n(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t 
 }
 template <typename TS, typename TG>
 hipError_t bwd_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    return d.K > 256 ? bwd_n<TS, TG, 1024>(d, a, s) : bwd_n<TS, TG, 256>(d, a, s);
+    if (d.K > 256) return bwd_n<TS, TG, 1024>(d, a, s);
+    return d.K > 64 || d.V > 64 * 64 ? bwd_n<TS, TG, 256>(d, a, s) : bwd_n<TS, TG, 64>(d, a, s);
 }
 
 }  // namespace
