@@ -428,7 +428,10 @@ int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void
  * dx and dg are 0 from a sequence's length to T.  Runs of rows are composed in
  * the form h -> h + (b - U h), with U = 1 - prod f accumulated directly, so
  * that gates near 1 (long memories) lose no digits; all of it in float32, in
- * a fixed order.  x, g in `dtype` and dx, dg in `grad_dtype` have strides
+ * a fixed order.  Where long sequences are cut into segments, a segment starts
+ * from the rows before it up to where what is left of a state is 2^-25 of it:
+ * the rest is below the state's last place (an infinity or NaN among those
+ * rows goes no further either).  hT is the last row of y, bit for bit.  x, g in `dtype` and dx, dg in `grad_dtype` have strides
  * (elements from one row to the next, and from one sequence to the next), so
  * they may be the halves of one projection; y, dy [B, T, D], h0, hT, dhT, dh0
  * [B, D] are contiguous float32. */
@@ -493,7 +496,8 @@ typedef struct {
 } kan_distill_desc_t;
 
 /* Bytes of workspace kan_distill_forward and kan_distill_step need (SIZE_MAX
- * if `desc` is invalid): with few rows, the maxima and sums of a row's parts. */
+ * if `desc` is invalid): for a step of few long rows, the maxima and sums of a
+ * row's parts; otherwise 0. */
 size_t kan_distill_workspace_size(const kan_distill_desc_t* desc);
 int kan_distill_forward(const kan_distill_desc_t* desc, const void* z, const void* ids, const void* t,
                         const float* w, float* loss, float* lse, void* workspace, size_t workspace_bytes,

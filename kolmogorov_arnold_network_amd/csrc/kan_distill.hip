@@ -5,8 +5,10 @@
 //     dz_v = dloss w tau (q_v - sum over k with id_k = v of p_k).
 //
 // K is small beside V: reading z once and writing dz once is the work, so HBM
-// traffic bounds it; the arithmetic is an exponential and about six operations
-// an element.  A row's maximum m and s = sum exp((z - m) / tau) are kept, not
+// traffic bounds it; the arithmetic is one or two exponentials and about six
+// operations an element.  Measured: step of 8192 x 65536 float32 769 us (4.1 GB,
+// 5.3 TB/s), backward of 4096 x 50021 bf16 154 us (779 MB, 5.1 TB/s), forward of
+// 4096 x 50021 float32 128 us (820 MB read, 6.4 TB/s).  A row's maximum m and s = sum exp((z - m) / tau) are kept, not
 // their sum in lse: the loss is formed from z_{id} - m and log s, which are
 // small where lse and z / tau may be large.
 //
@@ -314,57 +316,144 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
     if (te.id >= 0) put1(dz + te.id, fs * exp2_raw((zk - m0) * c) - f * te.p);
 }
 
-// Backward: block (row, p) writes part p of a row's vectors, the first block the
-// head too and the last the tail.
-template <typename TS, typename TG, int NT, int VE, bool STREAM>
-__global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, DistillArgs a, int parts,
-                                                         int64_t part) {
+// Part p of a row that is cut for several blocks: elements [v0, v1), the first
+// part with the head, vectors from v, and the part that ends the row with the
+// tail, `tail` on.  Parts are `part` elements of vectors; with a head the last
+// one may be empty (v0 = v1).
+struct Part {
+    int64_t v0, v1, v, tail;
+    __device__ __forceinline__ Part(int p, int64_t part, int head, int64_t V, int VE) {
+        v = head + p * part;
+        v0 = p ? min(v, V) : 0;
+        v1 = min(v + part, V);
+        tail = v0 < V && v1 == V ? V - (V - head) % VE : V;
+    }
+};
+
+// Maximum and sum of exp((z - max) / tau) of part p of a row, for a step of few
+// long rows: out[row][p].
+template <typename TS, int NT>
+__global__ void __launch_bounds__(NT) distill_part_kernel(kan_distill_desc_t d, DistillArgs a, int parts, int64_t part,
+                                                          float2* out) {
+    __shared__ float slots[3 * (NT / 64)];
+    const int64_t row = blockIdx.x / (unsigned)parts, V = d.V;
+    const int p = (int)(blockIdx.x % (unsigned)parts);
+    if (a.w && a.w[row] == 0.0f) return;               // not read in the second launch
+    const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
+    const int head = head_of(z, V);
+    const Part at(p, part, head, V, VE);
+    const float c = kLog2e / d.tau;
+    constexpr int64_t STRIDE = NT * VE;
+    float m = -INFINITY, s = 0.0f;
+    const float hz = p == 0 && (int)threadIdx.x < head ? load_f(z, threadIdx.x) : -INFINITY;
+    const float tz = at.tail + threadIdx.x < V ? load_f(z, at.tail + threadIdx.x) : -INFINITY;
+    for (int64_t v = at.v + (int64_t)threadIdx.x * VE; v + VE <= at.v1; v += STRIDE * DU) {
+        Raw<TS, VE> q[DU];
+#pragma unroll
+        for (int u = 0; u < DU; ++u) {
+            const int64_t e = v + u * STRIDE;
+            q[u] = load_raw<TS, VE>(z + (e + VE <= at.v1 ? e : v));
+        }
+        float g = m;
+#pragma unroll
+        for (int u = 0; u < DU; ++u) g = fmaxf(g, max_of<TS, VE>(q[u]));
+        const float g0 = g == -INFINITY ? 0.0f : g;
+        s *= exp2_raw((m - g0) * c);
+        m = g;
+#pragma unroll
+        for (int u = 0; u < DU; ++u) {
+            if (v + u * STRIDE + VE > at.v1) continue;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) s += exp2_raw((raw_value(q[u], i) - g0) * c);
+        }
+    }
+    const float mine = m;
+    m = block_max<NT>(fmaxf(m, fmaxf(hz, tz)), slots);
+    const float m0 = m == -INFINITY ? 0.0f : m;
+    s = s * exp2_raw((mine - m0) * c) + exp2_raw((hz - m0) * c) + exp2_raw((tz - m0) * c);
+    float none = 0.0f;
+    block_sum2<NT>(s, none, slots + NT / 64);
+    if (threadIdx.x == 0) out[blockIdx.x] = make_float2(m, s);
+}
+
+// Backward, or (STEP) the second launch of a step of few long rows: block (row,
+// p) writes part p of a row's gradient; a step's first block the loss too.
+template <typename TS, typename TG, int NT, int VE, bool STREAM, bool STEP>
+__global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, DistillArgs a, int parts, int64_t part,
+                                                         const float2* sums, int n_sums) {
     __shared__ TeacherShared<NT> sh;
+    __shared__ float slots[2 * (NT / 64)];
     const int64_t row = blockIdx.x / (unsigned)parts, V = d.V;
     const int p = (int)(blockIdx.x % (unsigned)parts);
     const TS* z = static_cast<const TS*>(a.z) + row * d.z_row;
     TG* dz = static_cast<TG*>(a.dz) + row * d.dz_row;
     const int head = head_of(dz, V);
-    const int64_t v0 = p ? min(head + p * part, V) : 0, v1 = p == parts - 1 ? V : min(head + (p + 1) * part, V);
-    const float w = a.w ? a.w[row] : 1.0f, lse = w != 0.0f ? a.lse_in[row] : 0.0f;
-    if (w == 0.0f || lse == -INFINITY) {
-        zeros<TG, NT>(dz, v0, v1);
-        return;
+    const Part at(p, part, head, V, VE);
+    const float w = a.w ? a.w[row] : 1.0f, inv = 1.0f / d.tau, c = kLog2e * inv;
+    float lse = 0.0f, m0 = 0.0f, s = 0.0f;
+    bool empty = w == 0.0f;
+    if (!empty && STEP) {
+        // every wave joins the parts' sums, a lane to a part (at most 64)
+        const int lane = threadIdx.x & 63;
+        const float2 q = lane < n_sums ? sums[row * n_sums + lane] : make_float2(-INFINITY, 0.0f);
+        float m = q.x;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+        m0 = m == -INFINITY ? 0.0f : m;
+        s = q.y * exp2_raw((q.x - m0) * c);
+        if (q.y == 0.0f) s = 0.0f;                     // a part of -inf only
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+        empty = s == 0.0f;
+    } else if (!empty) {
+        lse = a.lse_in[row];
+        empty = lse == -INFINITY;
     }
     Teacher<NT> te;
-    te.load(d, a, row);
-    te.template finish<true>(d, sh);
-    if (te.sum == 0.0f) {
-        zeros<TG, NT>(dz, v0, v1);
+    if (!empty) {                                      // uniform across the block
+        te.load(d, a, row);
+        te.template finish<true>(d, sh);
+        empty = te.sum == 0.0f;
+    }
+    if (empty) {
+        zeros<TG, NT>(dz, at.v0, at.v1);
+        if (STEP && p == 0 && threadIdx.x == 0) a.loss[row] = 0.0f;
         return;
     }
+    if (STEP && p == 0) {
+        float l = 0.0f, none = 0.0f;
+        if (te.id >= 0 && te.p != 0.0f) l = te.p * (te.t - (load_f(z, te.id) - m0) * inv);
+        block_sum2<NT>(l, none, slots);
+        if (threadIdx.x == 0) a.loss[row] = w * d.tau * d.tau * (l - logf(te.sum) + logf(s));
+    }
     te.join_equal(d, sh);
-    const float f = w * d.tau * a.dloss[row], inv = 1.0f / d.tau;
-    auto q = [&](float x) { return exp2_raw(__builtin_fmaf(x, inv, -lse) * kLog2e); };
+    const float f = w * d.tau * (STEP ? 1.0f : a.dloss[row]), fs = STEP ? f / s : f;
+    auto fq = [&](float x) {                           // f q
+        return fs * exp2_raw(STEP ? (x - m0) * c : __builtin_fmaf(x, inv, -lse) * kLog2e);
+    };
     constexpr int64_t STRIDE = NT * VE;
-    for (int64_t v = head + p * part + (int64_t)threadIdx.x * VE; v + VE <= v1; v += STRIDE * DU) {
+    for (int64_t v = at.v + (int64_t)threadIdx.x * VE; v + VE <= at.v1; v += STRIDE * DU) {
         Raw<TS, VE> x[DU];
 #pragma unroll
         for (int u = 0; u < DU; ++u) {
-            const int64_t at = v + u * STRIDE;
-            x[u] = load_raw<TS, VE>(z + (at + VE <= v1 ? at : v));
+            const int64_t e = v + u * STRIDE;
+            x[u] = load_raw<TS, VE>(z + (e + VE <= at.v1 ? e : v));
         }
 #pragma unroll
         for (int u = 0; u < DU; ++u) {
-            if (v + u * STRIDE + VE > v1) continue;
+            if (v + u * STRIDE + VE > at.v1) continue;
             float o[VE];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) o[i] = f * q(raw_value(x[u], i));
+            for (int i = 0; i < VE; ++i) o[i] = fq(raw_value(x[u], i));
             store_vec<VE, STREAM>(dz + v + u * STRIDE, o);
         }
     }
-    if (p == 0 && (int)threadIdx.x < head) put1(dz + threadIdx.x, f * q(load_f(z, threadIdx.x)));
-    if (p == parts - 1) {
-        const int64_t tail = V - (V - head) % VE + threadIdx.x;
-        if (tail < V) put1(dz + tail, f * q(load_f(z, tail)));
-    }
+    if (p == 0 && (int)threadIdx.x < head) put1(dz + threadIdx.x, fq(load_f(z, threadIdx.x)));
+    const int64_t tail = at.tail + threadIdx.x;
+    if (tail < V) put1(dz + tail, fq(load_f(z, tail)));
+    // the teacher's entries again, now with their p taken off
     __syncthreads();
-    if (te.id >= v0 && te.id < v1) put1(dz + te.id, f * (q(load_f(z, te.id)) - te.p));
+    if (te.id >= at.v0 && te.id < at.v1) put1(dz + te.id, fq(load_f(z, te.id)) - f * te.p);
 }
 
 template <typename TS, typename TG, int NT, int NV, bool STEP, bool STREAM>
@@ -405,8 +494,8 @@ hipError_t fwd_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t 
     return d.N * d.V * (int64_t)sizeof(TS) >= kStreamBytes ? fwd_s<TS, true>(d, a, s) : fwd_s<TS, false>(d, a, s);
 }
 
-template <typename TS, typename TG, int NT>
-hipError_t bwd_n(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
+template <typename TS, typename TG, int NT, bool STEP>
+hipError_t bwd_n(const kan_distill_desc_t& d, const DistillArgs& a, const float2* sums, int n_sums, hipStream_t s) {
     constexpr int VE = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;     // 16 bytes of the wider type
     constexpr int64_t round = NT * VE;
     // Blocks of one round of loads each, up to 32768 of them: 4096 x 50021 takes
@@ -414,35 +503,54 @@ hipError_t bwd_n(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t 
     // six.
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((32768 + d.N - 1) / d.N, d.V / (round * DU)));
     const int64_t part = round_up((d.V + parts - 1) / parts, round), n = (d.V + part - 1) / part;
-    // streamed stores past kStreamBytes: 4096 x 50021 bf16 197 -> 170 us, float32 372 -> 331
-    if (d.N * d.V * (int64_t)sizeof(TG) >= kStreamBytes)
-        hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, VE, true>), dim3((unsigned)(d.N * n)), dim3(NT), 0, s, d, a,
-                           (int)n, part);
+    const dim3 grid((unsigned)(d.N * n));
+    // streamed stores past kStreamBytes: 4096 x 50021 bf16 197 -> 170 us, float32
+    // 372 -> 331 (a step of few rows does not come near)
+    if (!STEP && d.N * d.V * (int64_t)sizeof(TG) >= kStreamBytes)
+        hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, VE, !STEP, STEP>), grid, dim3(NT), 0, s, d, a, (int)n, part,
+                           sums, n_sums);
     else
-        hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, VE, false>), dim3((unsigned)(d.N * n)), dim3(NT), 0, s, d, a,
-                           (int)n, part);
+        hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, VE, false, STEP>), grid, dim3(NT), 0, s, d, a, (int)n, part,
+                           sums, n_sums);
     return hipGetLastError();
 }
+template <typename TS, typename TG, bool STEP>
+hipError_t bwd_t(const kan_distill_desc_t& d, const DistillArgs& a, const float2* sums, int n_sums, hipStream_t s) {
+    if (d.K > 256) return bwd_n<TS, TG, 1024, STEP>(d, a, sums, n_sums, s);
+    if (STEP || d.K > 64 || d.V > 64 * 64) return bwd_n<TS, TG, 256, STEP>(d, a, sums, n_sums, s);
+    return bwd_n<TS, TG, 64, STEP>(d, a, sums, n_sums, s);
+}
+
 template <typename TS, typename TG>
-hipError_t bwd_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
-    if (d.K > 256) return bwd_n<TS, TG, 1024>(d, a, s);
-    return d.K > 64 || d.V > 64 * 64 ? bwd_n<TS, TG, 256>(d, a, s) : bwd_n<TS, TG, 64>(d, a, s);
+hipError_t cut_step(const kan_distill_desc_t& d, const DistillPlan& p, const DistillArgs& a, char* ws, hipStream_t s) {
+    float2* sums = reinterpret_cast<float2*>(ws);
+    hipLaunchKernelGGL((distill_part_kernel<TS, 256>), dim3((unsigned)(d.N * p.parts)), dim3(256), 0, s, d, a, p.parts,
+                       p.part, sums);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : bwd_t<TS, TG, true>(d, a, sums, p.parts, s);
+}
+
+template <typename TS, typename TG>
+hipError_t step(const kan_distill_desc_t& d, const DistillPlan& p, const DistillArgs& a, char* ws, hipStream_t s) {
+    return p.parts > 1 ? cut_step<TS, TG>(d, p, a, ws, s) : step_t<TS, TG>(d, a, s);
 }
 
 }  // namespace
 
-hipError_t launch_distill(const kan_distill_desc_t& d, const DistillPlan&, const DistillArgs& a, char*,
+hipError_t launch_distill(const kan_distill_desc_t& d, const DistillPlan& p, const DistillArgs& a, char* ws,
                           hipStream_t s) {
     if (!a.dz) return d.dtype == KAN_F32 ? fwd_t<float>(d, a, s) : fwd_t<uint16_t>(d, a, s);
     if (d.dtype == KAN_F32)
-        return d.grad_dtype == KAN_F32 ? step_t<float, float>(d, a, s) : step_t<float, uint16_t>(d, a, s);
-    return d.grad_dtype == KAN_F32 ? step_t<uint16_t, float>(d, a, s) : step_t<uint16_t, uint16_t>(d, a, s);
+        return d.grad_dtype == KAN_F32 ? step<float, float>(d, p, a, ws, s) : step<float, uint16_t>(d, p, a, ws, s);
+    return d.grad_dtype == KAN_F32 ? step<uint16_t, float>(d, p, a, ws, s) : step<uint16_t, uint16_t>(d, p, a, ws, s);
 }
 
 hipError_t launch_distill_bwd(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
     if (d.dtype == KAN_F32)
-        return d.grad_dtype == KAN_F32 ? bwd_t<float, float>(d, a, s) : bwd_t<float, uint16_t>(d, a, s);
-    return d.grad_dtype == KAN_F32 ? bwd_t<uint16_t, float>(d, a, s) : bwd_t<uint16_t, uint16_t>(d, a, s);
+        return d.grad_dtype == KAN_F32 ? bwd_t<float, float, false>(d, a, nullptr, 0, s)
+                                       : bwd_t<float, uint16_t, false>(d, a, nullptr, 0, s);
+    return d.grad_dtype == KAN_F32 ? bwd_t<uint16_t, float, false>(d, a, nullptr, 0, s)
+                                   : bwd_t<uint16_t, uint16_t, false>(d, a, nullptr, 0, s);
 }
 
 }  // namespace kan

@@ -62,7 +62,9 @@ hipError_t launch_recur_step(const kan_recur_desc_t& d, int64_t S, const void* x
 constexpr int64_t kDistillMaxN = int64_t(1) << 21;
 constexpr int kDistillMaxK = 1024;   // teacher logits of a row at most
 struct DistillPlan {
-    size_t ws;
+    int parts;           // of a row in the step's first launch (1: a block to a row, one launch)
+    int64_t part;        // vector elements of a part
+    size_t ws;           // maxima and sums of the parts: [N][parts] float2
 };
 DistillPlan distill_plan(const kan_distill_desc_t& d);
 

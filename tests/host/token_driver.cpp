@@ -93,6 +93,9 @@ hipError_t launch_distill(const kan_distill_desc_t& d, const DistillPlan& p, con
                           hipStream_t) {
     need(d.N > 0 && a.z && a.ids && a.t && a.loss && (a.lse != nullptr) != (a.dz != nullptr), "distillation");
     need(p.ws <= ws_bytes && d.N * 1024 <= kGrid && d.K <= 1024, "distillation plan");
+    need(p.parts >= 1 && p.parts <= 64 && p.parts * p.part >= d.V && (p.parts == 1 || p.part % 1024 == 0),
+         "parts cover a row");
+    need(p.parts == 1 || p.ws >= (size_t)(d.N * p.parts) * 8, "parts' sums fit");
     ++launches;
     return hipSuccess;
 }

@@ -204,6 +204,26 @@ def test_a_gradient_row_sums_to_zero_and_rows_are_untouched_outside(env):
     assert float(wide[:, :1003].double().sum(1).abs().max()) <= 40 * EPS * 30
 
 
+@pytest.mark.parametrize("V,dtype", [(20485, "f32"), (40965, "bf16"), (20485, "bf16"), (122885, "f32"), (122885, "bf16")])
+@pytest.mark.parametrize("N", [2, 40, 70])
+def test_a_part_that_ends_in_the_next_ones_head(env, V, dtype, N):
+    """Vocabularies a few elements past a whole number of a row's parts: with rows
+    that start inside a cache line the last part is empty, and the row's tail,
+    with the teacher's entries in it, belongs to the part before it."""
+    torch, F = env
+    z, ids, t, w = _case(torch, N, V, 12, dtype, V + N)
+    ids = torch.arange(V - 12, V, device="cuda:0").repeat(N, 1)
+    _check(torch, F, z, ids, t, w, 1.0, dtype)
+
+
+def test_rows_cut_over_blocks(env):
+    """Few rows of a large vocabulary: masks, empty rows and weights as elsewhere."""
+    test_masked_logits(env, 131075)
+    test_rows_without_weight_are_not_read(env, 131075, 4)
+    for bad in ("nan", "inf"):
+        test_nan_and_inf_show(env, 131075, 3, bad)
+
+
 def test_empty(env):
     torch, F = env
     z, ids, t = (torch.empty(0, n, device="cuda:0") for n in (10, 3, 3))
