@@ -75,6 +75,7 @@ __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, 
 }
 
 constexpr int RW = kRecurWaves;    // waves of a block at most
+constexpr int kRunsLanes(int vec) { return vec == 1 ? 4 : 16; }    // of the launch that composes segments
 
 // What a block works on: channels c .. c + VEC - 1 of sequence b, rows
 // [r0, r1) of segment seg.  Blocks that share cache lines of a row go to the
@@ -245,8 +246,8 @@ constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 // from the end that counts most, the one where it hands its state on, and ends
 // where the share that is left of what comes before is at most 2^-25 in every
 // channel of the block: the rest of the segment would change the state by less
-// than its last place.  Common gates forget in a tile or two (128 or 256 rows);
-// gates that do not are read to the segment's start.
+// than its last place.  Common gates forget in a tile or two (128 rows by 64
+// channels); gates that do not are read to the segment's start.
 template <typename TS, typename TV, int VEC, int RC, bool BACK>
 __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d, RecurPlan p, const TS* g, const TV* v,
                                                              int64_t v_row, int64_t v_seq, const int32_t* lengths,
@@ -274,9 +275,9 @@ __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d,
     float left[VEC];                                   // 1 - all.U, with the digits of small values
 #pragma unroll
     for (int i = 0; i < VEC; ++i) left[i] = 1.0f;
-    if (tiles > 0) load(start(0));
     for (int64_t k = 0; k < tiles; ++k) {
         const int64_t t = start(k) + first;
+        load(start(k));
         Run<VEC> run, whole;
         run.clear();
 #pragma unroll
@@ -291,7 +292,6 @@ __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d,
                 run.U[i] = e.lost(run.U[i]);
             }
         }
-        if (k + 1 < tiles) load(start(k + 1));
         block_run<VEC, RC, BACK>(run, whole, at.cl, at.tl, at.w, at.waves, tot[k & 1]);
         bool done = true;
 #pragma unroll
@@ -532,12 +532,24 @@ __global__ void __launch_bounds__(64) recur_step_kernel(kan_recur_desc_t d, int6
     y[b * d.D + c] = n;
 }
 
+// The plan of the launch that composes the segments' runs: lanes and waves of
+// its own, the same segments.
+RecurPlan runs_plan(const kan_recur_desc_t& d, RecurPlan p) {
+    p.lanes = kRunsLanes(p.vec);
+    p.blocks = (unsigned)((d.D + p.lanes * p.vec - 1) / (p.lanes * p.vec));
+    p.waves = 1;
+    while (p.waves < kRecurWaves && p.waves * kRecurRows * (64 / p.lanes) < p.seg_rows) p.waves *= 2;
+    return p;
+}
+
 template <typename TS, int VEC, int RC, bool STREAM = false>
 hipError_t fwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_runs_kernel<TS, TS, VEC, RC, false>), grid, block, 0, s, d, p,
+        const RecurPlan r = runs_plan(d, p);
+        hipLaunchKernelGGL((recur_runs_kernel<TS, TS, VEC, kRunsLanes(VEC), false>),
+                           dim3((unsigned)(d.B * r.blocks * r.segs)), dim3(64 * r.waves), 0, s, d, r,
                            static_cast<const TS*>(a.g), static_cast<const TS*>(a.x), d.x_row, d.x_seq, a.lengths,
                            runs);
         const hipError_t e = hipGetLastError();
@@ -552,7 +564,9 @@ hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs&
     float* runs = reinterpret_cast<float*>(ws);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
-        hipLaunchKernelGGL((recur_runs_kernel<TS, float, VEC, RC, true>), grid, block, 0, s, d, p,
+        const RecurPlan r = runs_plan(d, p);
+        hipLaunchKernelGGL((recur_runs_kernel<TS, float, VEC, kRunsLanes(VEC), true>),
+                           dim3((unsigned)(d.B * r.blocks * r.segs)), dim3(64 * r.waves), 0, s, d, r,
                            static_cast<const TS*>(a.g), a.dy, d.D, d.T * d.D, a.lengths, runs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
