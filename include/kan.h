@@ -431,9 +431,10 @@ int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void
  * a fixed order.  Where long sequences are cut into segments, a segment starts
  * from the rows before it up to where what is left of a state is 2^-25 of it:
  * the rest is below the state's last place (an infinity or NaN among those
- * rows goes no further either).  hT is the last row of y, bit for bit.  x, g in `dtype` and dx, dg in `grad_dtype` have strides
- * (elements from one row to the next, and from one sequence to the next), so
- * they may be the halves of one projection; y, dy [B, T, D], h0, hT, dhT, dh0
+ * rows goes no further either).  hT is the last row of y, bit for bit.
+ * x, g in `dtype` and dx, dg in `grad_dtype` have strides (elements from one row
+ * to the next, and from one sequence to the next), so they may be the halves of
+ * one projection; y, dy [B, T, D], h0, hT, dhT, dh0
  * [B, D] are contiguous float32. */
 typedef struct {
     int64_t B;              /* sequences, >= 0; B times D (rounded up to 64) at most 2^28 */

@@ -94,7 +94,8 @@ __device__ __forceinline__ void range_of(int r, int64_t& lo, int& width) {
 // Blocks past the ranges fill dE, `total` floats, with zeros.
 template <typename TI, bool STREAM>
 __global__ void __launch_bounds__(ES_T) embed_list_kernel(const TI* __restrict__ ids, int N, int64_t V,
-                                                          int2* __restrict__ list, int* __restrict__ start, int ranges, float* __restrict__ dE, int64_t total) {
+                                                          int2* __restrict__ list, int* __restrict__ start,
+                                                          int ranges, float* __restrict__ dE, int64_t total) {
     __shared__ int hist[ES_W][kEmbedWidth];
     __shared__ int sums[ES_W];
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -363,8 +364,8 @@ hipError_t bwd_t(const kan_embed_desc_t& d, const EmbedPlan& p, const void* dy, 
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.chunks == 1) return e;
     const unsigned jy = (unsigned)((d.D + 64 * VEC - 1) / (64 * VEC));
-    hipLaunchKernelGGL((embed_join_kernel<VEC>), dim3((unsigned)(p.chunks - 1), jy), dim3(64 * EJ_W), 0, s, d.V, d.D, p.chunk,
-                       list, start, d.scale, dE, part);
+    hipLaunchKernelGGL((embed_join_kernel<VEC>), dim3((unsigned)(p.chunks - 1), jy), dim3(64 * EJ_W), 0, s, d.V, d.D,
+                       p.chunk, list, start, d.scale, dE, part);
     return hipGetLastError();
 }
 
@@ -374,7 +375,8 @@ hipError_t list_t(const kan_embed_desc_t& d, const EmbedPlan& p, const void* ids
     const int64_t total = d.V * d.D, fill = (total + ES_T * EZ_V * 4 - 1) / (ES_T * EZ_V * 4);
     hipLaunchKernelGGL((embed_list_kernel<TI, STREAM>), dim3((unsigned)(p.ranges + fill)), dim3(ES_T), 0, s,
                        static_cast<const TI*>(ids), (int)d.N, d.V,
-                       reinterpret_cast<int2*>(ws + p.off_list), reinterpret_cast<int*>(ws + p.off_start), (int)p.ranges, dE, total);
+                       reinterpret_cast<int2*>(ws + p.off_list), reinterpret_cast<int*>(ws + p.off_start),
+                       (int)p.ranges, dE, total);
     return hipGetLastError();
 }
 // A large dE is filled past the caches (537 MB: 207 -> 180 us for the whole

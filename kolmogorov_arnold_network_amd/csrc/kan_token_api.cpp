@@ -190,7 +190,8 @@ RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
         const double most = n <= kCUs ? 1.0 : 1.4 * (double)((n + 2 * kCUs - 1) / (2 * kCUs));
         const double tiles = (double)((rows + tile - 1) / tile);
         const double traffic = (double)d.B * (double)T * (double)d.D / (128.0 * 64.0 * kCUs);
-        const double est = std::max(most * tiles, traffic) * lines(lanes) * (segs > 1 ? 1.1 : 1.0) + (segs > 1 ? 3.0 : 0.0);
+        const bool cut = segs > 1;
+        const double est = std::max(most * tiles, traffic) * lines(lanes) * (cut ? 1.1 : 1.0) + (cut ? 3.0 : 0.0);
         if (least >= 0.0 && est >= least) return;
         least = est;
         p.lanes = lanes;

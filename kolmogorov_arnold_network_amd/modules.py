@@ -279,7 +279,8 @@ class RecurFunction(torch.autograd.Function):
         D = p.shape[2] // 2
         dy = torch.zeros_like(y) if dy is None else dy.contiguous()
         dp = torch.empty(p.shape, dtype=p.dtype, device=p.device)
-        dh0 = F.kan_recur_backward(p[..., :D], p[..., D:], y, dy, h0, lengths, None if dhT is None else dhT.contiguous(),
+        dhT = None if dhT is None else dhT.contiguous()
+        dh0 = F.kan_recur_backward(p[..., :D], p[..., D:], y, dy, h0, lengths, dhT,
                                    need_dh0=ctx.needs_input_grad[1], dx=dp[..., :D], dg=dp[..., D:])[2]
         return dp, dh0, None
 
