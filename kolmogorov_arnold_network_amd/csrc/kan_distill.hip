@@ -6,11 +6,11 @@
 //
 // K is small beside V: reading z once and writing dz once is the work, so HBM
 // traffic bounds it; the arithmetic is one or two exponentials and about six
-// operations an element.  Measured: step of 8192 x 65536 float32 769 us (4.1 GB,
-// 5.3 TB/s), backward of 4096 x 50021 bf16 154 us (779 MB, 5.1 TB/s), forward of
-// 4096 x 50021 float32 128 us (820 MB read, 6.4 TB/s).  A row's maximum m and s = sum exp((z - m) / tau) are kept, not
-// their sum in lse: the loss is formed from z_{id} - m and log s, which are
-// small where lse and z / tau may be large.
+// operations an element.  Measured: step of 8192 x 65536 float32 755 us (4.1 GB,
+// 5.4 TB/s), backward of 4096 x 50021 bf16 157 us (784 MB, 5.0 TB/s), forward of
+// 4096 x 50021 float32 128 us (820 MB read, 6.4 TB/s).  A row's maximum m and
+// s = sum exp((z - m) / tau) are kept, not their sum in lse: the loss is formed
+// from z_{id} - m and log s, which are small where lse and z / tau may be large.
 //
 // A block takes a row.  In a step it holds the row in registers (up to 16
 // vectors of 16 bytes a thread, 256 KB for 1024 threads; what is left of a

@@ -28,9 +28,9 @@
 // launch composes every segment's run, from as many of its rows as still count
 // at its end, and the second starts each segment from the runs before it.
 //
-// Memory traffic bounds it: 8 x 4096 x 2048, bf16 forward 106 us (537 MB, 5.1
-// TB/s), float32 backward 314 us (1.61 GB, 5.1 TB/s), 1 x 65536 x 1024 float32
-// forward 152 us (805 MB, 5.3 TB/s), where a copy runs at 5.0 TB/s.  The
+// Memory traffic bounds it: 8 x 4096 x 2048, bf16 forward 104 us (537 MB, 5.2
+// TB/s), float32 backward 306 us (1.61 GB, 5.3 TB/s), 1 x 65536 x 1024 float32
+// forward 150 us (805 MB, 5.4 TB/s), where a copy runs at 5.0 TB/s.  The
 // arithmetic (two transcendentals and about 25 operations an element forward)
 // keeps the vector units busy for half of that.
 #include <type_traits>
