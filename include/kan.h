@@ -426,12 +426,13 @@ int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void
  *     dh0   = f_0 del_0 (dhT where len = 0)
  *
  * dx and dg are 0 from a sequence's length to T.  Runs of rows are composed in
- * the form h -> h + (b - U h), with U = 1 - prod f accumulated directly, so
- * that gates near 1 (long memories) lose no digits; all of it in float32, in
- * a fixed order.  Where long sequences are cut into segments, a segment starts
- * from the rows before it up to where what is left of a state is 2^-25 of it:
- * the rest is below the state's last place (an infinity or NaN among those
- * rows goes no further either).  hT is the last row of y, bit for bit.
+ * the form h -> L h + b, with L = prod f and 1 - L each accumulated to its own
+ * last places, so that neither long memories (L near 1) nor what is left of a
+ * large state (L near 0) lose digits; all of it in float32, in a fixed order.
+ * Where long sequences are cut into segments, a segment starts from the rows
+ * before it up to where 2^-64 is left of a state, and drops the rest (an
+ * infinity or NaN among those rows goes no further either).  hT is the last row
+ * of y, bit for bit.
  * x, g in `dtype` and dx, dg in `grad_dtype` have strides (elements from one row
  * to the next, and from one sequence to the next), so they may be the halves of
  * one projection; y, dy [B, T, D], h0, hT, dhT, dh0

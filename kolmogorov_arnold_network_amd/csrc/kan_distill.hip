@@ -6,7 +6,7 @@
 //
 // K is small beside V: reading z once and writing dz once is the work, so HBM
 // traffic bounds it; the arithmetic is one or two exponentials and about six
-// operations an element.  Measured: step of 8192 x 65536 float32 755 us (4.1 GB,
+// operations an element.  Measured: step of 8192 x 65536 float32 760 us (4.1 GB,
 // 5.4 TB/s), backward of 4096 x 50021 bf16 157 us (784 MB, 5.0 TB/s), forward of
 // 4096 x 50021 float32 128 us (820 MB read, 6.4 TB/s).  A row's maximum m and
 // s = sum exp((z - m) / tau) are kept, not their sum in lse: the loss is formed

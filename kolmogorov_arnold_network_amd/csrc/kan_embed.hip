@@ -13,7 +13,7 @@
 // mixed run at 5.
 //
 // Measured: lookup of 32768 x 2048 bf16 rows 31 us (5.7 TB/s); gradient of 32768
-// x 2048 float32 rows into 65536 183 us (805 MB, 4.4 TB/s: 98 us listing and
+// x 2048 float32 rows into 65536 185 us (805 MB, 4.4 TB/s: 98 us listing and
 // filling, 59 summing at 6 TB/s, 6 joining, the rest between launches).
 #include "kan_token.h"
 #include "kan_vec.h"

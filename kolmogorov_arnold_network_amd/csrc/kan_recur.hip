@@ -5,19 +5,21 @@
 //
 // its backward pass, and its single-row step on a pool of states.
 //
-// A step is taken from the side that the gate is near, by the smaller of the
-// two shares s = min(u, f): h + u (x - h) where f >= u, x + f (h - x) otherwise.
-// A share that rounds to 1 has lost the digits of the other one, which decide
-// how long a memory is (f near 1) or how much of a large state is left (u near
-// 1).  Backward, with c_t = f_t del_t the gradient that row t hands to row t - 1
-// (c_len = dhT), in the same way:
+// Backward, with c_t = f_t del_t the gradient that row t hands to row t - 1
+// (c_len = dhT):
 //
-//     del_t = dy_t + c_{t+1},  c_t = del_t - u_t del_t (f >= u), f_t del_t,
-//     dx_t = u_t del_t,  dg_t = f_t u_t (h_{t-1} - x_t) del_t,  dh0 = c_0.
+//     del_t = dy_t + c_{t+1},  dx_t = u_t del_t,
+//     dg_t  = f_t (h_{t-1} - x_t) dx_t,  dh0 = c_0.
 //
-// A run of steps is h -> h - U h + b with U = 1 - prod f, accumulated as the
-// share that is lost, and two runs compose to one (the earlier first):
-// U = U1 + U2 (1 - U1), b = b2 + b1 - U2 b1.  A block takes 16 to 128 channels
+// Both shares are computed to their own last places: a share that rounds to 1
+// has lost the digits of the other one, which decide how long a memory is (f
+// near 1) or how much of a large state is left (u near 1).  Where a state goes
+// on from tile to tile, or from call to call in the single step, it changes by
+// the smaller share alone, h + u (x - h) or x + f (h - x).
+//
+// A run of steps is h -> L h + b with L = prod f, kept like a gate: by the
+// smaller of L and U = 1 - L.  Two runs compose to one (the earlier first):
+// L = L1 L2, U = U1 + U2 L1, b = b2 + L2 b1.  A block takes 16 to 128 channels
 // of a sequence and walks along it in tiles, each read once: lanes hold four
 // channels of four consecutive rows in registers and compose them, the runs of
 // a wave's lanes and of the block's 8 waves are scanned, and every row's state
@@ -29,8 +31,9 @@
 // at its end, and the second starts each segment from the runs before it.
 //
 // Memory traffic bounds it: 8 x 4096 x 2048, bf16 forward 104 us (537 MB, 5.2
-// TB/s), float32 backward 306 us (1.61 GB, 5.3 TB/s), 1 x 65536 x 1024 float32
-// forward 150 us (805 MB, 5.4 TB/s), where a copy runs at 5.0 TB/s.  The
+// TB/s), float32 backward 316 us (1.61 GB, 5.1 TB/s), 1 x 65536 x 1024 float32
+// forward 162 us (805 MB, 5.0 TB/s: 13 for the segments' runs, 145 for the rows),
+// where a copy runs at 5.0 TB/s.  The
 // arithmetic (two transcendentals and about 25 operations an element forward)
 // keeps the vector units busy for half of that.
 #include <type_traits>
@@ -42,32 +45,38 @@ namespace kan {
 
 namespace {
 
-// The shares of x (u = sigmoid(-g)) and of the state (f = sigmoid(g)) as one
-// word: the smaller of the two, to a few ulp of its own size, with the sign bit
-// set where x's is the larger.
+// The shares of x and of the state, u = sigmoid(-g) and f = sigmoid(g), each to
+// a few ulp of its own size.
+struct Shares {
+    float u, f;
+    __device__ __forceinline__ static Shares of(float g) {
+        const float v = __expf(-fabsf(g)), most = __builtin_amdgcn_rcpf(1.0f + v), least = v * most;
+        return g < 0.0f ? Shares{most, least} : Shares{least, most};
+    }
+    __device__ __forceinline__ static Shares idle() { return Shares{0.0f, 1.0f}; }     // the state stays
+};
+
+// The same as one word: the smaller of the two, with the sign bit set where it
+// is f.  The larger one is 1 less it, and a state changes by it without the
+// rounding of the larger one, which would add up over a long memory.
 struct Gate {
     float e;
     __device__ __forceinline__ static Gate of(float g) {
         const float v = __expf(-fabsf(g));
-        Gate q;
-        q.e = __builtin_copysignf(v * __builtin_amdgcn_rcpf(1.0f + v), g);
-        return q;
+        return Gate{__builtin_copysignf(v * __builtin_amdgcn_rcpf(1.0f + v), g)};
     }
-    __device__ __forceinline__ static Gate idle() { return Gate{0.0f}; }   // the state stays
-    __device__ __forceinline__ float s() const { return fabsf(e); }
+    __device__ __forceinline__ static Gate idle() { return Gate{0.0f}; }
+    __device__ __forceinline__ static Gate of(Shares q) { return Gate{q.u < 0.5f ? q.u : -q.f}; }
     __device__ __forceinline__ bool keep() const { return (int)__float_as_uint(e) >= 0; }
-    __device__ __forceinline__ float u() const { return keep() ? e : 1.0f + e; }
+    __device__ __forceinline__ Shares shares() const {
+        return Shares{keep() ? e : 1.0f + e, keep() ? 1.0f - e : -e};
+    }
     __device__ __forceinline__ float step(float h, float x) const {
         const float a = keep() ? h : x, b = keep() ? x : h;
-        return __builtin_fmaf(s(), b - a, a);
+        return __builtin_fmaf(fabsf(e), b - a, a);
     }
-    __device__ __forceinline__ float back(float del) const {
-        return __builtin_fmaf(-e, del, keep() ? del : 0.0f);
-    }
-    // 1 - (1 - U) f: the share of a run's start that is lost after this step too
-    __device__ __forceinline__ float lost(float U) const {
-        return __builtin_fmaf(e, 1.0f - U, keep() ? U : 1.0f);
-    }
+    // what is left of h: f h
+    __device__ __forceinline__ float of_state(float h) const { return __builtin_fmaf(-e, h, keep() ? h : 0.0f); }
 };
 
 __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, int64_t T) {
@@ -104,90 +113,114 @@ struct Place {
     }
 };
 
-// A run (U, b) of VEC channels.
-template <int VEC>
+// Runs of N channels, h -> L h + b: U and L of a channel as a gate's u and f.
+template <int N>
 struct Run {
-    float U[VEC], b[VEC];
-    __device__ __forceinline__ void clear() {
+    float e[N], b[N];
+    __device__ __forceinline__ void apply(float (&h)[N]) const {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) U[i] = b[i] = 0.0f;
-    }
-    // the run of `before`, then this one
-    __device__ __forceinline__ void after(const Run& before) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            b[i] += __builtin_fmaf(-U[i], before.b[i], before.b[i]);
-            U[i] = __builtin_fmaf(U[i], 1.0f - before.U[i], before.U[i]);
-        }
-    }
-    __device__ __forceinline__ void apply(float (&h)[VEC]) const {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) h[i] = __builtin_fmaf(-U[i], h[i], h[i]) + b[i];
+        for (int i = 0; i < N; ++i) h[i] = Gate{e[i]}.of_state(h[i]) + b[i];
     }
 };
 
-// Scan of the block's runs, in row order (forward) or against it (BACK).
-// `run` is a lane's own; h, the state at the tile's start, becomes the state
-// at its end, and `mine` the state at the start of the lane's rows.
+// The same while runs are composed.  A tile's rows add to b by f and L as they
+// are rounded: that moves a contribution by some last places once, as the
+// state goes on from tile to tile by Run::apply.
+template <int N>
+struct Rows {
+    float U[N], L[N], b[N];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) U[i] = b[i] = 0.0f, L[i] = 1.0f;
+    }
+    __device__ __forceinline__ void step(int i, Shares q, float x) {
+        b[i] = __builtin_fmaf(q.f, b[i], q.u * x);
+        then(i, q);
+    }
+    __device__ __forceinline__ void back(int i, Shares q, float d) {
+        b[i] = q.f * (d + b[i]);
+        then(i, q);
+    }
+    // the rows of `before`, then these
+    __device__ __forceinline__ void after(const Rows& before) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            b[i] = __builtin_fmaf(L[i], before.b[i], b[i]);
+            U[i] = __builtin_fmaf(U[i], before.L[i], before.U[i]);
+            L[i] *= before.L[i];
+        }
+    }
+    __device__ __forceinline__ Run<N> run() const {
+        Run<N> o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.e[i] = Gate::of(Shares{U[i], L[i]}).e, o.b[i] = b[i];
+        return o;
+    }
+
+private:
+    __device__ __forceinline__ void then(int i, Shares q) {
+        U[i] = __builtin_fmaf(q.u, L[i], U[i]);
+        L[i] *= q.f;
+    }
+};
+
+// v of the lane k before this one in the order of the scan
+template <bool BACK>
+__device__ __forceinline__ float earlier(float v, int k) {
+    return BACK ? __shfl_down(v, k, 64) : __shfl_up(v, k, 64);
+}
+
+// Composes a wave's lanes, in row order (forward) or against it (BACK): the
+// runs up to and with each lane.
 template <int VEC, int RC, bool BACK>
-__device__ __forceinline__ void scan_tile(Run<VEC> run, float (&h)[VEC], float (&mine)[VEC], int cl, int tl, int w,
-                                          int waves, Run<VEC> (*tot)[RC]) {
+__device__ __forceinline__ void scan_wave(Rows<VEC>& rows, const Place<VEC, RC>& at) {
     constexpr int RL = 64 / RC;
-    const int at = BACK ? RL - 1 - tl : tl;            // place in the order of the scan
+    const int place = BACK ? RL - 1 - at.tl : at.tl;
 #pragma unroll
     for (int k = 1; k < RL; k *= 2) {
-        Run<VEC> o;
+        Rows<VEC> o;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            o.U[i] = BACK ? __shfl_down(run.U[i], k * RC, 64) : __shfl_up(run.U[i], k * RC, 64);
-            o.b[i] = BACK ? __shfl_down(run.b[i], k * RC, 64) : __shfl_up(run.b[i], k * RC, 64);
+            o.U[i] = earlier<BACK>(rows.U[i], k * RC);
+            o.L[i] = earlier<BACK>(rows.L[i], k * RC);
+            o.b[i] = earlier<BACK>(rows.b[i], k * RC);
         }
-        if (at >= k) run.after(o);
+        if (place >= k) rows.after(o);
     }
-    if (at == RL - 1) tot[w][cl] = run;
+}
+
+// Scan of the block's runs: h, the state at the tile's start, becomes the state
+// at its end, and `mine` the state at the start of the lane's rows.
+template <int VEC, int RC, bool BACK>
+__device__ __forceinline__ void scan_tile(Rows<VEC> rows, float (&h)[VEC], float (&mine)[VEC],
+                                          const Place<VEC, RC>& at, Run<VEC> (*tot)[RC]) {
+    constexpr int RL = 64 / RC;
+    scan_wave<VEC, RC, BACK>(rows, at);
+    const Run<VEC> run = rows.run();
+    if (at.tl == (BACK ? 0 : RL - 1)) tot[at.w][at.cl] = run;
     Run<VEC> o;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        o.U[i] = BACK ? __shfl_down(run.U[i], RC, 64) : __shfl_up(run.U[i], RC, 64);
-        o.b[i] = BACK ? __shfl_down(run.b[i], RC, 64) : __shfl_up(run.b[i], RC, 64);
+        o.e[i] = earlier<BACK>(run.e[i], RC);
+        o.b[i] = earlier<BACK>(run.b[i], RC);
     }
-    if (at == 0) o.clear();
-    __syncthreads();
-    for (int k = 0; k < waves; ++k) {
-        const int q = BACK ? waves - 1 - k : k;
-        if (q == w) {
+    if (at.tl == (BACK ? RL - 1 : 0)) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) mine[i] = h[i];
-        }
-        tot[q][cl].apply(h);
+        for (int i = 0; i < VEC; ++i) o.e[i] = o.b[i] = 0.0f;
     }
+    __syncthreads();
+    auto wave = [&](int k) {
+        const int q = BACK ? at.waves - 1 - k : k;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) mine[i] = k == 0 || q == at.w ? h[i] : mine[i];
+        tot[q][at.cl].apply(h);
+    };
+    if (at.waves == RW)
+#pragma unroll
+        for (int k = 0; k < RW; ++k) wave(k);
+    else
+        for (int k = 0; k < at.waves; ++k) wave(k);
     o.apply(mine);
-}
-
-// The composition of all of the block's runs of a tile, in every lane.
-template <int VEC, int RC, bool BACK>
-__device__ __forceinline__ void block_run(Run<VEC> run, Run<VEC>& out, int cl, int tl, int w, int waves,
-                                          Run<VEC> (*tot)[RC]) {
-    constexpr int RL = 64 / RC;
-    const int at = BACK ? RL - 1 - tl : tl;
-#pragma unroll
-    for (int k = 1; k < RL; k *= 2) {
-        Run<VEC> o;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            o.U[i] = BACK ? __shfl_down(run.U[i], k * RC, 64) : __shfl_up(run.U[i], k * RC, 64);
-            o.b[i] = BACK ? __shfl_down(run.b[i], k * RC, 64) : __shfl_up(run.b[i], k * RC, 64);
-        }
-        if (at >= k) run.after(o);
-    }
-    if (at == RL - 1) tot[w][cl] = run;
-    __syncthreads();
-    out.clear();
-    for (int k = 0; k < waves; ++k) {
-        Run<VEC> o = tot[BACK ? waves - 1 - k : k][cl];
-        o.after(out);
-        out = o;
-    }
 }
 
 // Element i of a row pointer's vector at row t.
@@ -199,43 +232,49 @@ __device__ __forceinline__ Raw<TS, VEC> row_at(const TS* p, int64_t t, int64_t s
 // h after the runs of the segments before this one (after it, BACK), from the
 // launch that composed them: each of the block's runs of lanes composes a
 // share of them, and the shares are scanned like a tile's.
-template <int VEC, int RC, bool BACK, typename P>
-__device__ __forceinline__ void from_segments(const RecurPlan& p, const P& at, int64_t D, const float* runs,
-                                              float (&h)[VEC], Run<VEC> (*tot)[RC]) {
+template <int VEC, int RC, bool BACK>
+__device__ __forceinline__ void from_segments(const RecurPlan& p, const Place<VEC, RC>& at, int64_t D,
+                                              const float* runs, float (&h)[VEC],
+                                              Run<VEC> (*tot)[RC]) {
     const int groups = at.waves * (64 / RC), g = at.w * (64 / RC) + at.tl;
     const int n = BACK ? p.segs - 1 - at.seg : at.seg, each = (n + groups - 1) / groups;
     const int k0 = (BACK ? groups - 1 - g : g) * each, k1 = min(k0 + each, n);
-    Run<VEC> run;
-    run.clear();
+    Rows<VEC> rows;
+    rows.clear();
     for (int k = k0; k < k1; ++k) {
         const float* r = runs + ((at.b * p.segs + (BACK ? p.segs - 1 - k : k)) * 2) * D + at.c;
-        const Raw<float, VEC> U = load_raw<float, VEC>(r), bb = load_raw<float, VEC>(r + D);
-        Run<VEC> one;
+        const Raw<float, VEC> e = load_raw<float, VEC>(r), bb = load_raw<float, VEC>(r + D);
+        Rows<VEC> one;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) one.U[i] = raw_value(U, i), one.b[i] = raw_value(bb, i);
-        one.after(run);
-        run = one;
+        for (int i = 0; i < VEC; ++i) {
+            const Shares q = Gate{raw_value(e, i)}.shares();
+            one.U[i] = q.u, one.L[i] = q.f, one.b[i] = raw_value(bb, i);
+        }
+        one.after(rows);
+        rows = one;
     }
     float mine[VEC];
-    scan_tile<VEC, RC, BACK>(run, h, mine, at.cl, at.tl, at.w, at.waves, tot);
-}
-template <int VEC, typename P>
-__device__ __forceinline__ void store_run(const RecurPlan& p, const P& at, int64_t D, float* runs,
-                                          const Run<VEC>& run) {
-    float* r = runs + ((at.b * p.segs + at.seg) * 2) * D + at.c;
-    store_vec<VEC>(r, run.U);
-    store_vec<VEC>(r + D, run.b);
+    scan_tile<VEC, RC, BACK>(rows, h, mine, at, tot);
 }
 
+// Rows' loads are waited for here, not where they are used.
+template <typename TS, int VEC, int N>
+__device__ __forceinline__ void arrived(Raw<TS, VEC> (&rows)[N]) {
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+#pragma unroll
+        for (uint32_t& w : rows[r].w) asm volatile("" : "+v"(w));
+}
 template <int VEC>
-__device__ __forceinline__ void load_state(const float* h0, int64_t b, int64_t D, int64_t c, float (&h)[VEC]) {
-    if (h0) {
-        const Raw<float, VEC> r = load_raw<float, VEC>(h0 + b * D + c);
+__device__ __forceinline__ void load_state(const float* from, int64_t at, float (&h)[VEC]) {
+    Raw<float, VEC> r;
+    if (from) r = load_raw<float, VEC>(from + at);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) h[i] = raw_value(r, i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) h[i] = 0.0f;
+    for (int i = 0; i < VEC; ++i) {
+        h[i] = from ? raw_value(r, i) : 0.0f;
+        // has arrived here: a wait where the tiles' loop uses it would, in every
+        // tile, be one for the next tile's loads
+        asm volatile("" : "+v"(h[i]));
     }
 }
 
@@ -244,15 +283,18 @@ constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 // The runs of the segments, for the launch that starts each segment from them:
 // of h from x and g, or (BACK) of c from dy and g.  A segment's run is composed
 // from the end that counts most, the one where it hands its state on, and ends
-// where the share that is left of what comes before is at most 2^-25 in every
-// channel of the block: the rest of the segment would change the state by less
-// than its last place.  Common gates forget in a tile or two (128 rows by 64
-// channels); gates that do not are read to the segment's start.
+// where the share that is left of what comes before is at most 2^-64 in every
+// channel of the block: less than half a last place of what follows, unless the
+// state that is dropped was 2^40 times as large.  (2^-25 is half a last place of
+// a state of the same size, and 7 us of the 162 less; but what is left of one
+// large input would then end at a segment's start.)  Common gates forget in a
+// tile or two (128 rows by 64 channels); gates that do not are read to the
+// segment's start.
 template <typename TS, typename TV, int VEC, int RC, bool BACK>
 __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d, RecurPlan p, const TS* g, const TV* v,
                                                              int64_t v_row, int64_t v_seq, const int32_t* lengths,
                                                              float* runs) {
-    __shared__ Run<VEC> tot[2][RW][RC];
+    __shared__ Rows<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
     const Place<VEC, RC> at(d, p, lengths);
     g += at.b * d.g_seq + at.c;
@@ -270,51 +312,47 @@ __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d,
         }
     };
     auto start = [&](int64_t k) { return at.r0 + (BACK ? k : tiles - 1 - k) * tile; };
-    Run<VEC> all;
+    Rows<VEC> all;
     all.clear();
-    float left[VEC];                                   // 1 - all.U, with the digits of small values
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) left[i] = 1.0f;
     for (int64_t k = 0; k < tiles; ++k) {
         const int64_t t = start(k) + first;
         load(start(k));
-        Run<VEC> run, whole;
-        run.clear();
+        Rows<VEC> rows;
+        rows.clear();
 #pragma unroll
         for (int j = 0; j < RF; ++j) {
             const int r = BACK ? RF - 1 - j : j;
             const bool in = t + r < inside;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const Gate e = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
+                const Shares q = in ? Shares::of(raw_value(gr[r], i)) : Shares::idle();
                 const float x = in ? raw_value(vr[r], i) : 0.0f;
-                run.b[i] = BACK ? e.back(x + run.b[i]) : e.step(run.b[i], x);
-                run.U[i] = e.lost(run.U[i]);
+                BACK ? rows.back(i, q, x) : rows.step(i, q, x);
             }
         }
-        block_run<VEC, RC, BACK>(run, whole, at.cl, at.tl, at.w, at.waves, tot[k & 1]);
+        scan_wave<VEC, RC, BACK>(rows, at);
+        if (at.tl == (BACK ? 0 : RL - 1)) tot[k & 1][at.w][at.cl] = rows;
+        __syncthreads();
+        for (int q = 0; q < at.waves; ++q) all.after(tot[k & 1][BACK ? q : at.waves - 1 - q][at.cl]);
         bool done = true;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            all.b[i] = __builtin_fmaf(left[i], whole.b[i], all.b[i]);
-            all.U[i] = __builtin_fmaf(all.U[i], 1.0f - whole.U[i], whole.U[i]);
-            left[i] *= 1.0f - whole.U[i];
-            done = done && left[i] <= 0x1p-25f;
-        }
+        for (int i = 0; i < VEC; ++i) done = done && all.L[i] <= 0x1p-64f;
         // a wave has all of the block's channels and the same runs of them as
         // every other wave: they leave together
         if (__all(done)) break;
     }
     if (at.w != 0 || at.tl != 0) return;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        if (left[i] < 0.5f) all.U[i] = 1.0f - left[i];
-    store_run<VEC>(p, at, d.D, runs, all);
+    const Run<VEC> run = all.run();
+    runs += (at.b * p.segs + at.seg) * 2 * d.D + at.c;
+    store_vec<VEC>(runs, run.e);
+    store_vec<VEC>(runs + d.D, run.b);
 }
 
-// Forward.
+// Forward.  Two blocks to a compute unit (at most 128 registers): 32 x 700 x 770
+// float32 47.0 -> 45.5 us, 64 x 300 x 768 39.9 -> 38.1, 4 x 1000 x 512 12.1 ->
+// 12.8.
 template <typename TS, int VEC, int RC, bool STREAM>
-__global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
+__global__ void __launch_bounds__(64 * RW, 4) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
                                                             const float* runs) {
     __shared__ Run<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
@@ -324,88 +362,91 @@ __global__ void __launch_bounds__(64 * RW) recur_fwd_kernel(kan_recur_desc_t d, 
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
     float* y = a.out + at.b * d.T * D + at.c;
     float h[VEC];
-    load_state<VEC>(a.h0, at.b, D, at.c, h);
+    load_state<VEC>(a.h0, at.b * D + at.c, h);
     if (p.segs > 1) from_segments<VEC, RC, false>(p, at, D, runs, h, tot[1]);
     const int tile = at.waves * RL * RF, first = (at.w * RL + at.tl) * RF;
     const int64_t inside = min(at.len, at.r1);
     Raw<TS, VEC> xr[RF], gr[RF];
-    auto load = [&](int64_t t0) {
-        const int64_t t = t0 + first;
-        if (t0 + tile <= inside) {                     // uniform
+    auto load = [&](int64_t t0, auto checked) {
 #pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                gr[r] = row_at<TS, VEC>(g, t + r, d.g_row);
-                xr[r] = row_at<TS, VEC>(x, t + r, d.x_row);
-            }
-        } else {
+        for (int r = 0; r < RF; ++r) {
+            const int64_t t = t0 + first + r, q = checked.value ? min(t, at.len - 1) : t;
+            gr[r] = row_at<TS, VEC>(g, q, d.g_row);
+            xr[r] = row_at<TS, VEC>(x, q, d.x_row);
+        }
+    };
+    // h from 0 at the lane's first row; from the state before it, a row's is this
+    // and what is left of that state
+    Rows<VEC> rows;
+    float f[RF][VEC], own[RF][VEC], start[VEC];
+    auto compose = [&](int64_t t, auto checked) {
+        rows.clear();
 #pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                const int64_t q = min(t + r, at.len - 1);
-                gr[r] = row_at<TS, VEC>(g, q, d.g_row);
-                xr[r] = row_at<TS, VEC>(x, q, d.x_row);
+        for (int r = 0; r < RF; ++r) {
+            const bool in = !checked.value || t + r < inside;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const Shares q = in ? Shares::of(raw_value(gr[r], i)) : Shares::idle();
+                rows.step(i, q, in ? raw_value(xr[r], i) : 0.0f);
+                f[r][i] = q.f;
+                own[r][i] = rows.b[i];
             }
         }
     };
-    if (at.r0 < inside) load(at.r0);
+    auto row = [&](int r, float (&o)[VEC]) {           // rows in order
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            start[i] *= f[r][i];
+            o[i] = start[i] + own[r][i];
+        }
+    };
+    int64_t t0 = at.r0;
     int parity = 0;
-    for (int64_t t0 = at.r0; t0 < at.r1; t0 += tile, parity ^= 1) {
+    bool ready = t0 + tile <= inside;
+    if (ready) {
+        load(t0, std::false_type());
+        arrived(gr), arrived(xr);
+    }
+    // The whole tiles that another one follows.  The next one's loads have the
+    // time of the scan, the stores that of the next tile up to its scan's end:
+    // were the loads waited for after the stores are issued, the wait would be
+    // one for the stores too.
+    for (; t0 + 2 * tile <= inside; t0 += tile, parity ^= 1) {
+        compose(t0 + first, std::false_type());
+        __builtin_amdgcn_sched_barrier(0);
+        load(t0 + tile, std::false_type());
+        scan_tile<VEC, RC, false>(rows, h, start, at, tot[parity]);
+        arrived(gr), arrived(xr);
+#pragma unroll
+        for (int r = 0; r < RF; ++r) {
+            float o[VEC];
+            row(r, o);
+            store_vec<VEC, STREAM>(y + (t0 + first + r) * D, o);
+        }
+    }
+    for (; t0 < inside; t0 += tile, parity ^= 1, ready = false) {      // the last ones
         const int64_t t = t0 + first;
-        if (t0 >= at.len) {                            // uniform: rows past the length
-            const float zero[VEC] = {};
+        if (!ready) load(t0, std::true_type());
+        compose(t, std::true_type());
+        scan_tile<VEC, RC, false>(rows, h, start, at, tot[parity]);
 #pragma unroll
-            for (int r = 0; r < RF; ++r)
-                if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, zero);
-            continue;
-        }
-        const bool whole = t0 + tile <= inside;        // uniform
-        // U and b of the lane's rows up to each row: from them a row's state is
-        // two operations once the state before the lane's rows is known
-        Run<VEC> run, upto[RF];
-        run.clear();
-        auto compose = [&](auto checked) {
+        for (int r = 0; r < RF; ++r) {
+            float o[VEC];
+            row(r, o);
+            if (a.hT && t + r == at.len - 1) store_vec<VEC>(a.hT + at.b * D + at.c, o);     // the bits of y
 #pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                const bool in = !checked.value || (t + r < at.len && t + r < at.r1);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const Gate e = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
-                    run.b[i] = e.step(run.b[i], in ? raw_value(xr[r], i) : 0.0f);
-                    run.U[i] = e.lost(run.U[i]);
-                }
-                upto[r] = run;
-            }
-        };
-        if (whole) compose(std::false_type());
-        else compose(std::true_type());
-        if (t0 + tile < inside) load(t0 + tile);       // arrives during the scan and the stores
-        float s[VEC];
-        scan_tile<VEC, RC, false>(run, h, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
-        if (whole && t0 + tile < at.len) {
-#pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                float o[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = s[i];
-                upto[r].apply(o);
-                store_vec<VEC, STREAM>(y + (t + r) * D, o);
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < RF; ++r) {
-                float o[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = s[i];
-                upto[r].apply(o);
-                if (a.hT && t + r == at.len - 1) store_vec<VEC>(a.hT + at.b * D + at.c, o);     // the bits of y
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? o[i] : 0.0f;
-                if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, o);
-            }
+            for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? o[i] : 0.0f;
+            if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, o);
         }
     }
-    if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
+    for (; t0 < at.r1; t0 += tile) {                   // rows past the length
+        const float zero[VEC] = {};
+#pragma unroll
+        for (int r = 0; r < RF; ++r)
+            if (t0 + first + r < at.r1) store_vec<VEC, STREAM>(y + (t0 + first + r) * D, zero);
+    }
+    if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0)
         store_vec<VEC>(a.hT + at.b * D + at.c, h);     // h0
-    }
 }
 
 // Backward: the same, from the last row of a segment to its first.
@@ -423,10 +464,9 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
     const bool grads = a.dx;
     TG* dx = grads ? static_cast<TG*>(a.dx) + at.b * d.dx_seq + at.c : nullptr;
     TG* dg = grads ? static_cast<TG*>(a.dg) + at.b * d.dg_seq + at.c : nullptr;
-    float c[VEC], h0[VEC];
-    load_state<VEC>(a.dhT, at.b, D, at.c, c);
+    float c[VEC];
+    load_state<VEC>(a.dhT, at.b * D + at.c, c);
     if (p.segs > 1) from_segments<VEC, RC, true>(p, at, D, runs, c, tot[1]);
-    load_state<VEC>(a.h0, at.b, D, at.c, h0);
     const int tile = at.waves * RL * RB, first = (at.w * RL + at.tl) * RB;
     int parity = 0;
     const int64_t tiles = (at.r1 - at.r0 + tile - 1) / tile;
@@ -443,6 +483,8 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
                 }
             continue;
         }
+        Rows<VEC> rows;
+        rows.clear();
         Gate e[RB][VEC];
         float dv[RB][VEC], diff[RB][VEC];              // dy; h_{t-1} - x_t
         const bool whole = t0 > 0 && t0 + tile <= min(at.len, at.r1);    // uniform
@@ -460,14 +502,16 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
                 }
             }
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
+            for (int r = RB - 1; r >= 0; --r) {
                 const bool in = !checked.value || (t + r < at.len && t + r < at.r1);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     e[r][i] = in ? Gate::of(raw_value(gr[r], i)) : Gate::idle();
                     dv[r][i] = in ? raw_value(dr[r], i) : 0.0f;
                     if (grads) {
-                        const float before = checked.value && t + r == 0 ? h0[i] : raw_value(yr[r], i);
+                        const float before = !checked.value || t + r > 0 ? raw_value(yr[r], i)
+                                             : a.h0                      ? a.h0[at.b * D + at.c + i]
+                                                                         : 0.0f;
                         diff[r][i] = in ? before - raw_value(xr[r], i) : 0.0f;
                     }
                 }
@@ -475,17 +519,12 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
         };
         if (whole) load(std::false_type());
         else load(std::true_type());
-        Run<VEC> run;
-        run.clear();
 #pragma unroll
         for (int r = RB - 1; r >= 0; --r)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                run.b[i] = e[r][i].back(dv[r][i] + run.b[i]);
-                run.U[i] = e[r][i].lost(run.U[i]);
-            }
+            for (int i = 0; i < VEC; ++i) rows.back(i, e[r][i].shares(), dv[r][i]);
         float s[VEC];
-        scan_tile<VEC, RC, true>(run, c, s, at.cl, at.tl, at.w, at.waves, tot[parity]);
+        scan_tile<VEC, RC, true>(rows, c, s, at, tot[parity]);
         parity ^= 1;
         if (!grads) continue;
 #pragma unroll
@@ -493,10 +532,11 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
             float ox[VEC], og[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float del = dv[r][i] + s[i], sh = e[r][i].s();
-                ox[i] = e[r][i].u() * del;
-                og[i] = sh * (1.0f - sh) * diff[r][i] * del;
-                s[i] = e[r][i].back(del);
+                const Shares q = e[r][i].shares();
+                const float del = dv[r][i] + s[i];
+                ox[i] = q.u * del;
+                og[i] = q.f * diff[r][i] * ox[i];
+                s[i] = q.f * del;
             }
             if (t + r < at.r1) {
                 if (t + r >= at.len)
@@ -507,9 +547,7 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
             }
         }
     }
-    if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
-        store_vec<VEC>(a.dh0 + at.b * D + at.c, c);
-    }
+    if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) store_vec<VEC>(a.dh0 + at.b * D + at.c, c);
 }
 
 // One row of each sequence.  Slots differ, so no two threads share a state

@@ -153,7 +153,7 @@ RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
     // forward: 106 us with 16 lanes, 126 with 8; 70 x 1531 x 770 bf16 backward:
     // 461 with 32, 529 with 16, 364 with 16 at 768 channels).  Segments read a
     // little twice and take a launch more (1 x 65536 x 1024 float32 forward:
-    // 644 us whole, 152 in segments).
+    // 644 us whole, 162 in segments).
     constexpr int64_t kCUs = 256;
     const bool forward = pass == KAN_PASS_FORWARD;
     RecurPlan p;

@@ -200,6 +200,45 @@ def test_long_memories_keep_their_digits(env):
     assert np.abs(y.double().cpu().numpy() - want[None, :, None]).max() <= tol
 
 
+@pytest.mark.parametrize("B,T,D", [(2, 300, 36), (1, 3000, 8), (1, 5000, 3), (3, 700, 130)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_states_are_forgotten_exactly(env, B, T, D, dtype):
+    """Single inputs and gradients of 3e7 among values around 1: what is left of
+    them n rows on is a product of n shares, each within 24 e and rounded in at
+    most 4 e more, so a row is within (28 T + 64) e of the sum of its
+    contributions' sizes, whatever the largest value of the sequence.  What lies
+    in earlier segments may be dropped once 2^-64 of it is left.  dg has three
+    such factors."""
+    torch, F = env
+    x, g = _draw(torch, B, T, D, dtype, "apart", B + 3 * T + D, gate=(0.0, 1.5))
+    dy = torch.randn(B, T, D, device="cuda:0")
+    x[:, 40::97] = 3e7
+    dy[:, 60::97] = -3e7
+    h0 = torch.randn(B, D, device="cuda:0") * 3e7
+    dhT = torch.randn(B, D, device="cuda:0") * 3e7
+    y, hT = F.kan_recur_forward(x, g, h0)
+    dx, dg, dh0 = F.kan_recur_backward(x, g, y, dy, h0, dhT=dhT)
+    ax, ag, ad, ah, at = _np(x), _np(g), _np(dy), _np(h0), _np(dhT)
+    wy, wh = O.recur_forward(ax, ag, ah)
+    wdx, wdg, wdh = O.recur_backward(ax, ag, ad, ah, dhT=at)
+    sy, sh = O.recur_forward(np.abs(ax), ag, np.abs(ah))
+    sdx, _, sdh = O.recur_backward(ax, ag, np.abs(ad), ah, dhT=np.abs(at))
+    f = O.sigmoid(ag.astype(np.float64))
+    before = np.concatenate([np.abs(ah)[:, None], sy[:, :-1]], 1)
+    sdg = f * sdx * (before + np.abs(ax))
+    r = (28 * T + 64) * EPS
+
+    def close(got, want, size, k=1):
+        err = np.abs(got.double().cpu().numpy() - want)
+        assert (err <= k * r * size + 2.0 ** -64 * size.max()).all()
+
+    close(y, wy, sy)
+    close(hT, wh, sh)
+    close(dx, wdx, sdx)
+    close(dh0, wdh, sdh)
+    close(dg, wdg, sdg, 3)
+
+
 def test_broadcast_inputs(env):
     """Stride 0: one gate for all rows and sequences."""
     torch, F = env
