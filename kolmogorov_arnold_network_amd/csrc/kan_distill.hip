@@ -19,6 +19,12 @@
 // maximum and sum.  The teacher's part is done while the row's loads are in
 // flight.  The step's stores are plain: streamed ones gained 2% at 8192 x 65536
 // and lost 4% at 4096 x 50021.
+//
+// The teacher's p are taken off at K of the row's elements.  Every element is
+// stored by one thread, which stores it a second time where a teacher's entry
+// has it: a store of another thread after a barrier may land before the first
+// one, since a barrier waits for LDS but not for stores in flight.
+#include "kan_distill_rows.h"
 #include "kan_token.h"
 #include "kan_vec.h"
 
@@ -61,12 +67,22 @@ __device__ __forceinline__ void block_sum2(float& a, float& b, float* slots) {
 
 // LDS of a row's teacher: ids (-1: absent) and p of its entries, and a table of
 // the ids that occur, twice as large as a block has entries: the id of a slot,
-// how many entries have it, and the first of them.
+// how many entries have it, and the first of them.  Then, for each thread, the
+// entries whose elements it stores: the first one (-1: none), the one after
+// entry k, and its gradient.  The latter two take the table's ids' place.
 template <int NT>
 struct TeacherShared {
     int ids[NT];
     float ps[NT];
-    int key[2 * NT], count[2 * NT], first[2 * NT];
+    union {
+        int key[2 * NT];
+        struct {
+            int next[NT];
+            float value[NT];
+        };
+    };
+    int count[2 * NT], first[2 * NT];
+    int given[NT];
     float slots[3 * (NT / 64)];
 };
 
@@ -102,6 +118,7 @@ struct Teacher {
         sh.ids[threadIdx.x] = id;
         sh.ps[threadIdx.x] = p;
         if (TABLE) {
+            sh.given[threadIdx.x] = -1;
 #pragma unroll
             for (int i = threadIdx.x; i < 2 * NT; i += NT) sh.key[i] = -1, sh.count[i] = 0, sh.first[i] = NT;
         }
@@ -132,10 +149,23 @@ struct Teacher {
             id = -1;
         }
     }
+    // After join_equal: this entry's element, whose gradient is `value`, to the
+    // thread that stores the element.
+    __device__ __forceinline__ void give(TeacherShared<NT>& sh, int owner, float value) {
+        sh.value[threadIdx.x] = value;
+        sh.next[threadIdx.x] = atomicExch(&sh.given[owner], (int)threadIdx.x);
+    }
 };
 
 __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put1(uint16_t* p, float v) { *p = f2bf(v); }
+
+// What this thread was given, a barrier after the block's last `give`: over its
+// own earlier stores.  The elements of a list differ, so its order is free.
+template <typename TG, int NT>
+__device__ __forceinline__ void put_given(TG* dz, const TeacherShared<NT>& sh) {
+    for (int k = sh.given[threadIdx.x]; k >= 0; k = sh.next[k]) put1(dz + sh.ids[k], sh.value[k]);
+}
 
 template <typename TS, int N>
 __device__ __forceinline__ float max_of(const Raw<TS, N>& r) {
@@ -146,17 +176,6 @@ __device__ __forceinline__ float max_of(const Raw<TS, N>& r) {
 }
 
 constexpr int VE = 4;             // elements of a vector (backward between bf16 arrays: 8)
-
-// A row is a head of single elements up to the first cache line of what is
-// written (of z, where nothing is), vectors, and a tail of fewer elements than
-// a vector.  Rows of an odd length start anywhere; lines cut between lanes and
-// waves cost 20% of a step with 50021 bf16 logits (241 us against 204 at 50024).
-// Thread i takes element i of the head and of the tail.
-template <typename T>
-__device__ __forceinline__ int head_of(const T* p, int64_t V) {
-    const int n = (int)((128 - (reinterpret_cast<uintptr_t>(p) & 127)) & 127) / (int)sizeof(T);
-    return (int)min((int64_t)n, V);
-}
 
 // All of a row's gradient, or of its elements [v0, v1), zero.
 template <typename TG, int NT>
@@ -279,6 +298,7 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
         return;
     }
     const float f = w * d.tau, fs = f / s;
+    if (te.id >= 0) te.give(sh, owner_of(te.id, head, V, VE, NT), fs * exp2_raw((zk - m0) * c) - f * te.p);
     if ((int)threadIdx.x < head) put1(dz + threadIdx.x, fs * hz);
     if (tail < V) put1(dz + tail, fs * tz);
     if (NV) {
@@ -311,24 +331,9 @@ __global__ void __launch_bounds__(NT) distill_row_kernel(kan_distill_desc_t d, D
             store_vec<VE>(dz + v + u * STRIDE, o);
         }
     }
-    // the teacher's entries again, now with their p taken off
     __syncthreads();
-    if (te.id >= 0) put1(dz + te.id, fs * exp2_raw((zk - m0) * c) - f * te.p);
+    put_given<TG, NT>(dz, sh);
 }
-
-// Part p of a row that is cut for several blocks: elements [v0, v1), the first
-// part with the head, vectors from v, and the part that ends the row with the
-// tail, `tail` on.  Parts are `part` elements of vectors; with a head the last
-// one may be empty (v0 = v1).
-struct Part {
-    int64_t v0, v1, v, tail;
-    __device__ __forceinline__ Part(int p, int64_t part, int head, int64_t V, int VE) {
-        v = head + p * part;
-        v0 = p ? min(v, V) : 0;
-        v1 = min(v + part, V);
-        tail = v0 < V && v1 == V ? V - (V - head) % VE : V;
-    }
-};
 
 // Maximum and sum of exp((z - max) / tau) of part p of a row, for a step of few
 // long rows: out[row][p].
@@ -426,11 +431,14 @@ __global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, D
         block_sum2<NT>(l, none, slots);
         if (threadIdx.x == 0) a.loss[row] = w * d.tau * d.tau * (l - logf(te.sum) + logf(s));
     }
+    const bool here = te.id >= at.v0 && te.id < at.v1;
+    const float zk = here ? load_f(z, te.id) : 0.0f;
     te.join_equal(d, sh);
     const float f = w * d.tau * (STEP ? 1.0f : a.dloss[row]), fs = STEP ? f / s : f;
     auto fq = [&](float x) {                           // f q
         return fs * exp2_raw(STEP ? (x - m0) * c : __builtin_fmaf(x, inv, -lse) * kLog2e);
     };
+    if (here && te.id >= 0) te.give(sh, owner_of(te.id, head, V, VE, NT), fq(zk) - f * te.p);
     constexpr int64_t STRIDE = NT * VE;
     for (int64_t v = at.v + (int64_t)threadIdx.x * VE; v + VE <= at.v1; v += STRIDE * DU) {
         Raw<TS, VE> x[DU];
@@ -451,9 +459,8 @@ __global__ void __launch_bounds__(NT) distill_bwd_kernel(kan_distill_desc_t d, D
     if (p == 0 && (int)threadIdx.x < head) put1(dz + threadIdx.x, fq(load_f(z, threadIdx.x)));
     const int64_t tail = at.tail + threadIdx.x;
     if (tail < V) put1(dz + tail, fq(load_f(z, tail)));
-    // the teacher's entries again, now with their p taken off
     __syncthreads();
-    if (te.id >= at.v0 && te.id < at.v1) put1(dz + te.id, fq(load_f(z, te.id)) - f * te.p);
+    put_given<TG, NT>(dz, sh);
 }
 
 template <typename TS, typename TG, int NT, int NV, bool STEP, bool STREAM>
