@@ -93,7 +93,7 @@ constexpr int kRunsLanes(int vec) { return vec == 1 ? 4 : 16; }    // of the lau
 template <int VEC, int RC>
 struct Place {
     int64_t b, c, r0, r1, len;
-    int seg, cl, tl, w, waves;
+    int before, seg, cl, tl, w, waves;
     __device__ __forceinline__ Place(const kan_recur_desc_t& d, const RecurPlan& p, const int32_t* lengths) {
         const unsigned n = gridDim.x, i = blockIdx.x;
         unsigned l = n % 8 == 0 ? i % 8 * (n / 8) + i / 8 : i;
@@ -106,7 +106,9 @@ struct Place {
         tl = lane / RC;
         w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         waves = blockDim.x >> 6;
-        c = min((int64_t)cb * (RC * VEC) + cl * VEC, d.D - VEC);
+        const LaneChannels own(cb, cl, RC, VEC, d.D);
+        c = own.c;
+        before = own.before;
         r0 = seg * p.seg_rows;
         r1 = min(r0 + p.seg_rows, d.T);
         len = length_of(lengths, b, d.T);
@@ -344,8 +346,16 @@ __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d,
     if (at.w != 0 || at.tl != 0) return;
     const Run<VEC> run = all.run();
     runs += (at.b * p.segs + at.seg) * 2 * d.D + at.c;
-    store_vec<VEC>(runs, run.e);
-    store_vec<VEC>(runs + d.D, run.b);
+    if (at.before == 0) {
+        store_vec<VEC>(runs, run.e);
+        store_vec<VEC>(runs + d.D, run.b);
+        return;
+    }
+    // the channel block before this one stores its own, which end where its
+    // channels let them and may differ from these in what 2^-64 is worth
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        if (i >= at.before) runs[i] = run.e[i], runs[d.D + i] = run.b[i];
 }
 
 // Forward.  Two blocks to a compute unit (at most 128 registers): 32 x 700 x 770

@@ -46,6 +46,19 @@ struct RecurPlan {
 };
 RecurPlan recur_plan(const kan_recur_desc_t& d, int pass);
 
+// Channels of lane `cl` of channel block `cb`: `vec` of them from `c` on.  A
+// lane whose channels would pass D has the last ones instead; the first
+// `before` of those are a channel block's before this one.
+struct LaneChannels {
+    int64_t c;
+    int before;
+    __host__ __device__ inline LaneChannels(int64_t cb, int cl, int lanes, int vec, int64_t D) {
+        const int64_t first = cb * lanes * vec, own = first + cl * vec;
+        c = own < D - vec ? own : D - vec;
+        before = c < first ? (int)(first - c) : 0;
+    }
+};
+
 struct RecurArgs {
     const void *x, *g;
     const float *h0, *y, *dy, *dhT;
