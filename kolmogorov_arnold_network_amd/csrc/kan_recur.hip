@@ -71,12 +71,18 @@ struct Gate {
     __device__ __forceinline__ Shares shares() const {
         return Shares{keep() ? e : 1.0f + e, keep() ? 1.0f - e : -e};
     }
+    // f h + u x; as it stands where the difference overflows or has an infinity in it
     __device__ __forceinline__ float step(float h, float x) const {
         const float a = keep() ? h : x, b = keep() ? x : h;
-        return __builtin_fmaf(fabsf(e), b - a, a);
+        const float n = __builtin_fmaf(fabsf(e), b - a, a);
+        const Shares q = shares();
+        return __builtin_isfinite(n) ? n : __builtin_fmaf(q.f, h, q.u * x);
     }
-    // what is left of h: f h
-    __device__ __forceinline__ float of_state(float h) const { return __builtin_fmaf(-e, h, keep() ? h : 0.0f); }
+    // what is left of h: f h, an infinity for an infinity (h - e h has none left)
+    __device__ __forceinline__ float of_state(float h) const {
+        const float left = __builtin_fmaf(-e, h, keep() ? h : 0.0f);
+        return __builtin_isinf(h) ? h : left;
+    }
 };
 
 __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, int64_t T) {
