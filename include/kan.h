@@ -430,9 +430,10 @@ int kan_embed_backward(const kan_embed_desc_t* desc, const void* ids, const void
  * last places, so that neither long memories (L near 1) nor what is left of a
  * large state (L near 0) lose digits; all of it in float32, in a fixed order.
  * Where long sequences are cut into segments, a segment starts from the rows
- * before it up to where 2^-64 is left of a state, and drops the rest (an
- * infinity or NaN among those rows goes no further either).  hT is the last row
- * of y, bit for bit.
+ * before it up to where 2^-64 is left of a state, and drops the rest.  A state
+ * that is infinite or NaN leaves none finite after it in its channel, whether
+ * the sequence is cut or not (an infinity may become NaN where float32 has no
+ * share of it left).  hT is the last row of y, bit for bit.
  * x, g in `dtype` and dx, dg in `grad_dtype` have strides (elements from one row
  * to the next, and from one sequence to the next), so they may be the halves of
  * one projection; y, dy [B, T, D], h0, hT, dhT, dh0
@@ -451,7 +452,8 @@ typedef struct {
 
 /* Bytes of workspace a pass (kan_pass_t) needs (SIZE_MAX if `desc` is
  * invalid): with few channels and long sequences, the composed runs of a
- * sequence's segments; otherwise 0. */
+ * sequence's segments and marks of the channels whose state is not finite;
+ * otherwise 0. */
 size_t kan_recur_workspace_size(const kan_recur_desc_t* desc, int pass);
 /* y and hT out (hT may be NULL). */
 int kan_recur_forward(const kan_recur_desc_t* desc, const void* x, const void* g, const float* h0,

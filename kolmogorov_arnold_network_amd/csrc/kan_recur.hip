@@ -288,6 +288,40 @@ __device__ __forceinline__ void load_state(const float* from, int64_t at, float 
 
 constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 
+// Infinities and NaN among the rows that a segment's run leaves out would end
+// with their segment.  A block marks the channels whose last state has one, and
+// a third launch (AGAIN) of blocks that return at once where nothing is marked
+// goes through the marked channels' sequences whole and stores these alone.  So
+// a result does not depend on whether its sequence was cut, for 3 us a call (a
+// launch that finds nothing).  marks: [B][D].
+template <int VEC>
+__device__ __forceinline__ void mark(int* marks, const float (&h)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        if (!__builtin_isfinite(h[i])) marks[i] = 1;
+}
+template <int VEC>
+struct Marked {
+    bool own[VEC];
+    bool none;                    // of the block's channels: the same in all of its waves, which have them all
+    __device__ __forceinline__ Marked(const int* marks) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) own[i] = marks[i] != 0, any = any || own[i];
+        none = !__any(any);
+    }
+    __device__ __forceinline__ void put(float* p, const float (&v)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (own[i]) p[i] = v[i];
+    }
+    __device__ __forceinline__ void put(uint16_t* p, const float (&v)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (own[i]) p[i] = f2bf(v[i]);
+    }
+};
+
 // The runs of the segments, for the launch that starts each segment from them:
 // of h from x and g, or (BACK) of c from dy and g.  A segment's run is composed
 // from the end that counts most, the one where it hands its state on, and ends
@@ -301,12 +335,13 @@ constexpr int RF = kRecurRows, RB = kRecurRows;    // rows of a lane in a tile
 template <typename TS, typename TV, int VEC, int RC, bool BACK>
 __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d, RecurPlan p, const TS* g, const TV* v,
                                                              int64_t v_row, int64_t v_seq, const int32_t* lengths,
-                                                             float* runs) {
+                                                             float* runs, int* marks) {
     __shared__ Rows<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
     const Place<VEC, RC> at(d, p, lengths);
     g += at.b * d.g_seq + at.c;
     v += at.b * v_seq + at.c;
+    if (const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; threadIdx.x < 64 && i < d.B * d.D) marks[i] = 0;
     const int tile = at.waves * RL * RF, first = (at.w * RL + at.tl) * RF;
     const int64_t inside = min(at.len, at.r1), tiles = max((int64_t)0, (inside - at.r0 + tile - 1) / tile);
     Raw<TS, VEC> gr[RF];
@@ -367,13 +402,24 @@ __global__ void __launch_bounds__(64 * RW) recur_runs_kernel(kan_recur_desc_t d,
 // Forward.  Two blocks to a compute unit (at most 128 registers): 32 x 700 x 770
 // float32 47.0 -> 45.5 us, 64 x 300 x 768 39.9 -> 38.1, 4 x 1000 x 512 12.1 ->
 // 12.8.
-template <typename TS, int VEC, int RC, bool STREAM>
+template <typename TS, int VEC, int RC, bool STREAM, bool AGAIN>
 __global__ void __launch_bounds__(64 * RW, 4) recur_fwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
-                                                            const float* runs) {
+                                                            const float* runs, int* marks) {
     __shared__ Run<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
     const Place<VEC, RC> at(d, p, a.lengths);
     const int64_t D = d.D;
+    typename std::conditional<AGAIN, Marked<VEC>, const int*>::type marked(marks + at.b * D + at.c);
+    if constexpr (AGAIN)
+        if (marked.none) return;
+    auto put = [&](float* to, const float (&v)[VEC]) {
+        if constexpr (AGAIN) marked.put(to, v);
+        else store_vec<VEC, STREAM>(to, v);
+    };
+    auto put_last = [&](const float (&v)[VEC]) {
+        if constexpr (AGAIN) marked.put(a.hT + at.b * D + at.c, v);
+        else store_vec<VEC>(a.hT + at.b * D + at.c, v);
+    };
     const TS* x = static_cast<const TS*>(a.x) + at.b * d.x_seq + at.c;
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
     float* y = a.out + at.b * d.T * D + at.c;
@@ -437,7 +483,7 @@ __global__ void __launch_bounds__(64 * RW, 4) recur_fwd_kernel(kan_recur_desc_t 
         for (int r = 0; r < RF; ++r) {
             float o[VEC];
             row(r, o);
-            store_vec<VEC, STREAM>(y + (t0 + first + r) * D, o);
+            put(y + (t0 + first + r) * D, o);
         }
     }
     for (; t0 < inside; t0 += tile, parity ^= 1, ready = false) {      // the last ones
@@ -449,30 +495,37 @@ __global__ void __launch_bounds__(64 * RW, 4) recur_fwd_kernel(kan_recur_desc_t 
         for (int r = 0; r < RF; ++r) {
             float o[VEC];
             row(r, o);
-            if (a.hT && t + r == at.len - 1) store_vec<VEC>(a.hT + at.b * D + at.c, o);     // the bits of y
+            if (a.hT && t + r == at.len - 1) put_last(o);     // the bits of y
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] = t + r < at.len ? o[i] : 0.0f;
-            if (t + r < at.r1) store_vec<VEC, STREAM>(y + (t + r) * D, o);
+            if (t + r < at.r1) put(y + (t + r) * D, o);
         }
     }
     for (; t0 < at.r1; t0 += tile) {                   // rows past the length
         const float zero[VEC] = {};
 #pragma unroll
         for (int r = 0; r < RF; ++r)
-            if (t0 + first + r < at.r1) store_vec<VEC, STREAM>(y + (t0 + first + r) * D, zero);
+            if (t0 + first + r < at.r1) put(y + (t0 + first + r) * D, zero);
     }
-    if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0)
-        store_vec<VEC>(a.hT + at.b * D + at.c, h);     // h0
+    if (a.hT && at.len == 0 && at.seg == 0 && at.w == 0 && at.tl == 0) put_last(h);     // h0
+    if (at.seg + 1 < p.segs && at.w == 0 && at.tl == 0) mark(marks + at.b * D + at.c, h);
 }
 
 // Backward: the same, from the last row of a segment to its first.
-template <typename TS, typename TG, int VEC, int RC, bool STREAM>
+template <typename TS, typename TG, int VEC, int RC, bool STREAM, bool AGAIN>
 __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, RecurPlan p, RecurArgs a,
-                                                            const float* runs) {
+                                                            const float* runs, int* marks) {
     __shared__ Run<VEC> tot[2][RW][RC];
     constexpr int RL = 64 / RC;
     const Place<VEC, RC> at(d, p, a.lengths);
     const int64_t D = d.D;
+    typename std::conditional<AGAIN, Marked<VEC>, const int*>::type marked(marks + at.b * D + at.c);
+    if constexpr (AGAIN)
+        if (marked.none) return;
+    auto put = [&](TG* to, const float (&v)[VEC]) {
+        if constexpr (AGAIN) marked.put(to, v);
+        else store_vec<VEC, STREAM>(to, v);
+    };
     const TS* x = static_cast<const TS*>(a.x) + at.b * d.x_seq + at.c;
     const TS* g = static_cast<const TS*>(a.g) + at.b * d.g_seq + at.c;
     const float* y = a.y + at.b * d.T * D + at.c;
@@ -494,8 +547,8 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
 #pragma unroll
             for (int r = 0; r < RB; ++r)
                 if (t + r < at.r1) {
-                    store_vec<VEC, STREAM>(dx + (t + r) * d.dx_row, zero);
-                    store_vec<VEC, STREAM>(dg + (t + r) * d.dg_row, zero);
+                    put(dx + (t + r) * d.dx_row, zero);
+                    put(dg + (t + r) * d.dg_row, zero);
                 }
             continue;
         }
@@ -558,12 +611,16 @@ __global__ void __launch_bounds__(64 * RW) recur_bwd_kernel(kan_recur_desc_t d, 
                 if (t + r >= at.len)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) ox[i] = og[i] = 0.0f;
-                store_vec<VEC, STREAM>(dx + (t + r) * d.dx_row, ox);
-                store_vec<VEC, STREAM>(dg + (t + r) * d.dg_row, og);
+                put(dx + (t + r) * d.dx_row, ox);
+                put(dg + (t + r) * d.dg_row, og);
             }
         }
     }
-    if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) store_vec<VEC>(a.dh0 + at.b * D + at.c, c);
+    if (a.dh0 && at.seg == 0 && at.w == 0 && at.tl == 0) {
+        if constexpr (AGAIN) marked.put(a.dh0 + at.b * D + at.c, c);
+        else store_vec<VEC>(a.dh0 + at.b * D + at.c, c);
+    }
+    if (at.seg > 0 && at.w == 0 && at.tl == 0) mark(marks + at.b * D + at.c, c);
 }
 
 // One row of each sequence.  Slots differ, so no two threads share a state
@@ -596,36 +653,55 @@ RecurPlan runs_plan(const kan_recur_desc_t& d, RecurPlan p) {
     return p;
 }
 
+// That of the launch which goes through marked channels: whole sequences.
+RecurPlan again_plan(const kan_recur_desc_t& d, RecurPlan p) {
+    p.segs = 1;
+    p.seg_rows = d.T;
+    return runs_plan(d, p);
+}
+
 template <typename TS, int VEC, int RC, bool STREAM = false>
 hipError_t fwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
+    int* marks = reinterpret_cast<int*>(ws + p.off_marks);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
         const RecurPlan r = runs_plan(d, p);
         hipLaunchKernelGGL((recur_runs_kernel<TS, TS, VEC, kRunsLanes(VEC), false>),
                            dim3((unsigned)(d.B * r.blocks * r.segs)), dim3(64 * r.waves), 0, s, d, r,
                            static_cast<const TS*>(a.g), static_cast<const TS*>(a.x), d.x_row, d.x_seq, a.lengths,
-                           runs);
+                           runs, marks);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, STREAM>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, RC, STREAM, false>), grid, block, 0, s, d, p, a, runs, marks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.segs == 1) return e;
+    const RecurPlan w = again_plan(d, p);
+    hipLaunchKernelGGL((recur_fwd_kernel<TS, VEC, kRunsLanes(VEC), false, true>), dim3((unsigned)(d.B * w.blocks)),
+                       dim3(64 * w.waves), 0, s, d, w, a, nullptr, marks);
     return hipGetLastError();
 }
 
 template <typename TS, typename TG, int VEC, int RC, bool STREAM = false>
 hipError_t bwd_t(const kan_recur_desc_t& d, const RecurPlan& p, const RecurArgs& a, char* ws, hipStream_t s) {
     float* runs = reinterpret_cast<float*>(ws);
+    int* marks = reinterpret_cast<int*>(ws + p.off_marks);
     const dim3 grid((unsigned)(d.B * p.blocks * p.segs)), block(64 * p.waves);
     if (p.segs > 1) {
         const RecurPlan r = runs_plan(d, p);
         hipLaunchKernelGGL((recur_runs_kernel<TS, float, VEC, kRunsLanes(VEC), true>),
                            dim3((unsigned)(d.B * r.blocks * r.segs)), dim3(64 * r.waves), 0, s, d, r,
-                           static_cast<const TS*>(a.g), a.dy, d.D, d.T * d.D, a.lengths, runs);
+                           static_cast<const TS*>(a.g), a.dy, d.D, d.T * d.D, a.lengths, runs, marks);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, STREAM>), grid, block, 0, s, d, p, a, runs);
+    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, RC, STREAM, false>), grid, block, 0, s, d, p, a, runs, marks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.segs == 1) return e;
+    const RecurPlan w = again_plan(d, p);
+    hipLaunchKernelGGL((recur_bwd_kernel<TS, TG, VEC, kRunsLanes(VEC), false, true>), dim3((unsigned)(d.B * w.blocks)),
+                       dim3(64 * w.waves), 0, s, d, w, a, nullptr, marks);
     return hipGetLastError();
 }
 

@@ -42,7 +42,8 @@ struct RecurPlan {
     bool on_lines;                   // rows start on cache lines
     unsigned blocks;                 // channel blocks
     int64_t seg_rows;
-    size_t ws;                       // runs of the segments: [B][segs][2][D] float
+    // runs of the segments [B][segs][2][D] float, then marks [B][D] int
+    size_t off_marks, ws;
 };
 RecurPlan recur_plan(const kan_recur_desc_t& d, int pass);
 

@@ -209,7 +209,8 @@ RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
     const int wave_rows = kRecurRows * (64 / p.lanes);
     p.waves = 1;
     while (p.waves < kRecurWaves && p.waves * wave_rows < p.seg_rows) p.waves *= 2;
-    p.ws = p.segs > 1 ? (size_t)round_up(d.B * p.segs * 2 * d.D * 4, 256) : 0;
+    p.off_marks = p.segs > 1 ? (size_t)round_up(d.B * p.segs * 2 * d.D * 4, 256) : 0;
+    p.ws = p.segs > 1 ? p.off_marks + (size_t)round_up(d.B * d.D * 4, 256) : 0;
     return p;
 }
 
