@@ -362,6 +362,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _placed(t):
+    """An input whose data starts on the 16 bytes that the entry points ask for: a
+    copy of a view that starts elsewhere (``ids[1:]``, the gradient of a part of
+    ``torch.cat``), the tensor itself otherwise."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
@@ -408,6 +415,7 @@ def kan_embed_forward(ids, table, scale=1.0, row_dtype=None, out=None):
     else:
         y = out
         _whole(y, "y", (row_dtype,), dev, (*ids.shape, D))
+    ids, table = _placed(ids), _placed(table)
     desc = embed_desc(ids.numel(), V, D, table.dtype, row_dtype, ids.dtype, scale)
     L.check(L.lib().kan_embed_forward(desc, ids.data_ptr(), table.data_ptr(), y.data_ptr(), _raw_stream(dev)),
             "kan_embed_forward")
@@ -427,6 +435,7 @@ def kan_embed_backward(ids, dy, num_rows, scale=1.0, ws=None, out=None):
     else:
         dE = out
         _whole(dE, "dE", _F32, dev, (num_rows, D))
+    ids, dy = _placed(ids), _placed(dy)
     desc = embed_desc(ids.numel(), num_rows, D, torch.float32, dy.dtype, ids.dtype, scale)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_embed_workspace_size(desc), dy)
@@ -482,6 +491,7 @@ def kan_recur_forward(x, g, h0=None, lengths=None, ws=None, out=None):
         y = out
         _whole(y, "y", _F32, dev, x.shape)
     hT = y.new_empty((B, D))
+    h0, lengths = _placed(h0), _placed(lengths)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_recur_workspace_size(desc, L.KAN_PASS_FORWARD), x)
     L.check(lib.kan_recur_forward(desc, x.data_ptr(), g.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
@@ -510,6 +520,7 @@ def kan_recur_backward(x, g, y, dy, h0=None, lengths=None, dhT=None, need_dh0=No
     desc = recur_desc(x, g, dx, dg)
     need_dh0 = h0 is not None if need_dh0 is None else need_dh0
     dh0 = y.new_empty((shape[0], shape[2])) if need_dh0 else None
+    h0, lengths, y, dy, dhT = _placed(h0), _placed(lengths), _placed(y), _placed(dy), _placed(dhT)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_recur_workspace_size(desc, L.KAN_PASS_BACKWARD), x)
     L.check(lib.kan_recur_backward(desc, x.data_ptr(), g.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
@@ -539,6 +550,7 @@ def kan_recur_step(x, g, state, slots=None, out=None):
     else:
         y = out
         _whole(y, "y", _F32, dev, shape)
+    slots = _placed(slots)
     L.check(L.lib().kan_recur_step(desc, state.shape[0], x.data_ptr(), g.data_ptr(), state.data_ptr(), _addr(slots),
                                    y.data_ptr(), _raw_stream(dev)), "kan_recur_step")
     return y
@@ -593,6 +605,7 @@ def kan_distill_forward(z, ids, t, temperature=1.0, weight=None, ws=None):
     desc = distill_desc(z, ids, t, temperature)
     loss = z.new_empty(z.shape[:1], dtype=torch.float32)
     lse = torch.empty_like(loss)
+    ids, t, weight = _placed(ids), _placed(t), _placed(weight)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_distill_workspace_size(desc), z)
     L.check(lib.kan_distill_forward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
@@ -609,6 +622,7 @@ def kan_distill_backward(z, ids, t, lse, dloss, temperature=1.0, weight=None, gr
     _whole(dloss, "dloss", _F32, dev, z.shape[:1])
     dz = _distill_grad(z, out, grad_dtype, dev)
     desc = distill_desc(z, ids, t, temperature, dz)
+    ids, t, weight, lse, dloss = _placed(ids), _placed(t), _placed(weight), _placed(lse), _placed(dloss)
     L.check(L.lib().kan_distill_backward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
                                          lse.data_ptr(), dloss.data_ptr(), dz.data_ptr(), _raw_stream(dev)),
             "kan_distill_backward")
@@ -622,6 +636,7 @@ def kan_distill_step(z, ids, t, temperature=1.0, weight=None, grad_dtype=torch.f
     dz = _distill_grad(z, out, grad_dtype, dev)
     desc = distill_desc(z, ids, t, temperature, dz)
     loss = z.new_empty(z.shape[:1], dtype=torch.float32)
+    ids, t, weight = _placed(ids), _placed(t), _placed(weight)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_distill_workspace_size(desc), z)
     L.check(lib.kan_distill_step(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight), loss.data_ptr(),
