@@ -313,7 +313,12 @@ class KANRecurrence(torch.nn.Module):
         return "in=%d, out=%d" % (self.in_features, self.out_features)
 
 
+_NO_GRADIENT = "the loss has no gradient of the teacher's logits or of the weights: detach them"
+
+
 class DistillFunction(torch.autograd.Function):
+    """The rows' losses; their gradient is that of the student's logits alone."""
+
     @staticmethod
     def forward(ctx, z, ids, t, temperature, weight):
         loss, lse = F.kan_distill_forward(z, ids, t, temperature, weight)
@@ -323,6 +328,8 @@ class DistillFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dloss):
+        if ctx.needs_input_grad[2] or ctx.needs_input_grad[4]:
+            raise ValueError(_NO_GRADIENT)
         z, ids, t, lse, weight = ctx.saved_tensors
         dz = F.kan_distill_backward(z, ids, t, lse, dloss.contiguous().float(), ctx.temperature, weight,
                                     grad_dtype=z.dtype)
@@ -333,7 +340,8 @@ class KANDistillLoss(torch.nn.Module):
     """``tau^2`` times the divergence of a student's logits ``z [..., V]`` from a
     teacher's top logits ``t [..., K]`` of the tokens ``ids [..., K]``, both
     softened by the temperature ``tau``.  ``weight [...]`` (float32) scales rows;
-    rows of weight 0 (padding) are not read.  ``reduction``: ``mean`` over all
+    rows of weight 0 (padding) reach neither loss nor gradient.  The gradient is
+    that of ``z``; ``t`` and ``weight`` must not require one.  ``reduction``: ``mean`` over all
     rows, ``sum`` or ``none``."""
 
     def __init__(self, temperature=1.0, reduction="mean"):
@@ -347,6 +355,8 @@ class KANDistillLoss(torch.nn.Module):
         lead = z.shape[:-1]
         if ids.shape[:-1] != lead or t.shape != ids.shape or (weight is not None and weight.shape != lead):
             raise ValueError("z, ids, t and weight must share their leading dimensions")
+        if torch.is_grad_enabled() and (t.requires_grad or (weight is not None and weight.requires_grad)):
+            raise ValueError(_NO_GRADIENT)
         K = ids.shape[-1]
         loss = DistillFunction.apply(z.reshape(-1, z.shape[-1]), ids.reshape(-1, K).contiguous(),
                                      t.reshape(-1, K).contiguous(), self.temperature,
