@@ -12,6 +12,7 @@ calls ``kan_backward``; torch only accumulates the returned gradients.
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import functional as F
 
@@ -232,6 +233,7 @@ class EmbedFunction(torch.autograd.Function):
         return F.kan_embed_forward(ids, table, scale, row_dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
         dE = F.kan_embed_backward(ids, dy.contiguous(), ctx.rows, ctx.scale)
@@ -274,6 +276,7 @@ class RecurFunction(torch.autograd.Function):
         return y, hT
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dhT):
         p, h0, lengths, y = ctx.saved_tensors
         D = p.shape[2] // 2
@@ -327,6 +330,7 @@ class DistillFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         if ctx.needs_input_grad[2] or ctx.needs_input_grad[4]:
             raise ValueError(_NO_GRADIENT)

@@ -1,5 +1,5 @@
 """GPU: what the token-side modules have no gradient of is refused, not left out:
-the distillation's teacher and weights."""
+the distillation's teacher and weights, and second derivatives."""
 
 import pytest
 
@@ -39,3 +39,17 @@ def test_distillation_refuses_gradients_that_it_does_not_have(env, which):
     rows = kan.DistillFunction.apply(z, ids, t, 2.0, w)
     with pytest.raises(ValueError):
         rows.sum().backward()
+
+
+def test_second_derivatives_are_refused(env):
+    torch, kan = env
+    z, ids, t, w = _case(torch)
+    emb = kan.KANEmbedding(30, 6, device="cuda:0")
+    p = torch.randn(2, 9, 8, device="cuda:0", requires_grad=True)
+    for out, x in (((emb(ids) ** 2).sum(), emb.table),
+                   ((kan.RecurFunction.apply(p, None, None)[0] ** 2).sum(), p),
+                   ((kan.DistillFunction.apply(z, ids, t, 2.0, w) ** 2).sum(), z)):
+        (first,) = torch.autograd.grad(out, x, create_graph=True)
+        assert bool(torch.isfinite(first).all()) and bool(first.any())
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            first.sum().backward()
