@@ -562,7 +562,7 @@ def _row_stride(t):
 
 
 def distill_desc(z, ids, t, tau, dz=None, grad_dtype=torch.float32):
-    """``kan_distill_desc_t`` of ``z [N, V]`` (any row stride) and ``ids``, ``t [N, K]``."""
+    """``kan_distill_desc_t`` of ``z [N, V]`` (a row stride of V or more) and ``ids``, ``t [N, K]``."""
     if z.dim() != 2 or ids.dim() != 2 or ids.shape[0] != z.shape[0]:
         raise ValueError("z must be [N, V] and ids [N, K]")
     if t.shape != ids.shape:

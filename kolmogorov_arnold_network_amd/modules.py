@@ -305,12 +305,15 @@ class KANRecurrence(torch.nn.Module):
         self.layer = KANLayer(in_features, 2 * out_features, **kw)
 
     def forward(self, x, h0=None, lengths=None):
-        return RecurFunction.apply(self.layer(x), h0, lengths)
+        # one initial state for all sequences comes expanded
+        return RecurFunction.apply(self.layer(x), None if h0 is None else h0.contiguous(),
+                                   None if lengths is None else lengths.contiguous())
 
     @torch.no_grad()
     def step(self, x, state, slots=None):
         p = self.layer(x)
-        return F.kan_recur_step(p[:, :self.out_features], p[:, self.out_features:], state, slots)
+        return F.kan_recur_step(p[:, :self.out_features], p[:, self.out_features:], state,
+                                None if slots is None else slots.contiguous())
 
     def extra_repr(self):
         return "in=%d, out=%d" % (self.in_features, self.out_features)
@@ -362,7 +365,10 @@ class KANDistillLoss(torch.nn.Module):
         if torch.is_grad_enabled() and (t.requires_grad or (weight is not None and weight.requires_grad)):
             raise ValueError(_NO_GRADIENT)
         K = ids.shape[-1]
-        loss = DistillFunction.apply(z.reshape(-1, z.shape[-1]), ids.reshape(-1, K).contiguous(),
+        z = z.reshape(-1, z.shape[-1])
+        if z.stride(1) != 1 or z.stride(0) < z.shape[1]:        # rows that are columns, or one for all
+            z = z.contiguous()
+        loss = DistillFunction.apply(z, ids.reshape(-1, K).contiguous(),
                                      t.reshape(-1, K).contiguous(), self.temperature,
                                      None if weight is None else weight.reshape(-1).contiguous())
         if self.reduction == "none":

@@ -1,6 +1,7 @@
 """GPU: the token-side operators on views of larger tensors: data that starts
 off 16 bytes, in the wrappers, in the modules and in gradients that autograd
-hands on.  Results equal those of copies, bit for bit."""
+hands on; strided and expanded views in the modules.  Results equal those of
+copies, bit for bit."""
 
 import pytest
 
@@ -136,3 +137,52 @@ def test_losses_and_states_through_cat(env):
         torch.cat([torch.zeros(1, device="cuda:0", requires_grad=True), out]).sum().backward()
         assert bool(torch.isfinite(x.grad).all()) and bool(x.grad.any())
         x.grad = None
+
+
+def test_one_initial_state_for_all_sequences(env):
+    """A learned state, expanded over the batch: its gradient is the sequences' sum."""
+    torch, kan = env
+    torch.manual_seed(6)
+    rec = kan.KANRecurrence(4, 6, grid_range=(-4.0, 4.0), device="cuda:0")
+    x = torch.randn(5, 8, 4, device="cuda:0")
+    lengths = torch.tensor([8, 1, 0, 1, 3, 1, 8, 1, 5, 1], dtype=torch.int32, device="cuda:0")[::2]
+    first = torch.randn(6, device="cuda:0", requires_grad=True)
+    y, hT = rec(x, first.expand(5, 6), lengths)
+    whole = first.detach().expand(5, 6).contiguous().requires_grad_()
+    y2, hT2 = rec(x, whole, lengths.contiguous())
+    assert torch.equal(y, y2) and torch.equal(hT, hT2)
+    dy, dh = torch.randn_like(y), torch.randn_like(hT)
+    torch.autograd.backward([y, hT], [dy, dh])
+    torch.autograd.backward([y2, hT2], [dy, dh])
+    assert torch.equal(first.grad, whole.grad.sum(0))
+    s1 = torch.randn(6, 6, device="cuda:0")
+    s2 = s1.clone()
+    slots = torch.tensor([4, 9, 0, 9, 3, 9], dtype=torch.int32, device="cuda:0")[::2]
+    assert torch.equal(rec.step(x[:3, 0], s1, slots), rec.step(x[:3, 0], s2, slots.contiguous())) and torch.equal(s1, s2)
+
+
+@pytest.mark.parametrize("layout", ["columns", "one row", "vocabulary first"])
+def test_logits_of_any_strides(env, layout):
+    torch, kan = env
+    torch.manual_seed(7)
+    loss = kan.KANDistillLoss(2.0)
+    if layout == "columns":
+        z = torch.randn(40, 6, device="cuda:0", requires_grad=True)
+        view = z.t()
+    elif layout == "one row":
+        z = torch.randn(40, device="cuda:0", requires_grad=True)
+        view = z.expand(6, 40)
+    else:
+        z = torch.randn(2, 40, 3, device="cuda:0", requires_grad=True)
+        view = z.transpose(1, 2)
+    lead = view.shape[:-1]
+    ids, t = torch.randint(0, 40, (*lead, 3), device="cuda:0"), torch.randn(*lead, 3, device="cuda:0")
+    w = torch.rand(*lead, device="cuda:0")
+    got = loss(view, ids, t, w)
+    copy = view.detach().contiguous().requires_grad_()
+    want = loss(copy, ids, t, w)
+    assert torch.equal(got, want)
+    got.backward()
+    want.backward()
+    back = {"columns": lambda v: v.t(), "one row": lambda v: v.sum(0), "vocabulary first": lambda v: v.transpose(1, 2)}
+    assert torch.equal(z.grad, back[layout](copy.grad))
