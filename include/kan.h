@@ -499,9 +499,9 @@ typedef struct {
     float tau;              /* finite, > 0 */
 } kan_distill_desc_t;
 
-/* Bytes of workspace kan_distill_forward and kan_distill_step need (SIZE_MAX
- * if `desc` is invalid): for a step of few long rows, the maxima and sums of a
- * row's parts; otherwise 0. */
+/* Bytes of workspace kan_distill_step needs (SIZE_MAX if `desc` is invalid):
+ * for few long rows, the maxima and sums of a row's parts; otherwise 0.
+ * kan_distill_forward needs none (its workspace may be NULL). */
 size_t kan_distill_workspace_size(const kan_distill_desc_t* desc);
 int kan_distill_forward(const kan_distill_desc_t* desc, const void* z, const void* ids, const void* t,
                         const float* w, float* loss, float* lse, void* workspace, size_t workspace_bytes,

@@ -391,15 +391,14 @@ int kan_distill_forward(const kan_distill_desc_t* desc, const void* z, const voi
     if ((st = distill_inputs(*desc, z, ids, t, w, in)) != KAN_OK) return st;
     if (desc->N > 0 && (!loss || !lse)) return KAN_ERR_NULL;
     if (!all_aligned({loss, lse}, 16)) return KAN_ERR_ALIGN;
-    const size_t need = kan_distill_workspace_size(desc);
-    if ((st = check_ws(ws, ws_bytes, need)) != KAN_OK) return st;
-    const Range outs[] = {{loss, (size_t)desc->N * 4}, {lse, (size_t)desc->N * 4}, {ws, need}};
+    if ((st = check_ws(ws, ws_bytes, 0)) != KAN_OK) return st;      // only the step's rows are cut
+    const Range outs[] = {{loss, (size_t)desc->N * 4}, {lse, (size_t)desc->N * 4}};
     if (any_overlap(outs, in)) return KAN_ERR_ALIAS;
     if (desc->N == 0) return KAN_OK;
     DistillArgs a = {};
     a.z = z, a.ids = ids, a.t = t, a.w = w, a.loss = loss, a.lse = lse;
     (void)hipGetLastError();
-    return status_of(launch_distill(*desc, distill_plan(*desc), a, static_cast<char*>(ws), (hipStream_t)stream));
+    return status_of(launch_distill(*desc, DistillPlan{1, desc->V, 0}, a, nullptr, (hipStream_t)stream));
 }
 
 int kan_distill_backward(const kan_distill_desc_t* desc, const void* z, const void* ids, const void* t,

@@ -606,10 +606,9 @@ def kan_distill_forward(z, ids, t, temperature=1.0, weight=None, ws=None):
     loss = z.new_empty(z.shape[:1], dtype=torch.float32)
     lse = torch.empty_like(loss)
     ids, t, weight = _placed(ids), _placed(t), _placed(weight)
-    lib = L.lib()
-    buf, n = _sized_ws(ws, lib.kan_distill_workspace_size(desc), z)
-    L.check(lib.kan_distill_forward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
-                                    loss.data_ptr(), lse.data_ptr(), _addr(buf), n, _raw_stream(dev)),
+    buf, n = (None, 0) if ws is None else _check_ws(ws, z.device)
+    L.check(L.lib().kan_distill_forward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
+                                        loss.data_ptr(), lse.data_ptr(), _addr(buf), n, _raw_stream(dev)),
             "kan_distill_forward")
     return loss, lse
 
