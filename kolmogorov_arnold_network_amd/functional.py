@@ -23,8 +23,20 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+_current = torch._C._cuda_getDevice                     # the current device's number
+_raw_stream = torch._C._cuda_getCurrentRawStream        # of a device number
+
+
+def _launch(what, dev, fn, *args):
+    """Calls entry point ``fn`` for tensors on device number ``dev``, on that
+    device's current stream and with it as the current device: a launch on the
+    null stream goes to the current one, whatever device its tensors are on."""
+    if _current() == dev:
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    L.check(status, what)
 
 
 def _check_tensor(t, name, dtypes, device=None):
@@ -108,8 +120,8 @@ def kan_prepare(x, C, W, grid, pass_, dy=None, variant="auto", ws=None, dense_fo
     if ws is None:
         ws = workspace(desc, pass_, C.device)
     buf, n = _check_ws(ws, C.device)
-    L.check(L.lib().kan_prepare(ctypes.byref(desc), int(pass_), _ptr(C), _ptr(W), _ptr(dy),
-                                _ptr(buf), n, _stream(C)), "kan_prepare")
+    _launch("kan_prepare", C.get_device(), L.lib().kan_prepare, ctypes.byref(desc), int(pass_), _ptr(C), _ptr(W),
+            _ptr(dy), _ptr(buf), n)
     return ws
 
 
@@ -130,8 +142,8 @@ def kan_forward(x, C, W, grid, variant="auto", ws=None, prepared=False, out=None
     y = out if out is not None else torch.empty((x.shape[0], C.shape[0]), dtype=torch.float32,
                                                 device=x.device)
     _check_out(y, "y", (x.shape[0], C.shape[0]), x.device)
-    L.check(L.lib().kan_forward(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(W), _ptr(y), _ptr(buf),
-                                n, _stream(x)), "kan_forward")
+    _launch("kan_forward", x.get_device(), L.lib().kan_forward, ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(W),
+            _ptr(y), _ptr(buf), n)
     return y
 
 
@@ -146,8 +158,8 @@ def kan_forward_static(x, C, W, grid, variant="auto", out=None, dense_forward=Fa
     y = out if out is not None else torch.empty((x.shape[0], C.shape[0]), dtype=torch.float32,
                                                 device=x.device)
     _check_out(y, "y", (x.shape[0], C.shape[0]), x.device)
-    L.check(L.lib().kan_forward_static(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(W), _ptr(y), _stream(x)),
-            "kan_forward_static")
+    _launch("kan_forward_static", x.get_device(), L.lib().kan_forward_static, ctypes.byref(desc), _ptr(x), _ptr(C),
+            _ptr(W), _ptr(y))
     return y
 
 
@@ -168,8 +180,8 @@ def kan_backward(x, C, W, dy, grid, need_dx=True, need_dC=True, need_dW=True, va
     dx = torch.empty(x.shape, **f32) if need_dx else None
     dC = torch.empty(C.shape, **f32) if need_dC else None
     dW = torch.empty(W.shape, **f32) if (need_dW and W is not None) else None
-    L.check(L.lib().kan_backward(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(W), _ptr(dy), _ptr(dx),
-                                 _ptr(dC), _ptr(dW), _ptr(buf), n, _stream(x)), "kan_backward")
+    _launch("kan_backward", x.get_device(), L.lib().kan_backward, ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(W),
+            _ptr(dy), _ptr(dx), _ptr(dC), _ptr(dW), _ptr(buf), n)
     return dx, dC, dW
 
 
@@ -180,7 +192,7 @@ def _basis(fn, name, x, grid, need_B, need_dB, degree):
     n = x.numel()
     B = torch.empty((n, G + degree), dtype=torch.float32, device=x.device) if need_B else None
     dB = torch.empty((n, G + degree), dtype=torch.float32, device=x.device) if need_dB else None
-    L.check(fn(ctypes.byref(g), n, _DTYPES[x.dtype], _ptr(x), _ptr(B), _ptr(dB), _stream(x)), name)
+    _launch(name, x.get_device(), fn, ctypes.byref(g), n, _DTYPES[x.dtype], _ptr(x), _ptr(B), _ptr(dB))
     return B, dB
 
 
@@ -219,8 +231,8 @@ def kan_group_forward(x, C, grid, out=None):
     desc = group_desc(x, C, grid)
     y = out if out is not None else torch.empty(x.shape, dtype=torch.float32, device=x.device)
     _check_out(y, "y", x.shape, x.device)
-    L.check(L.lib().kan_group_forward(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(y), _stream(x)),
-            "kan_group_forward")
+    _launch("kan_group_forward", x.get_device(), L.lib().kan_group_forward, ctypes.byref(desc), _ptr(x), _ptr(C),
+            _ptr(y))
     return y
 
 
@@ -239,8 +251,8 @@ def kan_group_backward(x, C, dy, grid, need_dx=True, need_dC=True, ws=None):
     f32 = dict(dtype=torch.float32, device=x.device)
     dx = torch.empty(x.shape, **f32) if need_dx else None
     dC = torch.empty(C.shape, **f32) if need_dC else None
-    L.check(L.lib().kan_group_backward(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(dy), _ptr(dx),
-                                       _ptr(dC), _ptr(buf), n, _stream(x)), "kan_group_backward")
+    _launch("kan_group_backward", x.get_device(), L.lib().kan_group_backward, ctypes.byref(desc), _ptr(x), _ptr(C),
+            _ptr(dy), _ptr(dx), _ptr(dC), _ptr(buf), n)
     return dx, dC
 
 
@@ -282,8 +294,8 @@ def kan_surface_forward(x, C, grid, ws=None, out=None, dense_forward=False):
     y = out if out is not None else torch.empty((x.shape[0], C.shape[0]), dtype=torch.float32,
                                                 device=x.device)
     _check_out(y, "y", (x.shape[0], C.shape[0]), x.device)
-    L.check(L.lib().kan_surface_forward(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(y), _ptr(buf), n,
-                                        _stream(x)), "kan_surface_forward")
+    _launch("kan_surface_forward", x.get_device(), L.lib().kan_surface_forward, ctypes.byref(desc), _ptr(x),
+            _ptr(C), _ptr(y), _ptr(buf), n)
     return y
 
 
@@ -299,8 +311,8 @@ def kan_surface_backward(x, C, dy, grid, need_dx=True, need_dC=True, ws=None):
     f32 = dict(dtype=torch.float32, device=x.device)
     dx = torch.empty(x.shape, **f32) if need_dx else None
     dC = torch.empty(C.shape, **f32) if need_dC else None
-    L.check(L.lib().kan_surface_backward(ctypes.byref(desc), _ptr(x), _ptr(C), _ptr(dy), _ptr(dx), _ptr(dC),
-                                         _ptr(buf), n, _stream(x)), "kan_surface_backward")
+    _launch("kan_surface_backward", x.get_device(), L.lib().kan_surface_backward, ctypes.byref(desc), _ptr(x),
+            _ptr(C), _ptr(dy), _ptr(dx), _ptr(dC), _ptr(buf), n)
     return dx, dC
 
 
@@ -308,8 +320,7 @@ def kan_cast_f32_to_bf16(t, out=None):
     """Round-to-nearest-even float32 -> bfloat16 on the device."""
     _check_tensor(t, "input", (torch.float32,))
     o = out if out is not None else torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-    L.check(L.lib().kan_cast_f32_to_bf16(_ptr(t), _ptr(o), t.numel(), _stream(t)),
-            "kan_cast_f32_to_bf16")
+    _launch("kan_cast_f32_to_bf16", t.get_device(), L.lib().kan_cast_f32_to_bf16, _ptr(t), _ptr(o), t.numel())
     return o
 
 
@@ -317,7 +328,10 @@ def kan_cast_f32_to_bf16(t, out=None):
 #
 # These are called once a token when serving, so their host side is kept short:
 # tensors are checked through their device number, addresses and the stream go
-# to the library as plain integers.
+# to the library as plain integers, and a call whose tensors lie on another
+# device than the current one, or start off the 16 bytes that the entry points
+# ask for, is made again on that device with copies of the latter.  (Both tests
+# are one expression in each wrapper: a function for them takes 0.4 us a call.)
 
 _INDEX = {torch.int32: L.KAN_I32, torch.int64: L.KAN_I64}
 _F32 = (torch.float32,)
@@ -363,14 +377,10 @@ def _addr(t):
 
 
 def _placed(t):
-    """An input whose data starts on the 16 bytes that the entry points ask for: a
-    copy of a view that starts elsewhere (``ids[1:]``, the gradient of a part of
-    ``torch.cat``), the tensor itself otherwise."""
+    """An input whose data starts on 16 bytes: a copy of a view that starts
+    elsewhere (``ids[1:]``, the gradient of a part of ``torch.cat``), the tensor
+    itself otherwise."""
     return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
-
-
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _sized_ws(ws, n, t):
@@ -406,6 +416,10 @@ def kan_embed_forward(ids, table, scale=1.0, row_dtype=None, out=None):
     _whole(table, "table", _DTYPES, dev)
     if table.dim() != 2:
         raise ValueError("table must be [V, D]")
+    ids_at, table_at = ids.data_ptr(), table.data_ptr()
+    if (ids_at | table_at) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_embed_forward(_placed(ids), _placed(table), scale, row_dtype, out)
     V, D = table.shape
     row_dtype = row_dtype or (table.dtype if out is None else out.dtype)
     if row_dtype not in _DTYPES:
@@ -415,10 +429,8 @@ def kan_embed_forward(ids, table, scale=1.0, row_dtype=None, out=None):
     else:
         y = out
         _whole(y, "y", (row_dtype,), dev, (*ids.shape, D))
-    ids, table = _placed(ids), _placed(table)
     desc = embed_desc(ids.numel(), V, D, table.dtype, row_dtype, ids.dtype, scale)
-    L.check(L.lib().kan_embed_forward(desc, ids.data_ptr(), table.data_ptr(), y.data_ptr(), _raw_stream(dev)),
-            "kan_embed_forward")
+    L.check(L.lib().kan_embed_forward(desc, ids_at, table_at, y.data_ptr(), _raw_stream(dev)), "kan_embed_forward")
     return y
 
 
@@ -429,18 +441,21 @@ def kan_embed_backward(ids, dy, num_rows, scale=1.0, ws=None, out=None):
     _whole(dy, "dy", _DTYPES, dev)
     if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
         raise ValueError("dy must be [*ids.shape, D], got %s" % (tuple(dy.shape),))
+    ids_at, dy_at = ids.data_ptr(), dy.data_ptr()
+    if (ids_at | dy_at) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_embed_backward(_placed(ids), _placed(dy), num_rows, scale, ws, out)
     D = dy.shape[-1]
     if out is None:
         dE = dy.new_empty((num_rows, D), dtype=torch.float32)
     else:
         dE = out
         _whole(dE, "dE", _F32, dev, (num_rows, D))
-    ids, dy = _placed(ids), _placed(dy)
     desc = embed_desc(ids.numel(), num_rows, D, torch.float32, dy.dtype, ids.dtype, scale)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_embed_workspace_size(desc), dy)
-    L.check(lib.kan_embed_backward(desc, ids.data_ptr(), dy.data_ptr(), dE.data_ptr(), _addr(buf), n,
-                                   _raw_stream(dev)), "kan_embed_backward")
+    L.check(lib.kan_embed_backward(desc, ids_at, dy_at, dE.data_ptr(), _addr(buf), n, _raw_stream(dev)),
+            "kan_embed_backward")
     return dE
 
 
@@ -483,6 +498,10 @@ def kan_recur_forward(x, g, h0=None, lengths=None, ws=None, out=None):
     ``h_t = sigmoid(g_t) h_{t-1} + sigmoid(-g_t) x_t``.  ``h0 [B, D]`` float32
     (default 0), ``lengths [B]`` int32 (default T); ``y`` is 0 past a length."""
     dev = _recur_inputs(x, g, h0, lengths)
+    h0_at, lengths_at = _addr(h0), _addr(lengths)
+    if ((h0_at or 0) | (lengths_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_recur_forward(x, g, _placed(h0), _placed(lengths), ws, out)
     desc = recur_desc(x, g)
     B, T, D = x.shape
     if out is None:
@@ -491,11 +510,10 @@ def kan_recur_forward(x, g, h0=None, lengths=None, ws=None, out=None):
         y = out
         _whole(y, "y", _F32, dev, x.shape)
     hT = y.new_empty((B, D))
-    h0, lengths = _placed(h0), _placed(lengths)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_recur_workspace_size(desc, L.KAN_PASS_FORWARD), x)
-    L.check(lib.kan_recur_forward(desc, x.data_ptr(), g.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
-                                  hT.data_ptr(), _addr(buf), n, _raw_stream(dev)), "kan_recur_forward")
+    L.check(lib.kan_recur_forward(desc, x.data_ptr(), g.data_ptr(), h0_at, lengths_at, y.data_ptr(), hT.data_ptr(),
+                                  _addr(buf), n, _raw_stream(dev)), "kan_recur_forward")
     return y, hT
 
 
@@ -513,6 +531,11 @@ def kan_recur_backward(x, g, y, dy, h0=None, lengths=None, dhT=None, need_dh0=No
         _whole(dhT, "dhT", _F32, dev, (shape[0], shape[2]))
     if (dx is None) != (dg is None):
         raise ValueError("give both dx and dg or neither")
+    h0_at, lengths_at, y_at, dy_at, dhT_at = _addr(h0), _addr(lengths), y.data_ptr(), dy.data_ptr(), _addr(dhT)
+    if ((h0_at or 0) | (lengths_at or 0) | y_at | dy_at | (dhT_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_recur_backward(x, g, _placed(y), _placed(dy), _placed(h0), _placed(lengths), _placed(dhT),
+                                      need_dh0, grad_dtype, dx, dg, ws)
     if dx is None:
         dx, dg = x.new_empty((2, *shape), dtype=grad_dtype).unbind(0)
     _rows(dx, "dx", _DTYPES, dev, shape)
@@ -520,12 +543,11 @@ def kan_recur_backward(x, g, y, dy, h0=None, lengths=None, dhT=None, need_dh0=No
     desc = recur_desc(x, g, dx, dg)
     need_dh0 = h0 is not None if need_dh0 is None else need_dh0
     dh0 = y.new_empty((shape[0], shape[2])) if need_dh0 else None
-    h0, lengths, y, dy, dhT = _placed(h0), _placed(lengths), _placed(y), _placed(dy), _placed(dhT)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_recur_workspace_size(desc, L.KAN_PASS_BACKWARD), x)
-    L.check(lib.kan_recur_backward(desc, x.data_ptr(), g.data_ptr(), _addr(h0), _addr(lengths), y.data_ptr(),
-                                   dy.data_ptr(), _addr(dhT), dx.data_ptr(), dg.data_ptr(), _addr(dh0), _addr(buf),
-                                   n, _raw_stream(dev)), "kan_recur_backward")
+    L.check(lib.kan_recur_backward(desc, x.data_ptr(), g.data_ptr(), h0_at, lengths_at, y_at, dy_at, dhT_at,
+                                   dx.data_ptr(), dg.data_ptr(), _addr(dh0), _addr(buf), n, _raw_stream(dev)),
+            "kan_recur_backward")
     return dx, dg, dh0
 
 
@@ -542,6 +564,10 @@ def kan_recur_step(x, g, state, slots=None, out=None):
     _whole(state, "state", _F32, dev)
     if slots is not None:
         _whole(slots, "slots", _I32, dev, shape[:1])
+    slots_at = _addr(slots)
+    if (slots_at or 0) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_recur_step(x, g, state, _placed(slots), out)
     B, D = shape
     xs, gs = x.stride(0), g.stride(0)
     desc = L.kan_recur_desc_t(B, 1, D, xs, xs, gs, gs, 0, 0, 0, 0, _DTYPES[x.dtype], L.KAN_F32)
@@ -550,8 +576,7 @@ def kan_recur_step(x, g, state, slots=None, out=None):
     else:
         y = out
         _whole(y, "y", _F32, dev, shape)
-    slots = _placed(slots)
-    L.check(L.lib().kan_recur_step(desc, state.shape[0], x.data_ptr(), g.data_ptr(), state.data_ptr(), _addr(slots),
+    L.check(L.lib().kan_recur_step(desc, state.shape[0], x.data_ptr(), g.data_ptr(), state.data_ptr(), slots_at,
                                    y.data_ptr(), _raw_stream(dev)), "kan_recur_step")
     return y
 
@@ -602,14 +627,16 @@ def kan_distill_forward(z, ids, t, temperature=1.0, weight=None, ws=None):
     teacher's, the softmax of its top logits ``t [N, K] / tau`` over the tokens
     ``ids [N, K]`` (int32 or int64; ids outside ``[0, V)`` are absent)."""
     dev = _distill_inputs(z, ids, t, weight)
+    ids_at, t_at, weight_at = ids.data_ptr(), t.data_ptr(), _addr(weight)
+    if (ids_at | t_at | (weight_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_distill_forward(z, _placed(ids), _placed(t), temperature, _placed(weight), ws)
     desc = distill_desc(z, ids, t, temperature)
     loss = z.new_empty(z.shape[:1], dtype=torch.float32)
     lse = torch.empty_like(loss)
-    ids, t, weight = _placed(ids), _placed(t), _placed(weight)
     buf, n = (None, 0) if ws is None else _check_ws(ws, z.device)
-    L.check(L.lib().kan_distill_forward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
-                                        loss.data_ptr(), lse.data_ptr(), _addr(buf), n, _raw_stream(dev)),
-            "kan_distill_forward")
+    L.check(L.lib().kan_distill_forward(desc, z.data_ptr(), ids_at, t_at, weight_at, loss.data_ptr(), lse.data_ptr(),
+                                        _addr(buf), n, _raw_stream(dev)), "kan_distill_forward")
     return loss, lse
 
 
@@ -619,12 +646,16 @@ def kan_distill_backward(z, ids, t, lse, dloss, temperature=1.0, weight=None, gr
     dev = _distill_inputs(z, ids, t, weight)
     _whole(lse, "lse", _F32, dev, z.shape[:1])
     _whole(dloss, "dloss", _F32, dev, z.shape[:1])
+    ids_at, t_at, weight_at, lse_at, dloss_at = (ids.data_ptr(), t.data_ptr(), _addr(weight), lse.data_ptr(),
+                                                 dloss.data_ptr())
+    if (ids_at | t_at | (weight_at or 0) | lse_at | dloss_at) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_distill_backward(z, _placed(ids), _placed(t), _placed(lse), _placed(dloss), temperature,
+                                        _placed(weight), grad_dtype, out)
     dz = _distill_grad(z, out, grad_dtype, dev)
     desc = distill_desc(z, ids, t, temperature, dz)
-    ids, t, weight, lse, dloss = _placed(ids), _placed(t), _placed(weight), _placed(lse), _placed(dloss)
-    L.check(L.lib().kan_distill_backward(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight),
-                                         lse.data_ptr(), dloss.data_ptr(), dz.data_ptr(), _raw_stream(dev)),
-            "kan_distill_backward")
+    L.check(L.lib().kan_distill_backward(desc, z.data_ptr(), ids_at, t_at, weight_at, lse_at, dloss_at, dz.data_ptr(),
+                                         _raw_stream(dev)), "kan_distill_backward")
     return dz
 
 
@@ -632,12 +663,15 @@ def kan_distill_step(z, ids, t, temperature=1.0, weight=None, grad_dtype=torch.f
     """``(loss [N], dz [N, V])`` in one call: the rows' losses and the gradient of
     their sum (put the mean's 1/N into ``weight``)."""
     dev = _distill_inputs(z, ids, t, weight)
+    ids_at, t_at, weight_at = ids.data_ptr(), t.data_ptr(), _addr(weight)
+    if (ids_at | t_at | (weight_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_distill_step(z, _placed(ids), _placed(t), temperature, _placed(weight), grad_dtype, out, ws)
     dz = _distill_grad(z, out, grad_dtype, dev)
     desc = distill_desc(z, ids, t, temperature, dz)
     loss = z.new_empty(z.shape[:1], dtype=torch.float32)
-    ids, t, weight = _placed(ids), _placed(t), _placed(weight)
     lib = L.lib()
     buf, n = _sized_ws(ws, lib.kan_distill_workspace_size(desc), z)
-    L.check(lib.kan_distill_step(desc, z.data_ptr(), ids.data_ptr(), t.data_ptr(), _addr(weight), loss.data_ptr(),
-                                 dz.data_ptr(), _addr(buf), n, _raw_stream(dev)), "kan_distill_step")
+    L.check(lib.kan_distill_step(desc, z.data_ptr(), ids_at, t_at, weight_at, loss.data_ptr(), dz.data_ptr(),
+                                 _addr(buf), n, _raw_stream(dev)), "kan_distill_step")
     return loss, dz
