@@ -11,7 +11,7 @@
 //     del_t = dy_t + c_{t+1},  dx_t = u_t del_t,
 //     dg_t  = f_t (h_{t-1} - x_t) dx_t,  dh0 = c_0.
 //
-// Both shares are computed to their own last places: a share that rounds to 1
+// Both shares are computed relative to their own size: a share that rounds to 1
 // has lost the digits of the other one, which decide how long a memory is (f
 // near 1) or how much of a large state is left (u near 1).  Where a state goes
 // on from tile to tile, or from call to call in the single step, it changes by
@@ -45,8 +45,9 @@ namespace kan {
 
 namespace {
 
-// The shares of x and of the state, u = sigmoid(-g) and f = sigmoid(g), each to
-// a few ulp of its own size.
+// The shares of x and of the state, u = sigmoid(-g) and f = sigmoid(g).  The
+// smaller one is within (1.3 |g| + 12) 2^-24 of its own size: exp's argument,
+// |g| log2 e, rounds.  The larger one is within a few ulp.
 struct Shares {
     float u, f;
     __device__ __forceinline__ static Shares of(float g) {
