@@ -483,7 +483,8 @@ int kan_recur_step(const kan_recur_desc_t* desc, int64_t S, const void* x, const
  * A row with w_b = 0, with no teacher entry (all absent or all t = -inf), or
  * whose z are all -inf has loss 0 and dz 0 (lse is that of its z all the same);
  * the backward and the step do not read rows with w_b = 0.  A teacher entry with
- * t = -inf adds nothing.  Layouts: z [N, V] in `dtype` with row stride z_row,
+ * t = -inf adds nothing.  A row's sums start at its first 128-byte line, so that
+ * their last bits go with where in a line the row starts.  Layouts: z [N, V] in `dtype` with row stride z_row,
  * dz [N, V] in `grad_dtype` with row stride dz_row; ids [N, K] (id_dtype),
  * t [N, K] in `teacher_dtype`; w (NULL: all 1), loss, lse, dloss [N] float32. */
 typedef struct {

@@ -7,8 +7,8 @@
 // K is small beside V: reading z once and writing dz once is the work, so HBM
 // traffic bounds it; the arithmetic is one or two exponentials and about six
 // operations an element.  Measured: step of 8192 x 65536 float32 760 us (4.1 GB,
-// 5.4 TB/s), backward of 4096 x 50021 bf16 157 us (784 MB, 5.0 TB/s), forward of
-// 4096 x 50021 float32 128 us (820 MB read, 6.4 TB/s).  A row's maximum m and
+// 5.4 TB/s), backward of 4096 x 50021 bf16 156 us (784 MB, 5.0 TB/s), forward of
+// 4096 x 50021 float32 124 us (820 MB read, 6.6 TB/s).  A row's maximum m and
 // s = sum exp((z - m) / tau) are kept, not their sum in lse: the loss is formed
 // from z_{id} - m and log s, which are small where lse and z / tau may be large.
 //
@@ -16,8 +16,8 @@
 // vectors of 16 bytes a thread, 256 KB for 1024 threads; what is left of a
 // longer row is read again from the caches), so z is read once though its
 // gradient needs m and s first; the forward streams the row with a running
-// maximum and sum.  The teacher's part is done while the row's loads are in
-// flight.  The step's stores are plain: streamed ones gained 2% at 8192 x 65536
+// maximum and sum.  The step does the teacher's part while the row's loads are
+// in flight.  Its stores are plain: streamed ones gained 2% at 8192 x 65536
 // and lost 4% at 4096 x 50021.
 //
 // The teacher's p are taken off at K of the row's elements.  Every element is
@@ -477,8 +477,8 @@ hipError_t step_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t
     constexpr int64_t per = NV * VE;
     const int64_t threads = std::max((d.V + per - 1) / per, d.K);
     // short rows leave most of the registers free, and their time is latency:
-    // more of them at a time (16384 x 4000 bf16 113 -> 83 us, 16384 x 3000 float32
-    // 89 -> 74)
+    // more of them at a time (16384 x 4000 bf16 129 -> 88 us, 16384 x 3000 float32
+    // 121 -> 85)
     if (d.K <= 64 && 4 * d.V <= 64 * per) return row_t<TS, TG, 64, NV / 4, true, false>(d, a, s);
     if (d.K <= 256 && 4 * d.V <= 256 * per) return row_t<TS, TG, 256, NV / 4, true, false>(d, a, s);
     if (threads <= 256) return row_t<TS, TG, 256, NV, true, false>(d, a, s);
@@ -486,8 +486,9 @@ hipError_t step_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t
     return row_t<TS, TG, 1024, NV, true, false>(d, a, s);
 }
 
-// Few long rows take a block of 1024 threads each (64 x 131072 float32: 23 us with
-// 256), many rows one of 256 (16384 x 4000 bf16: 47 us, 87 with 512).
+// Few long rows take a block of 1024 threads each (64 x 131072 float32: 16 us, 31
+// with 256), many rows one of 256 (16384 x 4000 bf16, K = 128: 45 us, 84 with 512),
+// short ones with few teacher's logits a wave (K = 64: 32 us, 43 with 256).
 template <typename TS, bool STREAM>
 hipError_t fwd_s(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
     if (d.K > 256 || (d.N <= 512 && d.V >= 8192)) return row_t<TS, TS, 1024, 0, false, STREAM>(d, a, s);
@@ -495,7 +496,7 @@ hipError_t fwd_s(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t 
     return row_t<TS, TS, 64, 0, false, STREAM>(d, a, s);
 }
 // Past kStreamBytes the logits cannot stay in the caches for the backward pass
-// and are read as streamed data (4096 x 50021 float32: 133 -> 119 us).
+// and are read as streamed data (4096 x 50021: float32 141 -> 124 us, bf16 76 -> 69).
 template <typename TS>
 hipError_t fwd_t(const kan_distill_desc_t& d, const DistillArgs& a, hipStream_t s) {
     return d.N * d.V * (int64_t)sizeof(TS) >= kStreamBytes ? fwd_s<TS, true>(d, a, s) : fwd_s<TS, false>(d, a, s);
@@ -506,13 +507,14 @@ hipError_t bwd_n(const kan_distill_desc_t& d, const DistillArgs& a, const float2
     constexpr int VE = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;     // 16 bytes of the wider type
     constexpr int64_t round = NT * VE;
     // Blocks of one round of loads each, up to 32768 of them: 4096 x 50021 takes
-    // 175 us (bf16) and 340 us (float32) with a block to a row, 162 and 308 with
-    // six.
+    // 181 us (bf16) and 348 us (float32) with a block to a row, 163 and 319 cut (all
+    // of these on one card; another one took 156).
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((32768 + d.N - 1) / d.N, d.V / (round * DU)));
     const int64_t part = round_up((d.V + parts - 1) / parts, round), n = (d.V + part - 1) / part;
     const dim3 grid((unsigned)(d.N * n));
-    // streamed stores past kStreamBytes: 4096 x 50021 bf16 197 -> 170 us, float32
-    // 372 -> 331 (a step of few rows does not come near)
+    // streamed stores past kStreamBytes: 4096 x 50021 bf16 166 -> 163 us, float32
+    // 322 -> 319, and 197 -> 170 and 372 -> 331 with a block to a row (a step of few
+    // rows does not come near)
     if (!STEP && d.N * d.V * (int64_t)sizeof(TG) >= kStreamBytes)
         hipLaunchKernelGGL((distill_bwd_kernel<TS, TG, NT, VE, !STEP, STEP>), grid, dim3(NT), 0, s, d, a, (int)n, part,
                            sums, n_sums);

@@ -32,8 +32,8 @@
 //
 // Memory traffic bounds it: 8 x 4096 x 2048, bf16 forward 104 us (537 MB, 5.2
 // TB/s), float32 backward 316 us (1.61 GB, 5.1 TB/s), 1 x 65536 x 1024 float32
-// forward 162 us (805 MB, 5.0 TB/s: 13 for the segments' runs, 145 for the rows),
-// where a copy runs at 5.0 TB/s.  The
+// forward 166 us (805 MB, 4.9 TB/s: 13 for the segments' runs, 146 for the rows, 4
+// for the launch that looks at marks), where a copy runs at 5.0 TB/s.  The
 // arithmetic (two transcendentals and about 25 operations an element forward)
 // keeps the vector units busy for half of that.
 #include <type_traits>
@@ -356,7 +356,7 @@ struct Marked {
 // where the share that is left of what comes before is at most 2^-64 in every
 // channel of the block: less than half a last place of what follows, unless the
 // state that is dropped was 2^40 times as large.  (2^-25 is half a last place of
-// a state of the same size, and 7 us of the 162 less; but what is left of one
+// a state of the same size, and 7 us less; but what is left of one
 // large input would then end at a segment's start.)  Common gates forget in a
 // tile or two (128 rows by 64 channels); gates that do not are read to the
 // segment's start.

@@ -152,8 +152,11 @@ RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
     // time goes with the lines to the power 0.75 or so (8 x 4096 x 2048 bf16
     // forward: 106 us with 16 lanes, 126 with 8; 70 x 1531 x 770 bf16 backward:
     // 461 with 32, 529 with 16, 364 with 16 at 768 channels).  Segments read a
-    // little twice and take a launch more (1 x 65536 x 1024 float32 forward:
-    // 644 us whole, 162 in segments).
+    // little twice and take two launches more (1 x 65536 x 1024 float32 forward:
+    // 564 us whole with 4 lanes, 172 in segments).  Of 19 shapes between 1 x 2048 x
+    // 1024 and 8 x 1024 x 768, timed with each of the plans below, the chosen one
+    // is the best or up to 13% over it (7 x 1531 x 770 bf16, lengths drawn:
+    // backward 62 us, 69 whole with 8 lanes; forward 38, 33 whole with 8 lanes).
     constexpr int64_t kCUs = 256;
     const bool forward = pass == KAN_PASS_FORWARD;
     RecurPlan p;
@@ -217,8 +220,11 @@ RecurPlan recur_plan(const kan_recur_desc_t& d, int pass) {
 DistillPlan distill_plan(const kan_distill_desc_t& d) {
     // A step of few long rows is cut over blocks: its maxima and sums in one
     // launch, the gradient in a second.  With a block to a row its time is one
-    // compute unit's arithmetic: 131072 bf16 logits take 22 us for one row and 25
-    // for 64, cut 16 and 16; at 65536 logits it is 13 whole, 16 cut.
+    // compute unit's arithmetic.  Whole and cut, us: one row of 131072 logits 19.8
+    // and 13.8 (bf16 22.6, 13.8), 64 rows 31.0 and 25.4 (26.6, 17.2); 64 rows of
+    // 98304 24.4 and 21.3 (22.2, 16.3); one row of 65536 11.5 and 14.2 (13.9, 13.9).
+    // With more rows than 64 the gain ends, at 96 in float32 (34.9, 33.9; 98304
+    // logits: 26.4, 29.3) and between 128 and 192 in bf16.
     DistillPlan p{1, d.V, 0};
     if (d.N > 0 && d.N <= 64 && d.V >= 98304) {
         const int64_t want = std::min<int64_t>(std::min<int64_t>(64, 512 / d.N), d.V / 4096);
