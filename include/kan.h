@@ -514,6 +514,127 @@ int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* 
                      const float* w, float* loss, void* dz, void* workspace, size_t workspace_bytes,
                      void* stream);
 
+/* ---- Gated delta rule and the join between blocks ---------------------------
+ * Two more operators of a model over tokens, with the conventions of the
+ * section above: a mixer of a sequence's rows whose state is a matrix for each
+ * head, and what stands between two blocks of a model.
+ *
+ * Delta rule: each of Hv heads of a sequence has a state S [Dk, Dv].  Row t lets
+ * it decay, corrects what the state answers to the key k_t towards the value
+ * v_t, and answers the query q_t:
+ *
+ *     S' = exp(g_t) S_{t-1},   w_t = v_t - S'^T k_t,   u_t = beta_t w_t
+ *     S_t = S' + k_t u_t^T,    y_t = scale S_t^T q_t,  S_{-1} = h0 (0 if NULL)
+ *
+ * for t < len = lengths[b] limited to [0, T] (T if `lengths` is NULL); y is 0
+ * from there to T, hT = S_{len-1} (h0 where len = 0), and nothing of a row past
+ * len is used.  With KAN_DELTA_UNIT q and k are divided by sqrt(|.|^2 + 1e-6)
+ * first.  Head h of v, g, beta, y and S uses head h / (Hv / Hk) of q and k.
+ * g is the logarithm of the decay (a decay of 0, g = -inf, is as good as
+ * g = -128); states grow where g > 0 or beta |k|^2 > 2.  Backward, with dy and
+ * the gradient dhT of hT (0 if NULL), gives the gradients of q, k, v, g, beta
+ * and h0; those of q and k are summed over the heads that share them, and those
+ * of rows past len are 0.
+ *
+ * Rows go through in chunks of 64, whose correction is a triangular system.
+ * All of it is float32 with values of more than 24 bits for sums of g, in a fixed
+ * order.  A NaN or an infinity in a row reaches the rows of its chunk, earlier
+ * ones included, and all later ones of its sequence and heads.
+ *
+ * Layouts: q, k [B, T, Hk, Dk], v [B, T, Hv, Dv] and their gradients in `dtype`
+ * with a stride (elements) for each of sequence, row and head, so that they may
+ * be slices of one projection; y, dy [B, T, Hv, Dv] in `dtype`, g, beta, dg,
+ * dbeta [B, T, Hv] and h0, hT, dhT, dh0 [B, Hv, Dk, Dv] float32, contiguous. */
+#define KAN_DELTA_UNIT 1
+typedef struct {
+    int64_t seq, row, head;         /* strides, >= 0 */
+} kan_heads_t;
+typedef struct {
+    int64_t B;                      /* sequences, >= 0 */
+    int64_t T;                      /* rows of a sequence, >= 0; B Hv ceil(T / 64) at most 2^23 */
+    int64_t Hk, Hv;                 /* heads, >= 1; Hv a multiple of Hk; B Hv at most 2^18 */
+    int64_t Dk;                     /* 1 .. 128 */
+    int64_t Dv;                     /* 1 .. 1024 */
+    kan_heads_t q, k, v;            /* strides of the inputs */
+    kan_heads_t dq, dk, dv;         /* strides of the gradients (backward only) */
+    int32_t dtype;                  /* kan_dtype_t: storage of q, k, v, y, dy, dq, dk, dv */
+    int32_t flags;                  /* 0 or KAN_DELTA_UNIT */
+    float scale;                    /* finite */
+} kan_delta_desc_t;
+
+/* Bytes of workspace a pass (kan_pass_t) needs (SIZE_MAX if `desc` is invalid):
+ * the chunks' triangular matrices; for the backward also the states at the
+ * chunks' starts and their gradients, and the rows' corrections. */
+size_t kan_delta_workspace_size(const kan_delta_desc_t* desc, int pass);
+/* y and hT out (hT may be NULL). */
+int kan_delta_forward(const kan_delta_desc_t* desc, const void* q, const void* k, const void* v, const float* g,
+                      const float* beta, const float* h0, const int32_t* lengths, void* y, float* hT,
+                      void* workspace, size_t workspace_bytes, void* stream);
+/* All gradients out (dh0 may be NULL). */
+int kan_delta_backward(const kan_delta_desc_t* desc, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, const float* h0, const int32_t* lengths, const void* dy,
+                       const float* dhT, void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dh0,
+                       void* workspace, size_t workspace_bytes, void* stream);
+/* One row of each of B sequences (desc->T is 1): the states live in a pool
+ * state [S, Hv, Dk, Dv] float32, sequence b's in row slots[b] (row b if `slots`
+ * is NULL; then S >= B), which is read and replaced.  A sequence whose slot is
+ * outside [0, S) is skipped and its y is 0.  The slots of one call must differ
+ * from each other. */
+int kan_delta_step(const kan_delta_desc_t* desc, int64_t S, const void* q, const void* k, const void* v,
+                   const float* g, const float* beta, float* state, const int32_t* slots, void* y, void* stream);
+
+/* Join: a block's output h, through its norm and gate, onto the residual rows
+ * r, and the norm of the sum for the next block:
+ *
+ *     t = h n1 (h without KAN_JOIN_POST),   n1 = 1 / sqrt(mean(h^2) + eps)
+ *     y = r + scale act(gate) w_post t
+ *     x = w_pre y n2 (with KAN_JOIN_PRE),   n2 = 1 / sqrt(mean(y^2) + eps)
+ *
+ * row by row over D columns.  r, gate, w_post and w_pre may be NULL (0, 1, 1, 1);
+ * n2 and x are of y before it is rounded to its storage.  The factors n1 and n2
+ * (1 where there is no norm) are kept for the backward:
+ *
+ *     z = y n2,  c = w_pre dx,  d = dy + n2 (c - z mean(c z)),   dr = d
+ *     e = scale act(gate) d,    dgate = scale act'(gate) w_post t d
+ *     dh = n1 (w_post e - t mean(w_post e t)) (w_post e without KAN_JOIN_POST)
+ *     dw_post = sum over rows of e t,   dw_pre = sum over rows of dx z
+ *
+ * y stands for itself as it was stored.  dy (NULL: 0) is the gradient of y from
+ * its other uses, dx (NULL: 0) that of x.  Weights' sums go row by row within a
+ * block and then block by block, in a fixed order.
+ * Layouts: h, gate, dh, dgate [N, D] in `dtype`, r, y, dy, dr [N, D] in
+ * `res_dtype`, x, dx [N, D] in `row_dtype`, h, r and gate with row strides, the
+ * rest contiguous; weights [D] and their gradients, stats [2, N] (n1, then n2)
+ * float32. */
+#define KAN_JOIN_POST 1
+#define KAN_JOIN_PRE 2
+typedef enum { KAN_GATE_SILU = 0, KAN_GATE_SIGMOID = 1 } kan_gate_t;
+typedef struct {
+    int64_t N;                      /* rows, 0 .. 2^25 (2^23 where D > 1024, 2^21 where D > 4096) */
+    int64_t D;                      /* columns, 1 .. 8192 */
+    int64_t h_row, r_row, gate_row; /* strides of h, r and gate, >= 0 */
+    int32_t dtype;                  /* kan_dtype_t: storage of h and gate */
+    int32_t res_dtype;              /* kan_dtype_t: storage of r and y */
+    int32_t row_dtype;              /* kan_dtype_t: storage of x */
+    int32_t activation;             /* kan_gate_t */
+    int32_t flags;                  /* KAN_JOIN_POST, KAN_JOIN_PRE */
+    float scale;                    /* finite */
+    float eps;                      /* finite, >= 0 */
+} kan_join_desc_t;
+
+/* Bytes of workspace kan_join_backward needs (SIZE_MAX if `desc` is invalid):
+ * the blocks' sums of the weights' gradients. */
+size_t kan_join_workspace_size(const kan_join_desc_t* desc);
+/* y, stats and, with KAN_JOIN_PRE, x out. */
+int kan_join_forward(const kan_join_desc_t* desc, const void* h, const void* r, const void* gate,
+                     const float* w_post, const float* w_pre, void* y, void* x, float* stats, void* stream);
+/* dh out; dr, dgate (with `gate`), dw_post (with `w_post`) and dw_pre (with
+ * `w_pre`) where they are not NULL. */
+int kan_join_backward(const kan_join_desc_t* desc, const void* h, const void* y, const float* stats,
+                      const void* dy, const void* dx, const void* gate, const float* w_post, const float* w_pre,
+                      void* dh, void* dr, void* dgate, float* dw_post, float* dw_pre, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

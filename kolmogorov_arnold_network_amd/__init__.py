@@ -22,7 +22,9 @@ from .functional import (kan_forward, kan_forward_static, kan_backward, kan_prep
                          kan_embed_forward, kan_embed_backward, kan_embed_workspace_size, embed_desc,
                          kan_recur_forward, kan_recur_backward, kan_recur_step, kan_recur_workspace_size,
                          recur_desc, kan_distill_forward, kan_distill_backward, kan_distill_step,
-                         kan_distill_workspace_size, distill_desc)
+                         kan_distill_workspace_size, distill_desc,
+                         kan_delta_forward, kan_delta_backward, kan_delta_step, kan_delta_workspace_size, delta_desc,
+                         kan_join_forward, kan_join_backward, kan_join_workspace_size, join_desc)
 from .modules import (KANLayer, KANNetwork, KANFunction, KANGroupedActivation, KANSurfaceLayer,
                       GroupedFunction, SurfaceFunction, KANEmbedding, KANRecurrence, KANDistillLoss,
                       EmbedFunction, RecurFunction, DistillFunction)
@@ -36,5 +38,7 @@ __all__ = ["kan_forward", "kan_forward_static", "kan_backward", "kan_prepare", "
            "kan_recur_forward", "kan_recur_backward", "kan_recur_step", "kan_recur_workspace_size", "recur_desc",
            "kan_distill_forward", "kan_distill_backward", "kan_distill_step", "kan_distill_workspace_size",
            "distill_desc",
+           "kan_delta_forward", "kan_delta_backward", "kan_delta_step", "kan_delta_workspace_size", "delta_desc",
+           "kan_join_forward", "kan_join_backward", "kan_join_workspace_size", "join_desc",
            "KANGroupedActivation", "KANSurfaceLayer", "GroupedFunction", "SurfaceFunction",
            "KANEmbedding", "KANRecurrence", "KANDistillLoss", "EmbedFunction", "RecurFunction", "DistillFunction"]

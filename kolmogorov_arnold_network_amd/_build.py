@@ -17,7 +17,8 @@ LIB_NAME = "libkan_mi355x.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["kan_api.cpp", "kan_plan.cpp", "kan_gather.hip", "kan_grouped.hip", "kan_mfma.hip", "kan_static.hip",
-           "kan_token_api.cpp", "kan_embed.hip", "kan_recur.hip", "kan_distill.hip"]
+           "kan_token_api.cpp", "kan_embed.hip", "kan_recur.hip", "kan_distill.hip",
+           "kan_delta_api.cpp", "kan_delta.hip", "kan_join.hip"]
 
 # -packed-fp32-ops off: the compiler must not form packed float32 ALU ops.
 HIPCC_FLAGS = [

@@ -37,6 +37,13 @@ KAN_FLAG_TP_FORWARD = 4
 KAN_I32 = 0
 KAN_I64 = 1
 
+KAN_DELTA_UNIT = 1
+
+KAN_JOIN_POST = 1
+KAN_JOIN_PRE = 2
+KAN_GATE_SILU = 0
+KAN_GATE_SIGMOID = 1
+
 KAN_STATIC_SCRATCH_BYTES = 32 << 20     # kan_forward_static's device array
 
 ABI_VERSION = 1
@@ -48,7 +55,9 @@ EXPORTS = ("kan_abi_version", "kan_status_string", "kan_workspace_size", "kan_pr
            "kan_surface_workspace_size", "kan_surface_forward", "kan_surface_backward",
            "kan_embed_workspace_size", "kan_embed_forward", "kan_embed_backward",
            "kan_recur_workspace_size", "kan_recur_forward", "kan_recur_backward", "kan_recur_step",
-           "kan_distill_workspace_size", "kan_distill_forward", "kan_distill_backward", "kan_distill_step")
+           "kan_distill_workspace_size", "kan_distill_forward", "kan_distill_backward", "kan_distill_step",
+           "kan_delta_workspace_size", "kan_delta_forward", "kan_delta_backward", "kan_delta_step",
+           "kan_join_workspace_size", "kan_join_forward", "kan_join_backward")
 
 
 class kan_grid_t(ctypes.Structure):
@@ -92,6 +101,26 @@ class kan_distill_desc_t(ctypes.Structure):
                 ("z_row", ctypes.c_int64), ("dz_row", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("teacher_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("tau", ctypes.c_float)]
+
+
+class kan_heads_t(ctypes.Structure):
+    _fields_ = [("seq", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class kan_delta_desc_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+                ("Dk", ctypes.c_int64), ("Dv", ctypes.c_int64),
+                ("q", kan_heads_t), ("k", kan_heads_t), ("v", kan_heads_t),
+                ("dq", kan_heads_t), ("dk", kan_heads_t), ("dv", kan_heads_t),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class kan_join_desc_t(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("h_row", ctypes.c_int64), ("r_row", ctypes.c_int64), ("gate_row", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32), ("row_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class KanError(RuntimeError):
@@ -151,18 +180,22 @@ def lib():
     for name, desc, forward, backward in (
             ("embed", kan_embed_desc_t, [_vp] * 4, [_vp] * 4 + [_sz, _vp]),
             ("recur", kan_recur_desc_t, [_vp] * 7 + [_sz, _vp], [_vp] * 11 + [_sz, _vp]),
-            ("distill", kan_distill_desc_t, [_vp] * 7 + [_sz, _vp], [_vp] * 8)):
+            ("distill", kan_distill_desc_t, [_vp] * 7 + [_sz, _vp], [_vp] * 8),
+            ("delta", kan_delta_desc_t, [_vp] * 10 + [_sz, _vp], [_vp] * 16 + [_sz, _vp]),
+            ("join", kan_join_desc_t, [_vp] * 9, [_vp] * 14 + [_sz, _vp])):
         for fn, args in (("forward", forward), ("backward", backward)):
             f = getattr(L, "kan_%s_%s" % (name, fn))
             f.restype = ctypes.c_int
             f.argtypes = [P(desc)] + args
         f = getattr(L, "kan_%s_workspace_size" % name)
         f.restype = _sz
-        f.argtypes = [P(desc)] + ([ctypes.c_int] if name == "recur" else [])
+        f.argtypes = [P(desc)] + ([ctypes.c_int] if name in ("recur", "delta") else [])
     L.kan_recur_step.restype = ctypes.c_int
     L.kan_recur_step.argtypes = [P(kan_recur_desc_t), _i64] + [_vp] * 6
     L.kan_distill_step.restype = ctypes.c_int
     L.kan_distill_step.argtypes = [P(kan_distill_desc_t)] + [_vp] * 7 + [_sz, _vp]
+    L.kan_delta_step.restype = ctypes.c_int
+    L.kan_delta_step.argtypes = [P(kan_delta_desc_t), _i64] + [_vp] * 9
     if L.kan_abi_version() != ABI_VERSION:
         raise RuntimeError("libkan ABI version %d, binding expects %d"
                            % (L.kan_abi_version(), ABI_VERSION))

@@ -1,0 +1,61 @@
+// Launch plan and kernel launchers of the gated delta rule.
+#pragma once
+
+#include "kan_token.h"
+
+namespace kan {
+
+constexpr int kDeltaChunk = 64;      // rows of a chunk
+constexpr int kDeltaTile = 32;       // state columns of a scan's block
+constexpr int kDeltaMaxDk = 128;
+constexpr int kDeltaMaxDv = 1024;
+constexpr int64_t kDeltaMaxHeads = int64_t(1) << 18;    // B Hv
+constexpr int64_t kDeltaMaxChunks = int64_t(1) << 23;   // chunks of all heads, B Hv ceil(T / 64)
+
+// What the launches of a call leave each other, in the workspace.  A chunk-head
+// is one chunk of one value head: number (b Hv + h) chunks + n.
+struct DeltaPlan {
+    int dkp, dvp;                    // Dk up to 32, 64 or 128; Dv up to a multiple of the tile
+    int64_t chunks, heads;           // of a sequence; B Hv
+    size_t off_rows, off_G, off_P;   // [chunk-head][8][64], [64][64], [64][64] float32
+    size_t off_Gt, off_Pt;           // their transposes (backward)
+    size_t off_w, off_r;             // [chunk-head][64][dvp] float32 (backward)
+    size_t off_S, off_dS;            // [chunk-head][dkp][dvp] float32 (backward)
+    size_t off_dq, off_dk;           // [B][T][Hv][Dk] float32, where heads share keys (backward)
+    size_t ws;
+};
+DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass);
+
+struct DeltaArgs {
+    const void *q, *k, *v, *dy;
+    const float *g, *beta, *h0, *dhT;
+    const int32_t* lengths;
+    void *y, *dq, *dk, *dv;
+    float *hT, *dg, *dbeta, *dh0;
+};
+hipError_t launch_delta_fwd(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s);
+hipError_t launch_delta_bwd(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s);
+hipError_t launch_delta_step(const kan_delta_desc_t& d, int64_t S, const DeltaArgs& a, float* state,
+                             const int32_t* slots, hipStream_t s);
+
+// ---- join ----
+constexpr int64_t kJoinMaxD = 8192;
+int64_t join_max_rows(int64_t D);
+constexpr int kJoinMaxBlocks = 1024; // blocks of a backward pass, each with its own sums for the weights
+struct JoinPlan {
+    int lanes, vecs;                 // threads of a row, and vectors of four elements that each holds
+    unsigned blocks;
+    size_t ws;                       // [blocks][2][D] float32 sums of the weights' gradients (backward)
+};
+JoinPlan join_plan(const kan_join_desc_t& d, int pass);
+
+struct JoinArgs {
+    const void *h, *r, *gate, *dy, *dx, *y_in;
+    const float *w_post, *w_pre, *stats_in;
+    void *y, *x, *dh, *dr, *dgate;
+    float *stats, *dw_post, *dw_pre;
+};
+hipError_t launch_join_fwd(const kan_join_desc_t& d, const JoinPlan& p, const JoinArgs& a, hipStream_t s);
+hipError_t launch_join_bwd(const kan_join_desc_t& d, const JoinPlan& p, const JoinArgs& a, char* ws, hipStream_t s);
+
+}  // namespace kan

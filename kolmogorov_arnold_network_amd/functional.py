@@ -675,3 +675,271 @@ def kan_distill_step(z, ids, t, temperature=1.0, weight=None, grad_dtype=torch.f
     L.check(lib.kan_distill_step(desc, z.data_ptr(), ids_at, t_at, weight_at, loss.data_ptr(), dz.data_ptr(),
                                  _addr(buf), n, _raw_stream(dev)), "kan_distill_step")
     return loss, dz
+
+
+def _strides(t):
+    """``kan_heads_t`` of ``[B, T, H, D]``; a dimension of one entry may have any stride."""
+    n, s = t.shape, t.stride()
+    return L.kan_heads_t(*(s[i] if n[i] > 1 else 0 for i in range(3)))
+
+
+def _row_strides(t):
+    """``kan_heads_t`` of one row ``[B, H, D]`` of each sequence."""
+    n, s = t.shape, t.stride()
+    return L.kan_heads_t(s[0] if n[0] > 1 else 0, 0, s[1] if n[1] > 1 else 0)
+
+
+_NO_STRIDES = L.kan_heads_t(0, 0, 0)
+
+
+def delta_desc(q, k, v, scale=None, unit=False, dq=None, dk=None, dv=None):
+    """``kan_delta_desc_t`` of ``q``, ``k [B, T, Hk, Dk]`` and ``v [B, T, Hv, Dv]`` (strides of
+    sequences, rows and heads are free) and, for the backward pass, their gradients."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, T, Hk, Dk] and v [B, T, Hv, Dv]")
+    if k.shape != q.shape:
+        raise ValueError("k must be %s, got %s" % (tuple(q.shape), tuple(k.shape)))
+    if v.shape[:2] != q.shape[:2]:
+        raise ValueError("v must be [%d, %d, Hv, Dv], got %s" % (*q.shape[:2], tuple(v.shape)))
+    B, T, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    if Hk < 1 or Hv % Hk:
+        raise ValueError("the %d heads of v must be a multiple of the %d of q and k" % (Hv, Hk))
+    grads = (_NO_STRIDES,) * 3 if dq is None else (_strides(dq), _strides(dk), _strides(dv))
+    return L.kan_delta_desc_t(B, T, Hk, Hv, Dk, Dv, _strides(q), _strides(k), _strides(v), *grads, _DTYPES[q.dtype],
+                              L.KAN_DELTA_UNIT if unit else 0, Dk ** -0.5 if scale is None else scale)
+
+
+def kan_delta_workspace_size(desc, pass_):
+    return _valid_size(L.lib().kan_delta_workspace_size(desc, int(pass_)), "delta rule")
+
+
+def _delta_inputs(q, k, v, g, beta, lead):
+    """Checks of what the passes and the step share; ``lead``: the dimensions before the heads."""
+    dev = _dev(q, "q")
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError("q, k must be [%s, Hk, Dk] and v [%s, Hv, Dv]" % (("B", "B") if lead == 1 else ("B, T",) * 2))
+    _rows(q, "q", _DTYPES, dev)
+    _rows(k, "k", (q.dtype,), dev, q.shape)
+    _rows(v, "v", (q.dtype,), dev)
+    if v.shape[:lead] != q.shape[:lead]:
+        raise ValueError("v must start with %s, got %s" % (tuple(q.shape[:lead]), tuple(v.shape)))
+    _whole(g, "g", _F32, dev, v.shape[:-1])
+    _whole(beta, "beta", _F32, dev, v.shape[:-1])
+    return dev
+
+
+def _delta_states(dev, v, q, **states):
+    shape = (v.shape[0], v.shape[-2], q.shape[-1], v.shape[-1])
+    for name, t in states.items():
+        if t is not None:
+            _whole(t, name, _F32, dev, shape)
+    return shape
+
+
+def kan_delta_forward(q, k, v, g, beta, h0=None, lengths=None, scale=None, unit=False, ws=None, out=None):
+    """``(y [B, T, Hv, Dv], hT [B, Hv, Dk, Dv])`` of the gated delta rule: each head's
+    state decays by ``exp(g_t)``, is corrected at the key ``k_t`` by ``beta_t`` times its
+    distance from ``v_t``, and answers the query, ``y_t = scale S_t^T q_t``.
+
+    ``q``, ``k [B, T, Hk, Dk]`` and ``v [B, T, Hv, Dv]`` share a dtype, which ``y`` has
+    too, and may have any strides but the last; ``Hv`` is a multiple of ``Hk``.  ``g``,
+    ``beta [B, T, Hv]`` float32; ``h0`` float32 (default 0), ``lengths [B]`` int32 (default
+    T; ``y`` is 0 past a length); ``scale`` (default ``Dk ** -0.5``); ``unit``: rows of q and
+    k are made unit vectors first."""
+    dev = _delta_inputs(q, k, v, g, beta, 2)
+    shape = _delta_states(dev, v, q, h0=h0)
+    if lengths is not None:
+        _whole(lengths, "lengths", _I32, dev, q.shape[:1])
+    g_at, beta_at, h0_at, lengths_at = g.data_ptr(), beta.data_ptr(), _addr(h0), _addr(lengths)
+    if (g_at | beta_at | (h0_at or 0) | (lengths_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_delta_forward(q, k, v, _placed(g), _placed(beta), _placed(h0), _placed(lengths), scale, unit,
+                                     ws, out)
+    desc = delta_desc(q, k, v, scale, unit)
+    if out is None:
+        y = q.new_empty(v.shape)
+    else:
+        y = out
+        _whole(y, "y", (q.dtype,), dev, v.shape)
+    hT = g.new_empty(shape)
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_delta_workspace_size(desc, L.KAN_PASS_FORWARD), q)
+    L.check(lib.kan_delta_forward(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), g_at, beta_at, h0_at, lengths_at,
+                                  y.data_ptr(), hT.data_ptr(), _addr(buf), n, _raw_stream(dev)), "kan_delta_forward")
+    return y, hT
+
+
+def kan_delta_backward(q, k, v, g, beta, dy, h0=None, lengths=None, dhT=None, scale=None, unit=False, need_dh0=None,
+                       dq=None, dk=None, dv=None, ws=None):
+    """``(dq, dk, dv, dg, dbeta, dh0)`` from ``dy [B, T, Hv, Dv]`` (and ``dhT [B, Hv, Dk,
+    Dv]``).  ``dq``, ``dk`` and ``dv`` have the inputs' dtype and are written into the given
+    tensors (any strides but the last, for instance slices of one array's rows) or into
+    new ones; ``dg``, ``dbeta`` float32; ``dh0`` float32 (default: with ``h0``)."""
+    dev = _delta_inputs(q, k, v, g, beta, 2)
+    shape = _delta_states(dev, v, q, h0=h0, dhT=dhT)
+    if lengths is not None:
+        _whole(lengths, "lengths", _I32, dev, q.shape[:1])
+    _whole(dy, "dy", (q.dtype,), dev, v.shape)
+    if (dq is None) != (dk is None) or (dq is None) != (dv is None):
+        raise ValueError("give all of dq, dk and dv or none")
+    g_at, beta_at, h0_at, lengths_at = g.data_ptr(), beta.data_ptr(), _addr(h0), _addr(lengths)
+    dy_at, dhT_at = dy.data_ptr(), _addr(dhT)
+    if (g_at | beta_at | (h0_at or 0) | (lengths_at or 0) | dy_at | (dhT_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_delta_backward(q, k, v, _placed(g), _placed(beta), _placed(dy), _placed(h0), _placed(lengths),
+                                      _placed(dhT), scale, unit, need_dh0, dq, dk, dv, ws)
+    if dq is None:
+        dq, dk, dv = q.new_empty(q.shape), q.new_empty(q.shape), q.new_empty(v.shape)
+    else:
+        _rows(dq, "dq", (q.dtype,), dev, q.shape)
+        _rows(dk, "dk", (q.dtype,), dev, q.shape)
+        _rows(dv, "dv", (q.dtype,), dev, v.shape)
+    desc = delta_desc(q, k, v, scale, unit, dq, dk, dv)
+    dg, dbeta = torch.empty_like(g), torch.empty_like(beta)
+    need_dh0 = h0 is not None if need_dh0 is None else need_dh0
+    dh0 = g.new_empty(shape) if need_dh0 else None
+    lib = L.lib()
+    buf, n = _sized_ws(ws, lib.kan_delta_workspace_size(desc, L.KAN_PASS_BACKWARD), q)
+    L.check(lib.kan_delta_backward(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), g_at, beta_at, h0_at, lengths_at,
+                                   dy_at, dhT_at, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+                                   dbeta.data_ptr(), _addr(dh0), _addr(buf), n, _raw_stream(dev)),
+            "kan_delta_backward")
+    return dq, dk, dv, dg, dbeta, dh0
+
+
+def kan_delta_step(q, k, v, g, beta, state, slots=None, scale=None, unit=False, out=None):
+    """One row of each sequence: ``state [S, Hv, Dk, Dv]`` float32 is read and replaced in
+    entries ``slots [B]`` (int32, all different; default ``0 .. B-1``) and ``y [B, Hv, Dv]``
+    in the inputs' dtype is returned; a slot outside the pool is skipped.  ``q``, ``k [B,
+    Hk, Dk]``, ``v [B, Hv, Dv]``, ``g``, ``beta [B, Hv]`` as in ``kan_delta_forward``."""
+    dev = _delta_inputs(q, k, v, g, beta, 1)
+    B, Hk, Dk = q.shape
+    Hv, Dv = v.shape[1:]
+    if Hk < 1 or Hv % Hk:
+        raise ValueError("the %d heads of v must be a multiple of the %d of q and k" % (Hv, Hk))
+    if state.dim() != 4 or state.shape[1:] != (Hv, Dk, Dv):
+        raise ValueError("state must be [S, %d, %d, %d], got %s" % (Hv, Dk, Dv, tuple(state.shape)))
+    _whole(state, "state", _F32, dev)
+    if slots is not None:
+        _whole(slots, "slots", _I32, dev, q.shape[:1])
+    g_at, beta_at, slots_at = g.data_ptr(), beta.data_ptr(), _addr(slots)
+    if (g_at | beta_at | (slots_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_delta_step(q, k, v, _placed(g), _placed(beta), state, _placed(slots), scale, unit, out)
+    desc = L.kan_delta_desc_t(B, 1, Hk, Hv, Dk, Dv, _row_strides(q), _row_strides(k), _row_strides(v), _NO_STRIDES,
+                              _NO_STRIDES, _NO_STRIDES, _DTYPES[q.dtype], L.KAN_DELTA_UNIT if unit else 0,
+                              Dk ** -0.5 if scale is None else scale)
+    if out is None:
+        y = q.new_empty(v.shape)
+    else:
+        y = out
+        _whole(y, "y", (q.dtype,), dev, v.shape)
+    L.check(L.lib().kan_delta_step(desc, state.shape[0], q.data_ptr(), k.data_ptr(), v.data_ptr(), g_at, beta_at,
+                                   state.data_ptr(), slots_at, y.data_ptr(), _raw_stream(dev)), "kan_delta_step")
+    return y
+
+
+_ACTIVATIONS = {"silu": L.KAN_GATE_SILU, "sigmoid": L.KAN_GATE_SIGMOID}
+
+
+def join_desc(h, r=None, gate=None, post=True, pre=True, activation="silu", scale=1.0, eps=1e-6, res_dtype=None,
+              row_dtype=None):
+    """``kan_join_desc_t`` of rows ``h [N, D]`` and, with their own row strides, ``r`` and ``gate``."""
+    if h.dim() != 2:
+        raise ValueError("h must be [N, D], got %s" % (tuple(h.shape),))
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % (tuple(_ACTIVATIONS),))
+    N, D = h.shape
+    row = [0 if t is None or N <= 1 else t.stride(0) for t in (h, r, gate)]
+    return L.kan_join_desc_t(N, D, *row, _DTYPES[h.dtype], _DTYPES[res_dtype or h.dtype],
+                             _DTYPES[row_dtype or h.dtype], _ACTIVATIONS[activation],
+                             (L.KAN_JOIN_POST if post else 0) | (L.KAN_JOIN_PRE if pre else 0), scale, eps)
+
+
+def kan_join_workspace_size(desc):
+    return _valid_size(L.lib().kan_join_workspace_size(desc), "join")
+
+
+def _join_inputs(h, gate, w_post, w_pre):
+    dev = _dev(h, "h")
+    if h.dim() != 2:
+        raise ValueError("h must be [N, D], got %s" % (tuple(h.shape),))
+    _rows(h, "h", _DTYPES, dev)
+    if gate is not None:
+        _rows(gate, "gate", (h.dtype,), dev, h.shape)
+    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+        if w is not None:
+            _whole(w, name, _F32, dev, h.shape[1:])
+    return dev
+
+
+def kan_join_forward(h, r=None, gate=None, w_post=None, w_pre=None, post=True, pre=True, activation="silu", scale=1.0,
+                     eps=1e-6, res_dtype=None, row_dtype=None):
+    """``(y, x, stats)`` of the join between two blocks, row by row of ``h [N, D]``:
+    ``y = r + scale act(gate) w_post norm(h)`` (``post``: with the norm) and, with
+    ``pre``, ``x = w_pre norm(y)`` (else None), ``norm(v) = v / sqrt(mean(v^2) + eps)``.
+
+    ``r``, ``gate`` and the weights (float32 ``[D]``) may be None; ``activation`` of the gate:
+    ``silu`` or ``sigmoid``.  ``y`` has ``res_dtype`` (default: r's, or h's without r), ``x``
+    ``row_dtype`` (default: h's); ``stats [2, N]`` float32 are the norms' factors, for the
+    backward pass.  ``h``, ``r`` and ``gate`` may have any row stride."""
+    dev = _join_inputs(h, gate, w_post, w_pre)
+    if w_pre is not None and not pre:
+        raise ValueError("w_pre belongs to the second norm, which pre=False leaves out")
+    res_dtype = res_dtype or (h.dtype if r is None else r.dtype)
+    row_dtype = row_dtype or h.dtype
+    for name, dt in (("res_dtype", res_dtype), ("row_dtype", row_dtype)):
+        if dt not in _DTYPES:
+            raise ValueError("%s must be one of %s" % (name, tuple(_DTYPES)))
+    if r is not None:
+        _rows(r, "r", (res_dtype,), dev, h.shape)
+    post_at, pre_at = _addr(w_post), _addr(w_pre)
+    if ((post_at or 0) | (pre_at or 0)) & 15 or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_join_forward(h, r, gate, _placed(w_post), _placed(w_pre), post, pre, activation, scale, eps,
+                                    res_dtype, row_dtype)
+    desc = join_desc(h, r, gate, post, pre, activation, scale, eps, res_dtype, row_dtype)
+    y = h.new_empty(h.shape, dtype=res_dtype)
+    x = h.new_empty(h.shape, dtype=row_dtype) if pre else None
+    stats = h.new_empty((2, h.shape[0]), dtype=torch.float32)
+    L.check(L.lib().kan_join_forward(desc, h.data_ptr(), _addr(r), _addr(gate), post_at, pre_at, y.data_ptr(), _addr(x),
+                                     stats.data_ptr(), _raw_stream(dev)), "kan_join_forward")
+    return y, x, stats
+
+
+def kan_join_backward(h, y, stats, dy=None, dx=None, gate=None, w_post=None, w_pre=None, post=True, activation="silu",
+                      scale=1.0, need_dr=True, ws=None):
+    """``(dh, dr, dgate, dw_post, dw_pre)`` from the forward's ``y`` and ``stats`` and the
+    gradients ``dy`` of y and ``dx`` of x (either may be None: 0).  ``dh`` and ``dgate``
+    have h's dtype, ``dr`` (None without ``need_dr``) y's, the weights' gradients are
+    float32; what the forward had no input for is None."""
+    dev = _join_inputs(h, gate, w_post, w_pre)
+    shape = h.shape
+    _whole(y, "y", _DTYPES, dev, shape)
+    _whole(stats, "stats", _F32, dev, (2, shape[0]))
+    if dy is not None:
+        _whole(dy, "dy", (y.dtype,), dev, shape)
+    if dx is not None:
+        _whole(dx, "dx", _DTYPES, dev, shape)
+    elif w_pre is not None:
+        raise ValueError("w_pre has a gradient through x alone: give dx")
+    at = [_addr(t) for t in (y, stats, dy, dx, w_post, w_pre)]
+    if any((p or 0) & 15 for p in at) or dev != _current():
+        with torch.cuda.device(dev):
+            return kan_join_backward(h, *(_placed(t) for t in (y, stats, dy, dx)), gate, _placed(w_post),
+                                     _placed(w_pre), post, activation, scale, need_dr, ws)
+    desc = join_desc(h, None, gate, post, dx is not None, activation, scale, 0.0, y.dtype,
+                     h.dtype if dx is None else dx.dtype)
+    dh = h.new_empty(shape)
+    dr = y.new_empty(shape) if need_dr else None
+    dgate = None if gate is None else h.new_empty(shape)
+    dw_post = None if w_post is None else torch.empty_like(w_post)
+    dw_pre = None if w_pre is None else torch.empty_like(w_pre)
+    lib = L.lib()
+    need = 0 if w_post is None and w_pre is None else lib.kan_join_workspace_size(desc)
+    buf, n = _sized_ws(ws, need, h)
+    L.check(lib.kan_join_backward(desc, h.data_ptr(), at[0], at[1], at[2], at[3], _addr(gate), at[4], at[5],
+                                  dh.data_ptr(), _addr(dr), _addr(dgate), _addr(dw_post), _addr(dw_pre), _addr(buf), n,
+                                  _raw_stream(dev)), "kan_join_backward")
+    return dh, dr, dgate, dw_post, dw_pre
