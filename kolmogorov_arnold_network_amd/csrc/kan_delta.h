@@ -6,7 +6,6 @@
 namespace kan {
 
 constexpr int kDeltaChunk = 64;      // rows of a chunk
-constexpr int kDeltaTile = 32;       // state columns of a scan's block
 constexpr int kDeltaMaxDk = 128;
 constexpr int kDeltaMaxDv = 1024;
 constexpr int64_t kDeltaMaxHeads = int64_t(1) << 18;    // B Hv
@@ -15,10 +14,12 @@ constexpr int64_t kDeltaMaxChunks = int64_t(1) << 23;   // chunks of all heads, 
 // What the launches of a call leave each other, in the workspace.  A chunk-head
 // is one chunk of one value head: number (b Hv + h) chunks + n.
 struct DeltaPlan {
-    int dkp, dvp;                    // Dk up to 32, 64 or 128; Dv up to a multiple of the tile
+    int dkp, dvp;                    // Dk up to 32, 64 or 128; Dv up to a multiple of 64
+    int waves;                       // of a scan's block, 16 state columns each
     int64_t chunks, heads;           // of a sequence; B Hv
-    size_t off_rows, off_G, off_P;   // [chunk-head][8][64], [64][64], [64][64] float32
-    size_t off_Gt, off_Pt;           // their transposes (backward)
+    int64_t mats;                    // bytes of a chunk-head's matrices
+    size_t off_rows;                 // [chunk-head][8][64] float32
+    size_t off_mats;                 // [chunk-head][mats]: planes of G, then P (backward: G, G^T, P^T)
     size_t off_w, off_r;             // [chunk-head][64][dvp] float32 (backward)
     size_t off_S, off_dS;            // [chunk-head][dkp][dvp] float32 (backward)
     size_t off_dq, off_dk;           // [B][T][Hv][Dk] float32, where heads share keys (backward)

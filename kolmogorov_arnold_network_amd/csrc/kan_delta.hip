@@ -39,45 +39,215 @@ namespace kan {
 
 namespace {
 
-constexpr int C = kDeltaChunk, NV = kDeltaTile;
-constexpr int NT = 256;              // threads of a block: four waves, 16 rows of a chunk each
+constexpr int C = kDeltaChunk;
 constexpr int LC = C + 4;            // LDS pitch of 64 floats: rows 16 bytes apart modulo the banks
 constexpr float kUnitEps = 1e-6f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // What a chunk's rows have for themselves: [8][64] floats of a chunk-head.
 enum RowField { kHi, kLo, kBeta, kNk, kNq, kFrom, kTo, kFields = 8 };
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
-
-// acc += A B over 16 values of the contracted index.  Lane l has A's row l % 16
-// (or B's column) at the four values 4 (l / 16) .. 4 (l / 16) + 3 of the index; acc has
-// rows 4 (l / 16) .. + 3 of column l % 16.
-__device__ __forceinline__ void mma(f32x4& acc, const f32x4& a, const f32x4& b) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], acc, 0, 0, 0);
-}
 __device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ void st4(float* p, const f32x4& v) { *reinterpret_cast<f32x4*>(p) = v; }
-
-// Elements at .. at + 3 of a row of D, zero past its end.
-template <typename TS>
-__device__ __forceinline__ f32x4 row4(const TS* p, int at, int D) {
-    f32x4 v = zero4();
-    if (at + 4 <= D) {
-        const Raw<TS, 4> r = load_raw<TS, 4>(p + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = raw_value(r, i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (at + i < D) v[i] = load_f(p, at + i);
-    }
-    return v;
-}
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = f2bf(v); }
+
+// ---- products of matrices ----------------------------------------------------------
+//
+// v_mfma_f32_16x16x32_bf16: lane l = 16 gq + m has row m of the left operand (or
+// column m of the right one) at eight values of the contracted index, and rows 4
+// gq .. 4 gq + 3 of column m of the result.  A float is the sum of three bfloat16s,
+// a plane each (24 bits); of two operands' planes the products are added whose
+// place is within those 24 bits: six for two floats, three where one operand is
+// bfloat16 as it stands.  That is 2.7 and 5.3 times as fast as float32's own
+// instruction, and as exact.
+//
+// The result of one product is an operand of the next without leaving its
+// lanes: of 32 values of a contracted index, lane (gq, m) takes 8 gq .. 8 gq + 7,
+// and two tiles 2 s, 2 s + 1 of a result have rows 32 s + 8 gq + 4 (tile % 2) + 0 .. 3 in
+// the lanes of gq.
+__device__ __forceinline__ int row_of(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
+
+// acc += sum over planes of a b, the small ones first
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]) {
+    constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+    for (int place = N - 1; place >= 0; --place)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (place - i >= 0 && place - i < NB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[place - i], acc, 0, 0, 0);
+}
+
+// Eight floats as N planes; every plane takes the rounding of what is left.
+template <int N>
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, bf16x8 (&out)[N]) {
+    uint32_t w[N][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            w[n][i] = pack_bf16(x, y);
+            x -= __uint_as_float(w[n][i] << 16);
+            y -= __uint_as_float(w[n][i] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) __builtin_memcpy(&out[n], w[n], 16);
+}
+
+// ---- rows in LDS ---------------------------------------------------------------------
+//
+// 64 rows of W bfloat16s, a plane after the other, in pieces of eight.  A row's
+// pieces are permuted so that the 16 rows of a tile, and the four rows by four
+// pieces of a transposed read, lie in different banks.
+template <int W>
+__device__ __forceinline__ int piece_at(int row, int c) {
+    constexpr int CH = W / 8;
+    return (row * CH + (c ^ ((((row & 3) << 2) | ((row >> 3) & 3)) & (CH - 1)))) * 8;
+}
+// Planes of pieces 32 s + 8 gq .. of a row: an operand's row, contracted along it.
+template <int PL, int W>
+__device__ __forceinline__ void row_frag(const uint16_t* lds, int row, int c, bf16x8 (&out)[PL]) {
+#pragma unroll
+    for (int n = 0; n < PL; ++n) out[n] = *reinterpret_cast<const bf16x8*>(lds + n * C * W + piece_at<W>(row, c));
+}
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+// The transposed operand: column `m` of 16, contracted along rows 32 s + 8 gq .. + 7.
+// The columns are those of pieces `c` to `c + PIECES - 1`, four a lane: lane 4 a + b of 16
+// reads four columns from row a; `c` and `half` are those of lane b.
+template <int PL, int W>
+__device__ __forceinline__ void col_frag(const uint16_t* lds, int s, int c, int half, bf16x8 (&out)[PL]) {
+    const int lane = threadIdx.x & 63, row = 32 * s + 8 * (lane >> 4) + ((lane & 15) >> 2);
+#pragma unroll
+    for (int n = 0; n < PL; ++n) {
+        s16x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4*)(lds + n * C * W + piece_at<W>(row + 4 * h, c) + 4 * half));
+        __builtin_memcpy(&out[n], v, 16);
+    }
+}
+
+// Eight elements of a row on their way from HBM to LDS.
+template <typename TS>
+struct Piece {
+    float v[8];
+};
+template <>
+struct Piece<uint16_t> {
+    uint32_t w[4];
+};
+__device__ __forceinline__ void load_piece(Piece<uint16_t>& p, const uint16_t* row, int at, int D) {
+    if (at + 8 <= D) {
+        const Raw<uint16_t, 8> r = load_raw<uint16_t, 8>(row + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.w[i] = r.w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p.w[i] = at + 2 * i < D ? row[at + 2 * i] : 0u;
+            if (at + 2 * i + 1 < D) p.w[i] |= (uint32_t)row[at + 2 * i + 1] << 16;
+        }
+    }
+}
+__device__ __forceinline__ void load_piece(Piece<float>& p, const float* row, int at, int D) {
+    if (at + 8 <= D) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const Raw<float, 4> r = load_raw<float, 4>(row + at + 4 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p.v[4 * h + i] = raw_value(r, i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.v[i] = at + i < D ? row[at + i] : 0.0f;
+    }
+}
+__device__ __forceinline__ void no_piece(Piece<uint16_t>& p) { p.w[0] = p.w[1] = p.w[2] = p.w[3] = 0u; }
+__device__ __forceinline__ void no_piece(Piece<float>& p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p.v[i] = 0.0f;
+}
+__device__ __forceinline__ float piece_value(const Piece<uint16_t>& p, int i) {
+    return __uint_as_float(i & 1 ? p.w[i / 2] & 0xffff0000u : p.w[i / 2] << 16);
+}
+__device__ __forceinline__ float piece_value(const Piece<float>& p, int i) { return p.v[i]; }
+template <typename TS>
+struct planes_of {
+    static constexpr int n = sizeof(TS) == 4 ? 3 : 1;
+};
+__device__ __forceinline__ void piece_planes(const Piece<uint16_t>& p, bf16x8 (&out)[1]) { __builtin_memcpy(&out[0], p.w, 16); }
+__device__ __forceinline__ void piece_planes(const Piece<float>& p, bf16x8 (&out)[3]) {
+    split8<3>(f32x4{p.v[0], p.v[1], p.v[2], p.v[3]}, f32x4{p.v[4], p.v[5], p.v[6], p.v[7]}, out);
+}
+
+// The 64 rows of a chunk as NT threads carry them: rows `rows` and on, and columns D
+// and on, are zero.
+template <typename TS, int W, int NT>
+struct Carry {
+    static constexpr int CH = W / 8, N = C * CH / NT > 0 ? C * CH / NT : 1;
+    Piece<TS> p[N];
+    __device__ __forceinline__ void load(const TS* base, int64_t row_stride, int rows, int D) {
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int e = threadIdx.x + NT * x, row = e / CH, c = e % CH;
+            if (row < rows && 8 * c < D) load_piece(p[x], base + row * row_stride, 8 * c, D);
+            else no_piece(p[x]);
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t* lds) const {
+        constexpr int PL = planes_of<TS>::n;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int e = threadIdx.x + NT * x;
+            if (C * CH % NT != 0 && e >= C * CH) break;
+            bf16x8 v[PL];
+            piece_planes(p[x], v);
+#pragma unroll
+            for (int n = 0; n < PL; ++n) *reinterpret_cast<bf16x8*>(lds + n * C * W + piece_at<W>(e / CH, e % CH)) = v[n];
+        }
+    }
+};
+// BYTES that follow each other, the same way.
+template <int BYTES, int NT>
+struct CarryBytes {
+    static constexpr int N = (BYTES / 16 + NT - 1) / NT;
+    u32x4v v[N];
+    __device__ __forceinline__ void load(const void* from) {
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int e = threadIdx.x + NT * x;
+            if (e < BYTES / 16) v[x] = static_cast<const u32x4v*>(from)[e];
+        }
+    }
+    __device__ __forceinline__ void store(void* to) const {
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int e = threadIdx.x + NT * x;
+            if (e < BYTES / 16) static_cast<u32x4v*>(to)[e] = v[x];
+        }
+    }
+};
+
+// A triangular matrix of 64 x 64 as left operand: six pieces [tile][32 columns] of 64
+// lanes by eight values are not zero, a plane after the other.
+constexpr int kTri = 6 * 64 * 8;
+__device__ __forceinline__ int lower_piece(int tile, int s) { return tile < 2 ? tile : 2 * tile - 2 + s; }    // s <= tile / 2
+__device__ __forceinline__ int upper_piece(int tile, int s) { return tile < 2 ? 2 * tile + s : tile + 2; }    // s >= tile / 2
+template <int PL>
+__device__ __forceinline__ void tri_frag(const uint16_t* lds, int piece, bf16x8 (&out)[PL]) {
+#pragma unroll
+    for (int n = 0; n < PL; ++n)
+        out[n] = *reinterpret_cast<const bf16x8*>(lds + n * kTri + (piece * 64 + (threadIdx.x & 63)) * 8);
+}
 
 __device__ __forceinline__ int64_t at_row(const kan_heads_t& s, int64_t b, int64_t t, int64_t h) {
     return b * s.seq + t * s.row + h * s.head;
@@ -93,657 +263,844 @@ __device__ __forceinline__ float decay(const float* row, int i, int j) {
 
 // ---- a chunk's rows among themselves -------------------------------------------
 
-// Rows of q or k to LDS (pitch DKP + 4), zero past the length and past Dk.
-template <typename TS, int DKP>
-__device__ __forceinline__ void fill_rows(float* lds, const TS* base, int64_t row_stride, int rows, int Dk) {
-    const int i = threadIdx.x >> 2;
-#pragma unroll
-    for (int s = 0; s < DKP / 16; ++s) {
-        const int d = 16 * s + 4 * (threadIdx.x & 3);
-        st4(lds + i * (DKP + 4) + d, i < rows ? row4<TS>(base + i * row_stride, d, Dk) : zero4());
-    }
-}
-// Every row times its factor.
-template <int DKP>
-__device__ __forceinline__ void scale_rows(float* lds, const float* factor) {
-    const int i = threadIdx.x >> 2;
-    const float f = factor[i];
-#pragma unroll
-    for (int s = 0; s < DKP / 16; ++s) {
-        float* p = lds + i * (DKP + 4) + 16 * s + 4 * (threadIdx.x & 3);
-        st4(p, ld4(p) * f);
-    }
-}
-template <int DKP>
-__device__ __forceinline__ void unit_factors(const float* lds, float* factor) {
-    const int i = threadIdx.x >> 2;
+// Factors that make rows unit vectors (sums over the planes' values).
+template <int PL, int W, int NT>
+__device__ __forceinline__ void unit_factors(const uint16_t* lds, float* factor) {
+    constexpr int PER = NT / C;                        // threads of a row
+    const int row = threadIdx.x / PER;
     float n = 0.0f;
 #pragma unroll
-    for (int s = 0; s < DKP / 16; ++s) {
-        const f32x4 v = ld4(lds + i * (DKP + 4) + 16 * s + 4 * (threadIdx.x & 3));
+    for (int c = threadIdx.x % PER; c < W / 8; c += PER) {
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) n = __builtin_fmaf(v[j], v[j], n);
+        for (int z = 0; z < PL; ++z) {
+            uint32_t w[4];
+            __builtin_memcpy(w, lds + z * C * W + piece_at<W>(row, c), 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+                x[i] = z ? x[i] + v : v;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n = __builtin_fmaf(x[i], x[i], n);
     }
-    n += __shfl_xor(n, 1, 64);
-    n += __shfl_xor(n, 2, 64);
-    if ((threadIdx.x & 3) == 0) factor[i] = 1.0f / sqrtf(n + kUnitEps);
+#pragma unroll
+    for (int o = 1; o < PER; o <<= 1) n += __shfl_xor(n, o, 64);
+    if (threadIdx.x % PER == 0) factor[row] = 1.0f / sqrtf(n + kUnitEps);
 }
 
-// Chunk n of head h of sequence b: row fields, G and P (BWD: their transposes too).
+// float32 products of 16 x 16 blocks for the triangular solution: lane (gq, m) has
+// four values 4 gq .. + 3 of the contracted index.
+__device__ __forceinline__ void mma_f32(f32x4& acc, const f32x4& a, const f32x4& b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], acc, 0, 0, 0);
+}
+
+// G in place of A (strictly lower, LDS pitch LC): G = A - A diag(beta) G.
+__device__ __forceinline__ void solve(float* A, const float* beta) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4;
+    // the diagonal blocks of 16, a wave each, column m to a lane ...
+    {
+        float h[16];                                   // beta_k G[k][m]
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float* Ai = A + (16 * wave + i) * LC + 16 * wave;
+            float v = Ai[m];
+#pragma unroll
+            for (int k = 0; k < i; ++k) v = __builtin_fmaf(-Ai[k], h[k], v);
+            h[i] = v * beta[16 * wave + i];
+            if (gq == 0) Ai[m] = v;
+        }
+    }
+    __syncthreads();
+    // ... and the blocks below, a row of blocks after the other: wave j has block j,
+    // R = A_ij - sum over k of A_ik diag(beta) G_kj,  G_ij = R - G_ii diag(beta) R
+    const int j = 16 * wave + m;
+    for (int it = 1; it < 4; ++it) {
+        f32x4 R = zero4();
+        auto scaled = [&](int kt) {
+            f32x4 v;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int k = 16 * kt + 4 * gq + x;
+                v[x] = -beta[k] * A[k * LC + j];
+            }
+            return v;
+        };
+        if (wave < it) {
+            for (int kt = wave; kt < it; ++kt) mma_f32(R, ld4(A + (16 * it + m) * LC + 16 * kt + 4 * gq), scaled(kt));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) R[x] += A[(16 * it + 4 * gq + x) * LC + j];
+        }
+        __syncthreads();                               // A_ik has been read
+        if (wave < it) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) A[(16 * it + 4 * gq + x) * LC + j] = R[x];
+            mma_f32(R, ld4(A + (16 * it + m) * LC + 16 * it + 4 * gq), scaled(it));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) A[(16 * it + 4 * gq + x) * LC + j] = R[x];
+        }
+    }
+    __syncthreads();
+}
+
+// Pieces of a triangular matrix (LDS pitch LC) or of its transpose, as operands.
+template <int PL, bool TRANSPOSED>
+__device__ __forceinline__ void write_tri(const float* X, uint16_t* out, int nt) {
+    for (int e = threadIdx.x; e < 6 * 64; e += nt) {
+        const int piece = e >> 6, lane = e & 63;
+        int tile, s;
+        if (TRANSPOSED) tile = piece < 4 ? piece >> 1 : piece - 2, s = piece < 4 ? piece & 1 : 1;
+        else tile = piece < 2 ? piece : (piece >> 1) + 1, s = piece < 2 ? 0 : piece & 1;
+        const int i = row_of(tile, lane & 15), j = 32 * s + 8 * (lane >> 4);
+        f32x4 v[2];
+        if (TRANSPOSED) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x >> 2][x & 3] = X[(j + x) * LC + i];
+        } else {
+            v[0] = ld4(X + i * LC + j), v[1] = ld4(X + i * LC + j + 4);
+        }
+        bf16x8 p[PL];
+        split8<PL>(v[0], v[1], p);
+#pragma unroll
+        for (int n = 0; n < PL; ++n) *reinterpret_cast<bf16x8*>(out + n * kTri + e * 8) = p[n];
+    }
+}
+
+// Planes of P: as many as the output has of 8 bits each, and a little more.
+template <typename TS>
+struct out_planes {
+    static constexpr int n = sizeof(TS) == 4 ? 3 : 2;
+};
+
+constexpr int PREP_NT = 256;
+// Chunk n of head h of sequence b: row fields, G and P (BWD: G and the transposes).
 template <typename TS, int DKP, bool BWD>
-__global__ void __launch_bounds__(NT) delta_prep_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
-    extern __shared__ float lds[];
-    float* K = lds;                                    // [64][DKP + 4]
-    float* Q = K + C * (DKP + 4);
-    float* A = Q + C * (DKP + 4);                      // [64][LC]
-    float* G = A + C * LC;
-    float* row = G + C * LC;                           // [8][64]
+__global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int PL = planes_of<TS>::n;
+    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP], then A and P in their place
+    uint16_t* const Q = K + PL * C * DKP;
+    float* const A = reinterpret_cast<float*>(lds);                // [64][LC], G in the end
+    float* const P = A + C * LC;
+    constexpr int BODY = 4 * PL * C * DKP > 8 * C * LC ? 4 * PL * C * DKP : 8 * C * LC;
+    float* const row = reinterpret_cast<float*>(lds + BODY);       // [8][64]
     const int64_t n = blockIdx.x % (unsigned)p.chunks, bh = blockIdx.x / (unsigned)p.chunks;
     const int64_t b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
     const int rows = length_of(a, b, d.T) - (int)n * C;
     if (rows <= 0) return;                             // uniform
-    const int64_t t0 = n * C;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, gq = lane >> 4;
-    fill_rows<TS, DKP>(K, static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, (int)d.Dk);
-    fill_rows<TS, DKP>(Q, static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, (int)d.Dk);
-    if (wave == 0) {
-        float g = 0.0f, beta = 0.0f;
-        if (lane < rows) {
-            g = a.g[(b * d.T + t0 + lane) * d.Hv + h];
-            beta = a.beta[(b * d.T + t0 + lane) * d.Hv + h];
-            g = g < -128.0f ? -128.0f : g;             // exp(-128) is 0; a NaN stays
-        }
-        double c = g;
+    const int64_t t0 = n * C, ch = bh * p.chunks + n;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    {
+        Carry<TS, DKP, PREP_NT> k, q;
+        k.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, (int)d.Dk);
+        q.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, (int)d.Dk);
+        if (wave == 0) {
+            float g = 0.0f, beta = 0.0f;
+            if (lane < rows) {
+                g = a.g[(b * d.T + t0 + lane) * d.Hv + h];
+                beta = a.beta[(b * d.T + t0 + lane) * d.Hv + h];
+                g = g < -128.0f ? -128.0f : g;         // exp(-128) is 0; a NaN stays
+            }
+            double c = g;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double before = __shfl_up(c, o, 64);
-            if (lane >= o) c += before;
+            for (int o = 1; o < 64; o <<= 1) {
+                const double before = __shfl_up(c, o, 64);
+                if (lane >= o) c += before;
+            }
+            const float hi = (float)c, lo = (float)(c - (double)hi);
+            row[kHi * C + lane] = hi;
+            row[kLo * C + lane] = hi - hi == 0.0f ? lo : 0.0f;
+            row[kBeta * C + lane] = beta;
+            row[kNk * C + lane] = row[kNq * C + lane] = 1.0f;
+            row[kFrom * C + lane] = (float)exp(c);
+            row[kTo * C + lane] = (float)exp(__shfl(c, 63, 64) - c);
+            row[7 * C + lane] = 0.0f;
         }
-        const float hi = (float)c, lo = (float)(c - (double)hi);
-        row[kHi * C + lane] = hi;
-        row[kLo * C + lane] = hi - hi == 0.0f ? lo : 0.0f;
-        row[kBeta * C + lane] = beta;
-        row[kNk * C + lane] = row[kNq * C + lane] = 1.0f;
-        row[kFrom * C + lane] = (float)exp(c);
-        row[kTo * C + lane] = (float)exp(__shfl(c, 63, 64) - c);
+        k.store(K);
+        q.store(Q);
     }
     __syncthreads();
     if (d.flags & KAN_DELTA_UNIT) {
-        unit_factors<DKP>(K, row + kNk * C);
-        unit_factors<DKP>(Q, row + kNq * C);
-        __syncthreads();
-        scale_rows<DKP>(K, row + kNk * C);
-        scale_rows<DKP>(Q, row + kNq * C);
-        __syncthreads();
+        unit_factors<PL, DKP, PREP_NT>(K, row + kNk * C);
+        unit_factors<PL, DKP, PREP_NT>(Q, row + kNq * C);
     }
-    char* const mine = ws;
-    const int64_t ch = bh * p.chunks + n;
-    float* out_row = reinterpret_cast<float*>(mine + p.off_rows) + ch * kFields * C;
-    for (int i = tid; i < kFields * C; i += NT) out_row[i] = i < (kTo + 1) * C ? row[i] : 0.0f;
-    float* out_P = reinterpret_cast<float*>(mine + p.off_P) + ch * C * C;
-    float* out_Pt = reinterpret_cast<float*>(mine + p.off_Pt) + ch * C * C;
-    // this wave's 16 rows of A and P
-    for (int jt = 0; jt < 4; ++jt) {
-        f32x4 kk = zero4(), qk = zero4();
-        if (jt <= wave) {
+    // this wave's 16 rows of K K^T and Q K^T
+    f32x4 kk[4], qk[4];
 #pragma unroll
-            for (int s = 0; s < DKP / 16; ++s) {
-                const f32x4 kb = ld4(K + (16 * jt + r) * (DKP + 4) + 16 * s + 4 * gq);
-                mma(kk, ld4(K + (16 * wave + r) * (DKP + 4) + 16 * s + 4 * gq), kb);
-                mma(qk, ld4(Q + (16 * wave + r) * (DKP + 4) + 16 * s + 4 * gq), kb);
-            }
-        }
-        const int j = 16 * jt + r;
-        f32x4 P;
+    for (int x = 0; x < 4; ++x) kk[x] = qk[x] = zero4();
+#pragma unroll
+    for (int s = 0; s < DKP / 32; ++s) {
+        bf16x8 ka[PL], qa[PL];
+        row_frag<PL, DKP>(K, 16 * wave + m, 4 * s + gq, ka);
+        row_frag<PL, DKP>(Q, 16 * wave + m, 4 * s + gq, qa);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int i = 16 * wave + 4 * gq + x;
-            const float D = j <= i ? decay(row, i, j) : 0.0f;
-            A[i * LC + j] = j < i ? kk[x] * D : 0.0f;
-            P[x] = j <= i ? d.scale * (qk[x] * D) : 0.0f;
-            out_P[i * C + j] = P[x];
+            if (x > wave) break;
+            bf16x8 kb[PL];
+            row_frag<PL, DKP>(K, 16 * x + m, 4 * s + gq, kb);
+            mma<PL, PL>(kk[x], ka, kb);
+            mma<PL, PL>(qk[x], qa, kb);
         }
-        if (BWD) st4(out_Pt + j * C + 16 * wave + 4 * gq, P);
     }
     __syncthreads();
-    const float* beta = row + kBeta * C;
-    // G = A - A diag(beta) G: the diagonal blocks of 16, a wave each, column r to a lane ...
-    {
-        float hv[16];                                  // beta_k G[k][r]
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float* Ai = A + (16 * wave + i) * LC + 16 * wave;
-            float v = Ai[r];
+    for (int x = 0; x < 4; ++x) {
+        const int j = 16 * x + m;
+        const float nj = row[kNk * C + j];
 #pragma unroll
-            for (int k = 0; k < i; ++k) v = __builtin_fmaf(-Ai[k], hv[k], v);
-            hv[i] = v * beta[16 * wave + i];
-            if (gq == 0) G[(16 * wave + i) * LC + 16 * wave + r] = v;
+        for (int y = 0; y < 4; ++y) {
+            const int i = 16 * wave + 4 * gq + y;
+            const float D = j <= i ? decay(row, i, j) * nj : 0.0f;
+            A[i * LC + j] = j < i ? kk[x][y] * (D * row[kNk * C + i]) : 0.0f;
+            P[i * LC + j] = j <= i ? qk[x][y] * (D * row[kNq * C + i] * d.scale) : 0.0f;
         }
-        for (int jt = wave + 1; jt < 4; ++jt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) G[(16 * wave + 4 * gq + x) * LC + 16 * jt + r] = 0.0f;
     }
     __syncthreads();
-    // ... and the blocks below it, a row of blocks after the other:
-    // R = A_ij - sum over k of A_ik diag(beta) G_kj,  G_ij = R - G_ii diag(beta) R
-    for (int it = 1; it < 4; ++it) {
-        f32x4 R = zero4();
-        const int j = 16 * wave + r;
-        if (wave < it) {
-            for (int kt = wave; kt < it; ++kt) {
-                f32x4 gb;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int k = 16 * kt + 4 * gq + x;
-                    gb[x] = -beta[k] * G[k * LC + j];
-                }
-                mma(R, ld4(A + (16 * it + r) * LC + 16 * kt + 4 * gq), gb);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int i = 16 * it + 4 * gq + x;
-                R[x] += A[i * LC + j];
-                G[i * LC + j] = R[x];
-            }
-        }
-        __syncthreads();
-        if (wave < it) {
-            f32x4 gb;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int k = 16 * it + 4 * gq + x;
-                gb[x] = -beta[k] * G[k * LC + j];
-            }
-            mma(R, ld4(G + (16 * it + r) * LC + 16 * it + 4 * gq), gb);
-        }
-        __syncthreads();
-        if (wave < it) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) G[(16 * it + 4 * gq + x) * LC + j] = R[x];
-        }
-        __syncthreads();
-    }
-    float* out_G = reinterpret_cast<float*>(mine + p.off_G) + ch * C * C;
-    float* out_Gt = reinterpret_cast<float*>(mine + p.off_Gt) + ch * C * C;
-    for (int e = tid; e < C * C / 4; e += NT) {
-        const int i = e >> 4, j = 4 * (e & 15);
-        st4(out_G + i * C + j, ld4(G + i * LC + j));
-        if (BWD) {
-            f32x4 v;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) v[x] = G[(j + x) * LC + i];
-            st4(out_Gt + i * C + j, v);
-        }
-    }
+    float* const out_row = reinterpret_cast<float*>(ws + p.off_rows) + ch * kFields * C;
+    for (int i = tid; i < kFields * C; i += PREP_NT) out_row[i] = row[i];
+    uint16_t* const mats = reinterpret_cast<uint16_t*>(ws + p.off_mats + ch * p.mats);
+    constexpr int NP = out_planes<TS>::n;
+    if (BWD) write_tri<3, true>(P, mats + 6 * kTri, PREP_NT);
+    else write_tri<NP, false>(P, mats + 3 * kTri, PREP_NT);
+    solve(A, row + kBeta * C);
+    write_tri<3, false>(A, mats, PREP_NT);
+    if (BWD) write_tri<3, true>(A, mats + 3 * kTri, PREP_NT);
 }
 
 // ---- along a sequence -------------------------------------------------------------
 
-// Columns n0 .. n0 + 31 of the state of head h of sequence b.  A wave has rows 16
-// wave .. of what has a chunk's rows, and tiles of 16 x 16 of the state.  BWD: keeps
-// the chunks' first states and w for the backward pass and writes no rows.
-template <typename TS, int DKP, bool BWD>
-__global__ void __launch_bounds__(NT) delta_scan_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
-    extern __shared__ float lds[];
-    constexpr int LK = DKP + 4;
-    constexpr int TILES = DKP / 16 * (NV / 16) / 4;    // of the state, for each wave
-    float* K = lds;                                    // [64][LK]
-    float* St = K + C * LK;                            // [32][LK]: S transposed
-    float* Et = St + NV * LK;                          // [32][LC]: beta e
-    float* Ut = Et + NV * LC;                          // [32][LC]: u
-    float* row = Ut + NV * LC;                         // [8][64]
-    const int tiles = p.dvp / NV;
+// A wave has 16 columns of the state, in registers from the sequence's start to
+// its end, and everything of a chunk's rows in these columns: what it computes is
+// an operand of its next product as it stands.  The left operands (K, Q, G, P) are
+// the same for the block's waves and come through LDS; the next chunk's are on
+// their way from HBM meanwhile.  BWD: keeps the chunks' first states and w for the
+// backward pass and writes no rows.
+template <typename TS, int DKP, int WAVES, bool BWD>
+__global__ void __launch_bounds__(64 * WAVES) delta_scan_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int PL = planes_of<TS>::n, NP = out_planes<TS>::n, NT = 64 * WAVES, DT = DKP / 16;
+    constexpr int MATS = (BWD ? 3 : 3 + NP) * kTri;
+    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
+    uint16_t* const Q = K + PL * C * DKP;                          // forward alone
+    uint16_t* const G = BWD ? Q : Q + PL * C * DKP;                // [3][kTri]
+    uint16_t* const P = G + 3 * kTri;                              // [NP][kTri], forward alone
+    float* const row = reinterpret_cast<float*>(G + MATS);         // [8][64]
+    const int tiles = (int)((d.Dv + 16 * WAVES - 1) / (16 * WAVES));
     const int64_t bh = blockIdx.x / (unsigned)tiles, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
-    const int n0 = (int)(blockIdx.x % (unsigned)tiles) * NV;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, gq = lane >> 4;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int n0 = (int)(blockIdx.x % (unsigned)tiles) * 16 * WAVES + 16 * wave;   // this wave's first column
     const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), chunks = (len + C - 1) / C;
-    // tile x of this wave: rows 16 dt of S, columns 16 nt
-    auto nt_of = [&](int x) { return (wave + 4 * x) & 1; };
-    auto dt_of = [&](int x) { return (wave + 4 * x) >> 1; };
-    f32x4 S[TILES];
+    const bool mine = n0 + m < Dv;
+    f32x4 S[DT];
 #pragma unroll
-    for (int x = 0; x < TILES; ++x) {
-        const int nn = n0 + 16 * nt_of(x) + r;
+    for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = 16 * dt_of(x) + 4 * gq + j;
-            S[x][j] = a.h0 && dd < Dk && nn < Dv ? a.h0[(bh * Dk + dd) * Dv + nn] : 0.0f;
+            const int dd = row_of(x, 4 * gq) + j;
+            S[x][j] = a.h0 && dd < Dk && mine ? a.h0[(bh * Dk + dd) * Dv + n0 + m] : 0.0f;
         }
-        st4(St + (16 * nt_of(x) + r) * LK + 16 * dt_of(x) + 4 * gq, S[x]);
-    }
+    const TS* const k_base = static_cast<const TS*>(a.k) + at_row(d.k, b, 0, hk);
+    const TS* const q_base = static_cast<const TS*>(a.q) + at_row(d.q, b, 0, hk);
+    const TS* const v_base = static_cast<const TS*>(a.v) + at_row(d.v, b, 0, h) + n0 + m;
+    const float* const rows_base = reinterpret_cast<const float*>(ws + p.off_rows) + bh * p.chunks * kFields * C;
+    const char* const mats_base = ws + p.off_mats + bh * p.chunks * p.mats;
+    Carry<TS, DKP, NT> ck, cq;
+    CarryBytes<MATS * 2, NT> cm;
+    CarryBytes<kFields * C * 4, NT> cr;
+    TS vn[4][4];
+    auto fetch = [&](int n) {
+        const int64_t t0 = (int64_t)n * C;
+        const int rows = len - n * C;
+        ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
+        if (!BWD) cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
+        cm.load(mats_base + n * p.mats);
+        cr.load(rows_base + (int64_t)n * kFields * C);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = row_of(t, 4 * gq) + j;
+                vn[t][j] = i < rows && mine ? v_base[(t0 + i) * d.v.row] : (TS)0;
+            }
+    };
+    if (chunks > 0) fetch(0);
     for (int n = 0; n < chunks; ++n) {
         const int64_t ch = bh * p.chunks + n, t0 = (int64_t)n * C;
         const int rows = len - n * C;
-        const float* in_row = reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C;
-        const float* in_G = reinterpret_cast<const float*>(ws + p.off_G) + ch * C * C;
-        const float* in_P = reinterpret_cast<const float*>(ws + p.off_P) + ch * C * C;
-        for (int i = tid; i < kFields * C; i += NT) row[i] = in_row[i];
-        fill_rows<TS, DKP>(K, static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
-        f32x4 v[2];
+        __syncthreads();                               // the chunk before is done with LDS
+        ck.store(K);
+        if (!BWD) cq.store(Q);
+        cm.store(G);
+        cr.store(row);
+        f32x4 w[4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 16 * wave + 4 * gq + j, nn = n0 + 16 * nt + r;
-                v[nt][j] = i < rows && nn < Dv ? load_f(static_cast<const TS*>(a.v) + at_row(d.v, b, t0 + i, h), nn)
-                                              : 0.0f;
+            for (int j = 0; j < 4; ++j) w[t][j] = load_f(&vn[t][j], 0);
+        __syncthreads();
+        if (n + 1 < chunks) fetch(n + 1);
+        // K S and Q S (the latter transposed: lanes have columns of one row)
+        f32x4 ks[4], o[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks[t] = o[t] = zero4();
+#pragma unroll
+        for (int s = 0; s < DKP / 32; ++s) {
+            bf16x8 sb[3];
+            split8<3>(S[2 * s], S[2 * s + 1], sb);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                bf16x8 ka[PL];
+                row_frag<PL, DKP>(K, row_of(t, m), 4 * s + gq, ka);
+                mma<PL, 3>(ks[t], ka, sb);
             }
-        __syncthreads();
-        scale_rows<DKP>(K, row + kNk * C);
-        __syncthreads();
-        f32x4 ks[2] = {zero4(), zero4()}, qs[2] = {zero4(), zero4()};
-        const int iq = 16 * wave + r;
-        const TS* q = static_cast<const TS*>(a.q) + at_row(d.q, b, t0 + (iq < rows ? iq : 0), hk);
+            if (BWD) continue;
+            bf16x8 sp[NP];
 #pragma unroll
-        for (int s = 0; s < DKP / 16; ++s) {
-            const int at = 16 * s + 4 * gq;
-            const f32x4 ka = ld4(K + iq * LK + at);
-            f32x4 qa = zero4();
-            if (!BWD && iq < rows) qa = row4<TS>(q, at, Dk);
+            for (int z = 0; z < NP; ++z) sp[z] = sb[z];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const f32x4 sb = ld4(St + (16 * nt + r) * LK + at);
-                mma(ks[nt], ka, sb);
-                if (!BWD) mma(qs[nt], qa, sb);
+            for (int t = 0; t < 4; ++t) {
+                bf16x8 qa[PL];
+                row_frag<PL, DKP>(Q, row_of(t, m), 4 * s + gq, qa);
+                mma<NP, PL>(o[t], sp, qa);
             }
         }
         if (BWD) {
-            float* out = reinterpret_cast<float*>(ws + p.off_S) + ch * DKP * p.dvp;
+            float* out = reinterpret_cast<float*>(ws + p.off_S) + ch * DKP * p.dvp + n0 + m;
 #pragma unroll
-            for (int x = 0; x < TILES; ++x)
+            for (int x = 0; x < DT; ++x)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    out[(16 * dt_of(x) + 4 * gq + j) * p.dvp + n0 + 16 * nt_of(x) + r] = S[x][j];
+                for (int j = 0; j < 4; ++j) out[(row_of(x, 4 * gq) + j) * p.dvp] = S[x][j];
         }
-        const f32x4 from = ld4(row + kFrom * C + 16 * wave + 4 * gq), beta = ld4(row + kBeta * C + 16 * wave + 4 * gq);
-        f32x4 w[2];
+        f32x4 be[4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            w[nt] = v[nt] - from * ks[nt];
-            st4(Et + (16 * nt + r) * LC + 16 * wave + 4 * gq, beta * w[nt]);
+        for (int t = 0; t < 4; ++t) {
+            const int i = row_of(t, 4 * gq);
+            w[t] = w[t] - ld4(row + kFrom * C + i) * ld4(row + kNk * C + i) * ks[t];       // e
+            be[t] = ld4(row + kBeta * C + i) * w[t];
         }
-        __syncthreads();
-        f32x4 ge[2] = {zero4(), zero4()};
-        for (int s = 0; s <= wave; ++s) {
-            const f32x4 ga = ld4(in_G + iq * C + 16 * s + 4 * gq);
+        {
+            bf16x8 eb[2][3];
+            split8<3>(be[0], be[1], eb[0]);
+            split8<3>(be[2], be[3], eb[1]);
+            f32x4 ge[4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma(ge[nt], ga, ld4(Et + (16 * nt + r) * LC + 16 * s + 4 * gq));
-        }
+            for (int t = 0; t < 4; ++t) {
+                ge[t] = zero4();
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            w[nt] = w[nt] - ge[nt];
-            st4(Ut + (16 * nt + r) * LC + 16 * wave + 4 * gq, beta * w[nt]);
-            if (BWD) {
-                float* out = reinterpret_cast<float*>(ws + p.off_w) + ch * C * p.dvp + n0 + 16 * nt + r;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) out[(16 * wave + 4 * gq + j) * p.dvp] = w[nt][j];
-            }
-        }
-        __syncthreads();
-        if (!BWD) {
-            f32x4 o[2] = {zero4(), zero4()};
-            for (int s = 0; s <= wave; ++s) {
-                const f32x4 pa = ld4(in_P + iq * C + 16 * s + 4 * gq);
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) mma(o[nt], pa, ld4(Ut + (16 * nt + r) * LC + 16 * s + 4 * gq));
-            }
-            const f32x4 nq = ld4(row + kNq * C + 16 * wave + 4 * gq);
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = 16 * wave + 4 * gq + j, nn = n0 + 16 * nt + r;
-                    if (i < rows && nn < Dv)
-                        put(static_cast<TS*>(a.y) + ((b * d.T + t0 + i) * d.Hv + h) * Dv + nn,
-                            o[nt][j] + d.scale * nq[j] * from[j] * qs[nt][j]);
+                for (int s = 0; s <= t / 2; ++s) {
+                    bf16x8 ga[3];
+                    tri_frag<3>(G, lower_piece(t, s), ga);
+                    mma<3, 3>(ge[t], ga, eb[s]);
                 }
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = w[t] - ge[t];
         }
+        f32x4 u[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t] = ld4(row + kBeta * C + row_of(t, 4 * gq)) * w[t];
+        if (BWD) {
+            float* out = reinterpret_cast<float*>(ws + p.off_w) + ch * C * p.dvp + n0 + m;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) out[(row_of(t, 4 * gq) + j) * p.dvp] = w[t][j];
+        } else {
+            bf16x8 ub[2][NP];
+            split8<NP>(u[0], u[1], ub[0]);
+            split8<NP>(u[2], u[3], ub[1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int i = row_of(t, m);
+                o[t] = o[t] * (d.scale * row[kFrom * C + i] * row[kNq * C + i]);
+#pragma unroll
+                for (int s = 0; s <= t / 2; ++s) {
+                    bf16x8 pa[NP];
+                    tri_frag<NP>(P, lower_piece(t, s), pa);
+                    mma<NP, NP>(o[t], ub[s], pa);
+                }
+                if (i >= rows) continue;
+                TS* y = static_cast<TS*>(a.y) + ((b * d.T + t0 + i) * d.Hv + h) * Dv + n0 + 4 * gq;
+                if (n0 + 4 * gq + 4 <= Dv) {
+                    const float v[4] = {o[t][0], o[t][1], o[t][2], o[t][3]};
+                    store_vec<4>(y, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n0 + 4 * gq + j < Dv) put(y + j, o[t][j]);
+                }
+            }
+        }
+        // S = exp(c_63) S + K^T (exp(c_63 - c) u)
+        bf16x8 ub[2][3];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int i = row_of(t, 4 * gq);
+            u[t] = u[t] * (ld4(row + kTo * C + i) * ld4(row + kNk * C + i));
+        }
+        split8<3>(u[0], u[1], ub[0]);
+        split8<3>(u[2], u[3], ub[1]);
         const float whole = row[kFrom * C + C - 1];
 #pragma unroll
-        for (int x = 0; x < TILES; ++x) {
-            f32x4 add = zero4();
+        for (int x = 0; x < DT; ++x) {
+            S[x] = whole * S[x];
 #pragma unroll
-            for (int s = 0; s < C / 16; ++s) {
-                f32x4 ka;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = 16 * s + 4 * gq + j;
-                    ka[j] = K[i * LK + 16 * dt_of(x) + r] * row[kTo * C + i];
-                }
-                mma(add, ka, ld4(Ut + (16 * nt_of(x) + r) * LC + 16 * s + 4 * gq));
+            for (int s = 0; s < 2; ++s) {
+                bf16x8 kt[PL];
+                col_frag<PL, DKP>(K, s, 4 * (x >> 1) + (m & 3), x & 1, kt);
+                mma<PL, 3>(S[x], kt, ub[s]);
             }
-            S[x] = whole * S[x] + add;
-            st4(St + (16 * nt_of(x) + r) * LK + 16 * dt_of(x) + 4 * gq, S[x]);
         }
-        __syncthreads();
     }
     if (BWD) return;
-    for (int64_t e = tid; e < (d.T - len) * NV; e += NT) {
-        const int64_t t = len + e / NV;
-        const int nn = n0 + (int)(e % NV);
+    for (int64_t e = lane; e < (d.T - len) * 16; e += 64) {
+        const int64_t t = len + e / 16;
+        const int nn = n0 + (int)(e % 16);
         if (nn < Dv) put(static_cast<TS*>(a.y) + ((b * d.T + t) * d.Hv + h) * Dv + nn, 0.0f);
     }
-    if (!a.hT) return;
+    if (!a.hT || !mine) return;
 #pragma unroll
-    for (int x = 0; x < TILES; ++x) {
-        const int nn = n0 + 16 * nt_of(x) + r;
+    for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = 16 * dt_of(x) + 4 * gq + j;
-            if (dd < Dk && nn < Dv) a.hT[(bh * Dk + dd) * Dv + nn] = S[x][j];
+            const int dd = row_of(x, 4 * gq) + j;
+            if (dd < Dk) a.hT[(bh * Dk + dd) * Dv + n0 + m] = S[x][j];
         }
-    }
 }
 
 // Backwards along a sequence: r, dv and the gradients of the chunks' last states.
-template <typename TS, int DKP>
-__global__ void __launch_bounds__(NT) delta_back_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
-    extern __shared__ float lds[];
-    constexpr int LK = DKP + 4;
-    constexpr int TILES = DKP / 16 * (NV / 16) / 4;
-    float* K = lds;                                    // [64][LK]
-    float* Q = K + C * LK;                             // [64][LK]
-    float* St = Q + C * LK;                            // [32][LK]: dS transposed
-    float* Yt = St + NV * LK;                          // [32][LC]: dY
-    float* Ut = Yt + NV * LC;                          // [32][LC]: beta du, then dv
-    float* row = Ut + NV * LC;                         // [8][64]
-    const int tiles = p.dvp / NV;
+template <typename TS, int DKP, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) delta_back_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int PL = planes_of<TS>::n, NT = 64 * WAVES, DT = DKP / 16, W = 16 * WAVES;
+    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
+    uint16_t* const Q = K + PL * C * DKP;
+    uint16_t* const Y = Q + PL * C * DKP;                          // [PL][64][W]: dY
+    uint16_t* const G = Y + PL * C * W;                            // [3][kTri]: G^T
+    uint16_t* const P = G + 3 * kTri;                              // [3][kTri]: P^T
+    float* const row = reinterpret_cast<float*>(P + 3 * kTri);     // [8][64]
+    const int tiles = (int)((d.Dv + W - 1) / W);
     const int64_t bh = blockIdx.x / (unsigned)tiles, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
-    const int n0 = (int)(blockIdx.x % (unsigned)tiles) * NV;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, gq = lane >> 4;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int nb = (int)(blockIdx.x % (unsigned)tiles) * W, n0 = nb + 16 * wave;
     const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), chunks = (len + C - 1) / C;
-    auto nt_of = [&](int x) { return (wave + 4 * x) & 1; };
-    auto dt_of = [&](int x) { return (wave + 4 * x) >> 1; };
-    for (int64_t e = tid; e < (d.T - len) * NV; e += NT) {
-        const int64_t t = len + e / NV;
-        const int nn = n0 + (int)(e % NV);
+    const bool mine = n0 + m < Dv;
+    for (int64_t e = lane; e < (d.T - len) * 16; e += 64) {
+        const int64_t t = len + e / 16;
+        const int nn = n0 + (int)(e % 16);
         if (nn < Dv) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t, h) + nn, 0.0f);
     }
-    f32x4 S[TILES];
+    f32x4 S[DT];
 #pragma unroll
-    for (int x = 0; x < TILES; ++x) {
-        const int nn = n0 + 16 * nt_of(x) + r;
+    for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = 16 * dt_of(x) + 4 * gq + j;
-            S[x][j] = a.dhT && dd < Dk && nn < Dv ? a.dhT[(bh * Dk + dd) * Dv + nn] : 0.0f;
+            const int dd = row_of(x, 4 * gq) + j;
+            S[x][j] = a.dhT && dd < Dk && mine ? a.dhT[(bh * Dk + dd) * Dv + n0 + m] : 0.0f;
         }
-        st4(St + (16 * nt_of(x) + r) * LK + 16 * dt_of(x) + 4 * gq, S[x]);
-    }
+    const TS* const k_base = static_cast<const TS*>(a.k) + at_row(d.k, b, 0, hk);
+    const TS* const q_base = static_cast<const TS*>(a.q) + at_row(d.q, b, 0, hk);
+    const TS* const y_base = static_cast<const TS*>(a.dy) + (b * d.T * d.Hv + h) * Dv + nb;
+    const float* const rows_base = reinterpret_cast<const float*>(ws + p.off_rows) + bh * p.chunks * kFields * C;
+    const char* const mats_base = ws + p.off_mats + bh * p.chunks * p.mats + 3 * kTri * 2;
+    Carry<TS, DKP, NT> ck, cq;
+    Carry<TS, W, NT> cy;
+    CarryBytes<6 * kTri * 2, NT> cm;
+    CarryBytes<kFields * C * 4, NT> cr;
+    auto fetch = [&](int n) {
+        const int64_t t0 = (int64_t)n * C;
+        const int rows = len - n * C;
+        ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
+        cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
+        cy.load(y_base + t0 * d.Hv * Dv, d.Hv * Dv, rows, Dv - nb);
+        cm.load(mats_base + n * p.mats);
+        cr.load(rows_base + (int64_t)n * kFields * C);
+    };
+    if (chunks > 0) fetch(chunks - 1);
     for (int n = chunks - 1; n >= 0; --n) {
         const int64_t ch = bh * p.chunks + n, t0 = (int64_t)n * C;
         const int rows = len - n * C;
-        const float* in_row = reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C;
-        const float* in_Gt = reinterpret_cast<const float*>(ws + p.off_Gt) + ch * C * C;
-        const float* in_Pt = reinterpret_cast<const float*>(ws + p.off_Pt) + ch * C * C;
-        for (int i = tid; i < kFields * C; i += NT) row[i] = in_row[i];
-        fill_rows<TS, DKP>(K, static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
-        fill_rows<TS, DKP>(Q, static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, Dk);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            f32x4 y;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 16 * wave + 4 * gq + j, nn = n0 + 16 * nt + r;
-                y[j] = i < rows && nn < Dv
-                           ? load_f(static_cast<const TS*>(a.dy) + ((b * d.T + t0 + i) * d.Hv + h) * Dv, nn)
-                           : 0.0f;
-            }
-            st4(Yt + (16 * nt + r) * LC + 16 * wave + 4 * gq, y);
-        }
-        float* out_S = reinterpret_cast<float*>(ws + p.off_dS) + ch * DKP * p.dvp;
-#pragma unroll
-        for (int x = 0; x < TILES; ++x)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                out_S[(16 * dt_of(x) + 4 * gq + j) * p.dvp + n0 + 16 * nt_of(x) + r] = S[x][j];
         __syncthreads();
-        scale_rows<DKP>(K, row + kNk * C);
-        scale_rows<DKP>(Q, row + kNq * C);
+        ck.store(K);
+        cq.store(Q);
+        cy.store(Y);
+        cm.store(G);
+        cr.store(row);
         __syncthreads();
-        const int iq = 16 * wave + r;
-        f32x4 kd[2] = {zero4(), zero4()}, py[2] = {zero4(), zero4()};
+        if (n > 0) fetch(n - 1);
+        float* const out_S = reinterpret_cast<float*>(ws + p.off_dS) + ch * DKP * p.dvp + n0 + m;
 #pragma unroll
-        for (int s = 0; s < DKP / 16; ++s) {
-            const f32x4 ka = ld4(K + iq * LK + 16 * s + 4 * gq);
+        for (int x = 0; x < DT; ++x)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma(kd[nt], ka, ld4(St + (16 * nt + r) * LK + 16 * s + 4 * gq));
-        }
-        for (int s = wave; s < 4; ++s) {
-            const f32x4 pa = ld4(in_Pt + iq * C + 16 * s + 4 * gq);
+            for (int j = 0; j < 4; ++j) out_S[(row_of(x, 4 * gq) + j) * p.dvp] = S[x][j];
+        f32x4 kd[4], py[4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma(py[nt], pa, ld4(Yt + (16 * nt + r) * LC + 16 * s + 4 * gq));
-        }
-        const f32x4 to = ld4(row + kTo * C + 16 * wave + 4 * gq), beta = ld4(row + kBeta * C + 16 * wave + 4 * gq);
-        const f32x4 from = ld4(row + kFrom * C + 16 * wave + 4 * gq);
+        for (int t = 0; t < 4; ++t) kd[t] = py[t] = zero4();
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            py[nt] = py[nt] + to * kd[nt];             // du
-            st4(Ut + (16 * nt + r) * LC + 16 * wave + 4 * gq, beta * py[nt]);
-        }
-        __syncthreads();
-        f32x4 gu[2] = {zero4(), zero4()};
-        for (int s = wave; s < 4; ++s) {
-            const f32x4 ga = ld4(in_Gt + iq * C + 16 * s + 4 * gq);
+        for (int s = 0; s < DKP / 32; ++s) {
+            bf16x8 sb[3];
+            split8<3>(S[2 * s], S[2 * s + 1], sb);
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma(gu[nt], ga, ld4(Ut + (16 * nt + r) * LC + 16 * s + 4 * gq));
-        }
-        __syncthreads();
-        float* out_r = reinterpret_cast<float*>(ws + p.off_r) + ch * C * p.dvp + n0;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const f32x4 rr = py[nt] - gu[nt], dv = beta * rr;
-            // rows of dS0: exp(c) (scale q dY - k dv), dY and dv with their factor
-            st4(Ut + (16 * nt + r) * LC + 16 * wave + 4 * gq, from * dv);
-            float* y = Yt + (16 * nt + r) * LC + 16 * wave + 4 * gq;
-            st4(y, ld4(y) * from * d.scale);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 16 * wave + 4 * gq + j, nn = n0 + 16 * nt + r;
-                out_r[i * p.dvp + 16 * nt + r] = rr[j];
-                if (i < rows && nn < Dv) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t0 + i, h) + nn, dv[j]);
+            for (int t = 0; t < 4; ++t) {
+                bf16x8 ka[PL];
+                row_frag<PL, DKP>(K, row_of(t, m), 4 * s + gq, ka);
+                mma<PL, 3>(kd[t], ka, sb);
             }
         }
-        __syncthreads();
+        bf16x8 yb[2][PL];                              // dY in this wave's columns
+        col_frag<PL, W>(Y, 0, 2 * wave + ((m & 3) >> 1), m & 1, yb[0]);
+        col_frag<PL, W>(Y, 1, 2 * wave + ((m & 3) >> 1), m & 1, yb[1]);
+        f32x4 y[4];                                    // the same as floats
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int z = 0; z < PL; ++z) {
+                uint32_t wd[4];
+                __builtin_memcpy(wd, &yb[s][z], 16);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = __uint_as_float(j & 1 ? wd[j / 2] & 0xffff0000u : wd[j / 2] << 16);
+                    y[2 * s + (j >> 2)][j & 3] = z ? y[2 * s + (j >> 2)][j & 3] + v : v;
+                }
+            }
+        f32x4 du[4], r[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int s = t / 2; s < 2; ++s) {
+                bf16x8 pa[3];
+                tri_frag<3>(P, upper_piece(t, s), pa);
+                mma<3, PL>(py[t], pa, yb[s]);
+            }
+            const int i = row_of(t, 4 * gq);
+            du[t] = py[t] + ld4(row + kTo * C + i) * ld4(row + kNk * C + i) * kd[t];
+            r[t] = ld4(row + kBeta * C + i) * du[t];
+        }
+        {
+            bf16x8 ub[2][3];
+            split8<3>(r[0], r[1], ub[0]);
+            split8<3>(r[2], r[3], ub[1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f32x4 gu = zero4();
+#pragma unroll
+                for (int s = t / 2; s < 2; ++s) {
+                    bf16x8 ga[3];
+                    tri_frag<3>(G, upper_piece(t, s), ga);
+                    mma<3, 3>(gu, ga, ub[s]);
+                }
+                r[t] = du[t] - gu;
+            }
+        }
+        float* const out_r = reinterpret_cast<float*>(ws + p.off_r) + ch * C * p.dvp + n0 + m;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int i = row_of(t, 4 * gq);
+            const f32x4 dv = ld4(row + kBeta * C + i) * r[t], from = ld4(row + kFrom * C + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                out_r[(i + j) * p.dvp] = r[t][j];
+                if (i + j < rows && mine) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t0 + i + j, h) + n0 + m, dv[j]);
+            }
+            // rows of exp(c) (scale Q^T dY - K^T dv)
+            y[t] = y[t] * (d.scale * from * ld4(row + kNq * C + i));
+            r[t] = -dv * from * ld4(row + kNk * C + i);
+        }
+        bf16x8 ys[2][3], vs[2][3];
+        split8<3>(y[0], y[1], ys[0]);
+        split8<3>(y[2], y[3], ys[1]);
+        split8<3>(r[0], r[1], vs[0]);
+        split8<3>(r[2], r[3], vs[1]);
         const float whole = row[kFrom * C + C - 1];
 #pragma unroll
-        for (int x = 0; x < TILES; ++x) {
-            f32x4 add = zero4(), sub = zero4();
+        for (int x = 0; x < DT; ++x) {
+            S[x] = whole * S[x];
 #pragma unroll
-            for (int s = 0; s < C / 16; ++s) {
-                f32x4 ka, qa;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = 16 * s + 4 * gq + j;
-                    ka[j] = K[i * LK + 16 * dt_of(x) + r];
-                    qa[j] = Q[i * LK + 16 * dt_of(x) + r];
-                }
-                mma(add, qa, ld4(Yt + (16 * nt_of(x) + r) * LC + 16 * s + 4 * gq));
-                mma(sub, ka, ld4(Ut + (16 * nt_of(x) + r) * LC + 16 * s + 4 * gq));
+            for (int s = 0; s < 2; ++s) {
+                bf16x8 kt[PL], qt[PL];
+                col_frag<PL, DKP>(K, s, 4 * (x >> 1) + (m & 3), x & 1, kt);
+                col_frag<PL, DKP>(Q, s, 4 * (x >> 1) + (m & 3), x & 1, qt);
+                mma<PL, 3>(S[x], kt, vs[s]);
+                mma<PL, 3>(S[x], qt, ys[s]);
             }
-            S[x] = whole * S[x] + (add - sub);
-            st4(St + (16 * nt_of(x) + r) * LK + 16 * dt_of(x) + 4 * gq, S[x]);
         }
-        __syncthreads();
     }
-    if (!a.dh0) return;
+    if (!a.dh0 || !mine) return;
 #pragma unroll
-    for (int x = 0; x < TILES; ++x) {
-        const int nn = n0 + 16 * nt_of(x) + r;
+    for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = 16 * dt_of(x) + 4 * gq + j;
-            if (dd < Dk && nn < Dv) a.dh0[(bh * Dk + dd) * Dv + nn] = S[x][j];
+            const int dd = row_of(x, 4 * gq) + j;
+            if (dd < Dk) a.dh0[(bh * Dk + dd) * Dv + n0 + m] = S[x][j];
         }
-    }
 }
 
 // ---- gradients of a chunk's rows -----------------------------------------------------
 
-// 16 x 16 values of a wave, summed over each row's 16 lanes: all of them get it.
-__device__ __forceinline__ f32x4 row_sums(f32x4 v) {
+// A block has a chunk; wave w rows 16 w .. + 15, of which lane (gq, m) has row 16 w + m in
+// four columns 16 x + 4 gq .. of every tile x.
+constexpr int GRAD_NT = 256, GS = 32;                // GS: state columns at a time
+template <int DKP>
+__device__ __forceinline__ int slice_at(int row, int c) { return row * GS + ((c ^ (row >> 2)) & 3) * 8; }
+__device__ __forceinline__ float quad_sum(float v) {  // over the four lanes of a row
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+template <typename TS>
+__device__ __forceinline__ void put4(TS* p, int at, int D, const f32x4& v) {
+    if (at + 4 <= D) {
+        const float t[4] = {v[0], v[1], v[2], v[3]};
+        store_vec<4>(p + at, t);
+    } else {
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1)
+        for (int j = 0; j < 4; ++j)
+            if (at + j < D) put(p + at + j, v[j]);
+    }
+}
+// Four values of a row in LDS planes, columns 16 x + 4 gq ..
+template <int PL, int W>
+__device__ __forceinline__ f32x4 row_values(const uint16_t* lds, int row, int x, int gq) {
+    f32x4 v = zero4();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], o, 64);
+    for (int n = 0; n < PL; ++n) {
+        uint32_t w[2];
+        __builtin_memcpy(w, lds + n * C * W + piece_at<W>(row, 2 * x + (gq >> 1)) + 4 * (gq & 1), 8);
+        const f32x4 t = {__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                         __uint_as_float(w[1] & 0xffff0000u)};
+        v = n ? v + t : t;
+    }
     return v;
 }
 
 template <typename TS, int DKP>
-__global__ void __launch_bounds__(NT) delta_grad_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
-    extern __shared__ float lds[];
-    constexpr int LK = DKP + 4, DT = DKP / 16;
-    float* K = lds;                                    // [64][LK]
-    float* Q = K + C * LK;
-    float* PD = Q + C * LK;                            // [64][LC]: scale dP D
-    float* XD = PD + C * LC;                           // X D
-    float* E = XD + C * LC;                            // dP P - X A, and its sums along rows
-    float* row = E + C * LC;                           // [8][64]
-    float* xs = row + kFields * C;                     // [64] parts of rows that come from S0
-    float* zs = xs + C;                                // [64] parts of rows that reach dS1
-    float* part = zs + C;                              // [4] of <dS1, S0>
+__global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int PL = planes_of<TS>::n, DT = DKP / 16, NT = GRAD_NT;
+    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
+    uint16_t* const Q = K + PL * C * DKP;
+    uint16_t* const S0 = Q + PL * C * DKP;                         // [3][DKP][32]
+    uint16_t* const S1 = S0 + 3 * DKP * GS;                        // [3][DKP][32]: dS
+    uint16_t* const U = S1 + 3 * DKP * GS;                         // [3][64][32]: u
+    float* const PD = reinterpret_cast<float*>(S0);                // [64][LC]: scale dP D, in their place
+    float* const XD = PD + C * LC;                                 // X D
+    float* const E = XD + C * LC;                                  // dP P - X A, and its sums along rows
+    constexpr int STATES = 3 * GS * (2 * DKP + C) * 2, PAIRS = 3 * C * LC * 4;
+    float* const row = reinterpret_cast<float*>(reinterpret_cast<char*>(S0) + (STATES > PAIRS ? STATES : PAIRS));
+    float* const xs = row + kFields * C;                           // [64] parts of rows that come from S0
+    float* const zs = xs + C;                                      // [64] parts of rows that reach dS1
+    float* const part = zs + C;                                    // [4] of <dS1, S0>
     const int64_t n = blockIdx.x % (unsigned)p.chunks, bh = blockIdx.x / (unsigned)p.chunks;
     const int64_t b = bh / d.Hv, h = bh % d.Hv, share = d.Hv / d.Hk, hk = h / share;
     const int64_t t0 = n * C, ch = bh * p.chunks + n;
     const int Dk = (int)d.Dk, Dv = (int)d.Dv;
     const int rows = length_of(a, b, d.T) - (int)t0;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, gq = lane >> 4;
-    const int inside = (int)(d.T - t0 < C ? d.T - t0 : C);   // rows of the chunk that the arrays have
-    TS* const dq = static_cast<TS*>(a.dq) + at_row(d.dq, b, t0, hk);
-    TS* const dk = static_cast<TS*>(a.dk) + at_row(d.dk, b, t0, hk);
-    float* const part_q = reinterpret_cast<float*>(ws + p.off_dq) + ((b * d.T + t0) * d.Hv + h) * Dk;
-    float* const part_k = reinterpret_cast<float*>(ws + p.off_dk) + ((b * d.T + t0) * d.Hv + h) * Dk;
-    if (rows <= 0) {                                   // uniform
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int inside = (int)(d.T - t0 < C ? d.T - t0 : C);         // rows of the chunk that the arrays have
+    const int im = 16 * wave + m;                                  // this lane's row
+    TS* const dq = static_cast<TS*>(a.dq) + at_row(d.dq, b, t0 + im, hk);
+    TS* const dk = static_cast<TS*>(a.dk) + at_row(d.dk, b, t0 + im, hk);
+    if (rows <= 0) {                                               // uniform
         if (tid < inside) {
             a.dg[(b * d.T + t0 + tid) * d.Hv + h] = 0.0f;
             a.dbeta[(b * d.T + t0 + tid) * d.Hv + h] = 0.0f;
         }
-        if (share == 1)
-            for (int e = tid; e < inside * Dk; e += NT) {
-                put(dq + e / Dk * d.dq.row + e % Dk, 0.0f);
-                put(dk + e / Dk * d.dk.row + e % Dk, 0.0f);
+        if (share == 1 && im < inside)
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {
+                put4(dq, 16 * x + 4 * gq, Dk, zero4());
+                put4(dk, 16 * x + 4 * gq, Dk, zero4());
             }
         return;
     }
-    const float* in_row = reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C;
-    for (int i = tid; i < kFields * C; i += NT) row[i] = in_row[i];
-    fill_rows<TS, DKP>(K, static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
-    fill_rows<TS, DKP>(Q, static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, Dk);
-    __syncthreads();
-    scale_rows<DKP>(K, row + kNk * C);
-    scale_rows<DKP>(Q, row + kNq * C);
-    __syncthreads();
-    const float* S0 = reinterpret_cast<const float*>(ws + p.off_S) + ch * DKP * p.dvp;
-    const float* dS = reinterpret_cast<const float*>(ws + p.off_dS) + ch * DKP * p.dvp;
-    const float* in_w = reinterpret_cast<const float*>(ws + p.off_w) + ch * C * p.dvp;
-    const float* in_r = reinterpret_cast<const float*>(ws + p.off_r) + ch * C * p.dvp;
-    const int im = 16 * wave + r;                      // this lane's row of A operands
-    const float beta_m = row[kBeta * C + im];
-    const TS* dy = static_cast<const TS*>(a.dy) + ((b * d.T + t0 + (im < rows ? im : 0)) * d.Hv + h) * Dv;
+    {
+        Carry<TS, DKP, NT> ck, cq;
+        CarryBytes<kFields * C * 4, NT> cr;
+        ck.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
+        cq.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, Dk);
+        cr.load(reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C);
+        ck.store(K);
+        cq.store(Q);
+        cr.store(row);
+    }
+    const float* const in_S = reinterpret_cast<const float*>(ws + p.off_S) + ch * DKP * p.dvp;
+    const float* const in_dS = reinterpret_cast<const float*>(ws + p.off_dS) + ch * DKP * p.dvp;
+    const float* const in_w = reinterpret_cast<const float*>(ws + p.off_w) + (ch * C + im) * p.dvp;
+    const float* const in_r = reinterpret_cast<const float*>(ws + p.off_r) + (ch * C + im) * p.dvp;
+    const TS* const dy = static_cast<const TS*>(a.dy) + ((b * d.T + t0 + (im < rows ? im : 0)) * d.Hv + h) * Dv;
+    const float* const rows_at = reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C;
+    const float beta_m = rows_at[kBeta * C + im];
     f32x4 ys[DT], vs[DT], us[DT], dP[4], X[4];
 #pragma unroll
     for (int x = 0; x < DT; ++x) ys[x] = vs[x] = us[x] = zero4();
 #pragma unroll
     for (int x = 0; x < 4; ++x) dP[x] = X[x] = zero4();
     float rw = 0.0f, ss = 0.0f;
-    for (int s = 0; s < p.dvp / 16; ++s) {
-        const int at = 16 * s + 4 * gq;
-        const f32x4 ya = im < rows ? row4<TS>(dy, at, Dv) : zero4();
-        const f32x4 wa = ld4(in_w + im * p.dvp + at), ra = ld4(in_r + im * p.dvp + at);
-        const f32x4 ua = beta_m * wa, va = beta_m * ra;
+    constexpr int SP = DKP * GS / 8 / NT > 0 ? DKP * GS / 8 / NT : 1;      // pieces of a state's slice, a thread
+    Piece<float> s0[SP], s1[SP];
+    Piece<TS> py;
+    f32x4 wn[2], rn[2];
+    auto fetch = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rw = __builtin_fmaf(wa[j], ra[j], rw);
+        for (int x = 0; x < SP; ++x) {
+            const int e = tid + NT * x, dd = e / (GS / 8), c = e % (GS / 8);
+            if (e >= DKP * GS / 8) break;
+            load_piece(s0[x], in_S + dd * p.dvp + GS * s, 8 * c, GS);
+            load_piece(s1[x], in_dS + dd * p.dvp + GS * s, 8 * c, GS);
+        }
+        const int at = GS * s + 8 * gq;
+        if (im < rows && at < Dv) load_piece(py, dy, at, Dv);
+        else no_piece(py);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) wn[z] = ld4(in_w + at + 4 * z), rn[z] = ld4(in_r + at + 4 * z);
+    };
+    fetch(0);
+    const int steps = (Dv + GS - 1) / GS;
+    for (int s = 0; s < steps; ++s) {
+        bf16x8 ya[PL], ua[3], va[3];
+        piece_planes(py, ya);
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rw = __builtin_fmaf(wn[z][j], rn[z][j], rw);
+        split8<3>(beta_m * wn[0], beta_m * wn[1], ua);
+        split8<3>(beta_m * rn[0], beta_m * rn[1], va);
+        __syncthreads();                               // the slice before is done with LDS
+#pragma unroll
+        for (int x = 0; x < SP; ++x) {
+            const int e = tid + NT * x, dd = e / (GS / 8), c = e % (GS / 8);
+            if (e >= DKP * GS / 8) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(s0[x].v[j], s1[x].v[j], ss);
+            bf16x8 v[3];
+            piece_planes(s0[x], v);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(S0 + z * DKP * GS + slice_at<DKP>(dd, c)) = v[z];
+            piece_planes(s1[x], v);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(S1 + z * DKP * GS + slice_at<DKP>(dd, c)) = v[z];
+        }
+#pragma unroll
+        for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(U + z * C * GS + slice_at<C>(im, gq)) = ua[z];
+        __syncthreads();
+        if (s + 1 < steps) fetch(s + 1);
 #pragma unroll
         for (int x = 0; x < DT; ++x) {
-            const f32x4 sb = ld4(S0 + (16 * x + r) * p.dvp + at), db = ld4(dS + (16 * x + r) * p.dvp + at);
-            mma(ys[x], ya, sb);
-            mma(vs[x], va, sb);
-            mma(us[x], ua, db);
-            if ((x & 3) == wave)
+            bf16x8 sb[3], db[3];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ss = __builtin_fmaf(sb[j], db[j], ss);
+            for (int z = 0; z < 3; ++z) {
+                sb[z] = *reinterpret_cast<const bf16x8*>(S0 + z * DKP * GS + slice_at<DKP>(16 * x + m, gq));
+                db[z] = *reinterpret_cast<const bf16x8*>(S1 + z * DKP * GS + slice_at<DKP>(16 * x + m, gq));
+            }
+            mma<3, PL>(ys[x], sb, ya);
+            mma<3, 3>(vs[x], sb, va);
+            mma<3, 3>(us[x], db, ua);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             if (x > wave) break;
-            const f32x4 ub = row[kBeta * C + 16 * x + r] * ld4(in_w + (16 * x + r) * p.dvp + at);
-            mma(dP[x], ya, ub);
-            mma(X[x], va, ub);
+            bf16x8 ub[3];
+#pragma unroll
+            for (int z = 0; z < 3; ++z) ub[z] = *reinterpret_cast<const bf16x8*>(U + z * C * GS + slice_at<C>(16 * x + m, gq));
+            mma<3, PL>(dP[x], ub, ya);
+            mma<3, 3>(X[x], ub, va);
         }
     }
-    rw += __shfl_xor(rw, 16, 64);
-    rw += __shfl_xor(rw, 32, 64);
+    rw = quad_sum(rw);
     if (gq == 0 && im < inside) a.dbeta[(b * d.T + t0 + im) * d.Hv + h] = im < rows ? rw : 0.0f;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) ss += __shfl_xor(ss, o, 64);
     if (lane == 0) part[wave] = ss;
-    // the states' parts, with their factors
-    const f32x4 from = ld4(row + kFrom * C + 16 * wave + 4 * gq), to = ld4(row + kTo * C + 16 * wave + 4 * gq);
-    f32x4 xr = zero4(), zr = zero4();
+    __syncthreads();                                   // the states' slices are done with
+    // the states' parts, with their factors; gradients of q and k as they were divided
+    const float from = row[kFrom * C + im], to = row[kTo * C + im], nk = row[kNk * C + im], nq = row[kNq * C + im];
+    float xr = 0.0f, zr = 0.0f;
 #pragma unroll
     for (int x = 0; x < DT; ++x) {
-        ys[x] = d.scale * (from * ys[x]);
+        const f32x4 qv = nq * row_values<PL, DKP>(Q, im, x, gq), kv = nk * row_values<PL, DKP>(K, im, x, gq);
+        ys[x] = (d.scale * from) * ys[x];
         vs[x] = from * vs[x];
         us[x] = to * us[x];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int at = (16 * wave + 4 * gq + j) * LK + 16 * x + r;
-            xr[j] += Q[at] * ys[x][j] - K[at] * vs[x][j];
-            zr[j] += K[at] * us[x][j];
+            xr += qv[j] * ys[x][j] - kv[j] * vs[x][j];
+            zr += kv[j] * us[x][j];
         }
         us[x] = us[x] - vs[x];                         // dk so far; ys: dq so far
     }
-    xr = row_sums(xr);
-    zr = row_sums(zr);
-    if (r == 0) {
-        st4(xs + 16 * wave + 4 * gq, xr);
-        st4(zs + 16 * wave + 4 * gq, zr);
+    xr = quad_sum(xr);
+    zr = quad_sum(zr);
+    if (gq == 0) xs[im] = xr, zs[im] = zr;
+    // pairs of rows: this lane's row i = im against rows j = 16 x + 4 gq ..
+    f32x4 qk[4], kk[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) qk[x] = kk[x] = zero4();
+#pragma unroll
+    for (int s = 0; s < DKP / 32; ++s) {
+        bf16x8 ka[PL], qa[PL];
+        row_frag<PL, DKP>(K, im, 4 * s + gq, ka);
+        row_frag<PL, DKP>(Q, im, 4 * s + gq, qa);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (x > wave) break;
+            bf16x8 kb[PL];
+            row_frag<PL, DKP>(K, 16 * x + m, 4 * s + gq, kb);
+            mma<PL, PL>(qk[x], kb, qa);
+            mma<PL, PL>(kk[x], kb, ka);
+        }
     }
-    // pairs of rows
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        f32x4 qk = zero4(), kk = zero4();
-        if (x <= wave) {
-#pragma unroll
-            for (int s = 0; s < DT; ++s) {
-                const f32x4 kb = ld4(K + (16 * x + r) * LK + 16 * s + 4 * gq);
-                mma(qk, ld4(Q + im * LK + 16 * s + 4 * gq), kb);
-                mma(kk, ld4(K + im * LK + 16 * s + 4 * gq), kb);
-            }
-        }
-        const int j = 16 * x + r;
+        const int j0 = 16 * x + 4 * gq;
+        const f32x4 nj = ld4(row + kNk * C + j0);
+        f32x4 pd, xd, e;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const int i = 16 * wave + 4 * gq + y;
-            const float D = j <= i ? decay(row, i, j) : 0.0f;
-            const float pd = j <= i ? d.scale * (dP[x][y] * D) : 0.0f, xd = j < i ? X[x][y] * D : 0.0f;
-            PD[i * LC + j] = pd;
-            XD[i * LC + j] = xd;
-            E[i * LC + j] = j < i ? pd * qk[y] - xd * kk[y] : 0.0f;
+            const int j = j0 + y;
+            const float D = j <= im ? decay(row, im, j) : 0.0f;
+            pd[y] = j <= im ? d.scale * (dP[x][y] * D) : 0.0f;
+            xd[y] = j < im ? X[x][y] * D : 0.0f;
+            e[y] = j < im ? nj[y] * (pd[y] * (nq * qk[x][y]) - xd[y] * (nk * kk[x][y])) : 0.0f;
         }
+        st4(PD + im * LC + j0, pd);
+        st4(XD + im * LC + j0, xd);
+        st4(E + im * LC + j0, e);
     }
     __syncthreads();
-    // products of the pairs with the rows; rows of K and Q as columns
+    // products of the pairs with the rows, which are divided here by their pair's factor
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        f32x4 pt, xt;
+    for (int s = 0; s < 2; ++s) {
+        const int j0 = 32 * s + 8 * gq;
+        f32x4 pr[2], pc[2], xc[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            pt[j] = PD[(16 * s + 4 * gq + j) * LC + im];
-            xt[j] = XD[(16 * s + 4 * gq + j) * LC + im];
+        for (int z = 0; z < 2; ++z) {
+            const f32x4 nkj = ld4(row + kNk * C + j0 + 4 * z), nqj = ld4(row + kNq * C + j0 + 4 * z);
+            pr[z] = ld4(PD + im * LC + j0 + 4 * z) * nkj;
+            xc[z] = ld4(XD + im * LC + j0 + 4 * z);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int j = j0 + 4 * z + y;
+                pc[z][y] = PD[j * LC + im];
+                xc[z][y] += XD[j * LC + im];
+            }
+            pc[z] = pc[z] * nqj;
+            xc[z] = -xc[z] * nkj;
         }
-        const f32x4 pa = ld4(PD + im * LC + 16 * s + 4 * gq), xa = ld4(XD + im * LC + 16 * s + 4 * gq) + xt;
+        bf16x8 pra[3], pca[3], xca[3];
+        split8<3>(pr[0], pr[1], pra);
+        split8<3>(pc[0], pc[1], pca);
+        split8<3>(xc[0], xc[1], xca);
 #pragma unroll
         for (int x = 0; x < DT; ++x) {
-            f32x4 kb, qb;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                kb[j] = K[(16 * s + 4 * gq + j) * LK + 16 * x + r];
-                qb[j] = Q[(16 * s + 4 * gq + j) * LK + 16 * x + r];
+            bf16x8 kt[PL], qt[PL];
+            col_frag<PL, DKP>(K, s, 2 * x + ((m & 3) >> 1), m & 1, kt);
+            if (s <= wave / 2) mma<PL, 3>(ys[x], kt, pra);
+            if (s >= wave / 2) {
+                col_frag<PL, DKP>(Q, s, 2 * x + ((m & 3) >> 1), m & 1, qt);
+                mma<PL, 3>(us[x], qt, pca);
             }
-            if (s <= wave) mma(ys[x], pa, kb);
-            if (s >= wave) mma(us[x], pt, qb);
-            mma(us[x], -xa, kb);
+            mma<PL, 3>(us[x], kt, xca);
         }
     }
     // dg: sums of E along rows (wave 0, a row to a lane), then down the columns
@@ -763,51 +1120,55 @@ __global__ void __launch_bounds__(NT) delta_grad_kernel(kan_delta_desc_t d, Delt
         dg += row[kFrom * C + C - 1] * (part[0] + part[1] + part[2] + part[3]);
         if (lane < inside) a.dg[(b * d.T + t0 + lane) * d.Hv + h] = lane < rows ? dg : 0.0f;
     }
+    if (im >= inside) return;
     if (share > 1) {
+        if (im >= rows) return;
+        const int64_t at = ((b * d.T + t0 + im) * d.Hv + h) * Dk;
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 16 * wave + 4 * gq + j, dd = 16 * x + r;
-                if (i < rows && dd < Dk) {
-                    part_q[(int64_t)i * d.Hv * Dk + dd] = ys[x][j];
-                    part_k[(int64_t)i * d.Hv * Dk + dd] = us[x][j];
-                }
-            }
+        for (int x = 0; x < DT; ++x) {
+            put4(reinterpret_cast<float*>(ws + p.off_dq) + at, 16 * x + 4 * gq, Dk, ys[x]);
+            put4(reinterpret_cast<float*>(ws + p.off_dk) + at, 16 * x + 4 * gq, Dk, us[x]);
+        }
         return;
     }
-    if (d.flags & KAN_DELTA_UNIT) {                    // through x / sqrt(x.x + eps), x here already divided
-        f32x4 qd = zero4(), kd = zero4();
+    if (d.flags & KAN_DELTA_UNIT) {                    // through x / sqrt(x.x + eps)
+        float qd = 0.0f, kd = 0.0f;
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
+        for (int x = 0; x < DT; ++x) {
+            const f32x4 qv = row_values<PL, DKP>(Q, im, x, gq), kv = row_values<PL, DKP>(K, im, x, gq);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = (16 * wave + 4 * gq + j) * LK + 16 * x + r;
-                qd[j] += Q[at] * ys[x][j];
-                kd[j] += K[at] * us[x][j];
-            }
-        qd = row_sums(qd);
-        kd = row_sums(kd);
-        const f32x4 nq = ld4(row + kNq * C + 16 * wave + 4 * gq), nk = ld4(row + kNk * C + 16 * wave + 4 * gq);
+            for (int j = 0; j < 4; ++j) qd += qv[j] * ys[x][j], kd += kv[j] * us[x][j];
+        }
+        qd = quad_sum(qd) * nq * nq;
+        kd = quad_sum(kd) * nk * nk;
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = (16 * wave + 4 * gq + j) * LK + 16 * x + r;
-                ys[x][j] = nq[j] * (ys[x][j] - Q[at] * qd[j]);
-                us[x][j] = nk[j] * (us[x][j] - K[at] * kd[j]);
-            }
+        for (int x = 0; x < DT; ++x) {
+            const f32x4 qv = row_values<PL, DKP>(Q, im, x, gq), kv = row_values<PL, DKP>(K, im, x, gq);
+            ys[x] = nq * (ys[x] - qd * qv);
+            us[x] = nk * (us[x] - kd * kv);
+        }
     }
 #pragma unroll
-    for (int x = 0; x < DT; ++x)
+    for (int x = 0; x < DT; ++x) {
+        put4(dq, 16 * x + 4 * gq, Dk, im < rows ? ys[x] : zero4());
+        put4(dk, 16 * x + 4 * gq, Dk, im < rows ? us[x] : zero4());
+    }
+}
+
+constexpr int NT = 256;              // threads of the row-wise kernels' blocks
+template <typename TS>
+__device__ __forceinline__ f32x4 row4(const TS* p, int at, int D) {    // zero past the row's end
+    f32x4 v = zero4();
+    if (at + 4 <= D) {
+        const Raw<TS, 4> r = load_raw<TS, 4>(p + at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = 16 * wave + 4 * gq + j, dd = 16 * x + r;
-            if (i < inside && dd < Dk) {
-                put(dq + i * d.dq.row + dd, i < rows ? ys[x][j] : 0.0f);
-                put(dk + i * d.dk.row + dd, i < rows ? us[x][j] : 0.0f);
-            }
-        }
+        for (int i = 0; i < 4; ++i) v[i] = raw_value(r, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at + i < D) v[i] = load_f(p, at + i);
+    }
+    return v;
 }
 
 // Heads that share a key: their gradients summed in order, a wave to a row of q
@@ -937,29 +1298,40 @@ __global__ void __launch_bounds__(NT) delta_step_kernel(kan_delta_desc_t d, int6
 
 // ---- launches ----------------------------------------------------------------------
 
-template <typename K>
-hipError_t set_lds(K kernel, size_t bytes) {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)bytes);
+template <typename K, typename... Args>
+hipError_t launch(K kernel, int64_t blocks, int threads, size_t lds, hipStream_t s, Args... args) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), lds, s, args...);
+    return hipGetLastError();
 }
 
 template <typename TS, int DKP, bool BWD>
 hipError_t prep(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    constexpr size_t lds = 4 * (2 * C * (DKP + 4) + 2 * C * LC + kFields * C);
-    const hipError_t e = set_lds(delta_prep_kernel<TS, DKP, BWD>, lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_prep_kernel<TS, DKP, BWD>), dim3((unsigned)(p.heads * p.chunks)), dim3(NT), lds, s, d, p,
-                       a, ws);
-    return hipGetLastError();
+    constexpr size_t rows = 4 * planes_of<TS>::n * C * DKP, pairs = 8 * C * LC;
+    return launch(delta_prep_kernel<TS, DKP, BWD>, p.heads * p.chunks, PREP_NT,
+                  (rows > pairs ? rows : pairs) + 4 * kFields * C, s, d, p, a, ws);
 }
-template <typename TS, int DKP, bool BWD>
-hipError_t scan(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    constexpr size_t lds = 4 * ((C + NV) * (DKP + 4) + 2 * NV * LC + kFields * C);
-    const hipError_t e = set_lds(delta_scan_kernel<TS, DKP, BWD>, lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_scan_kernel<TS, DKP, BWD>), dim3((unsigned)(p.heads * (p.dvp / NV))), dim3(NT), lds, s, d,
-                       p, a, ws);
-    return hipGetLastError();
+template <typename TS, int DKP, int WAVES, bool BWD>
+hipError_t scan_w(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    constexpr size_t lds = (size_t)(BWD ? 1 : 2) * planes_of<TS>::n * C * DKP * 2 +
+                           (BWD ? 3 : 3 + out_planes<TS>::n) * kTri * 2 + 4 * kFields * C;
+    return launch(delta_scan_kernel<TS, DKP, WAVES, BWD>, p.heads * ((d.Dv + 16 * WAVES - 1) / (16 * WAVES)), 64 * WAVES,
+                  lds, s, d, p, a, ws);
+}
+template <typename TS, int DKP, int WAVES>
+hipError_t back_w(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    constexpr size_t lds = planes_of<TS>::n * C * (2 * DKP + 16 * WAVES) * 2 + 6 * kTri * 2 + 4 * kFields * C;
+    return launch(delta_back_kernel<TS, DKP, WAVES>, p.heads * ((d.Dv + 16 * WAVES - 1) / (16 * WAVES)), 64 * WAVES, lds,
+                  s, d, p, a, ws);
+}
+template <typename TS, int DKP>
+hipError_t grad(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    constexpr size_t states = 3 * GS * (2 * DKP + C) * 2, pairs = 3 * C * LC * 4;
+    constexpr size_t lds = planes_of<TS>::n * C * 2 * DKP * 2 + (states > pairs ? states : pairs) + 4 * kFields * C +
+                           8 * C + 16;
+    return launch(delta_grad_kernel<TS, DKP>, p.heads * p.chunks, GRAD_NT, lds, s, d, p, a, ws);
 }
 template <typename TS, int DKP>
 hipError_t forward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
@@ -967,25 +1339,19 @@ hipError_t forward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArg
         const hipError_t e = prep<TS, DKP, false>(d, p, a, ws, s);
         if (e != hipSuccess) return e;
     }
-    return scan<TS, DKP, false>(d, p, a, ws, s);
+    return p.waves == 4 ? scan_w<TS, DKP, 4, false>(d, p, a, ws, s) : scan_w<TS, DKP, 2, false>(d, p, a, ws, s);
 }
 template <typename TS, int DKP>
 hipError_t backward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
     hipError_t e;
     if (p.chunks > 0) {
         if ((e = prep<TS, DKP, true>(d, p, a, ws, s)) != hipSuccess) return e;
-        if ((e = scan<TS, DKP, true>(d, p, a, ws, s)) != hipSuccess) return e;
+        e = p.waves == 4 ? scan_w<TS, DKP, 4, true>(d, p, a, ws, s) : scan_w<TS, DKP, 2, true>(d, p, a, ws, s);
+        if (e != hipSuccess) return e;
     }
-    constexpr size_t lds_b = 4 * ((2 * C + NV) * (DKP + 4) + 2 * NV * LC + kFields * C);
-    if ((e = set_lds(delta_back_kernel<TS, DKP>, lds_b)) != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_back_kernel<TS, DKP>), dim3((unsigned)(p.heads * (p.dvp / NV))), dim3(NT), lds_b, s, d, p,
-                       a, ws);
-    if ((e = hipGetLastError()) != hipSuccess || p.chunks == 0) return e;
-    constexpr size_t lds_g = 4 * (2 * C * (DKP + 4) + 3 * C * LC + kFields * C + 2 * C + 4);
-    if ((e = set_lds(delta_grad_kernel<TS, DKP>, lds_g)) != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_grad_kernel<TS, DKP>), dim3((unsigned)(p.heads * p.chunks)), dim3(NT), lds_g, s, d, p, a,
-                       ws);
-    if ((e = hipGetLastError()) != hipSuccess || d.Hv == d.Hk) return e;
+    e = p.waves == 4 ? back_w<TS, DKP, 4>(d, p, a, ws, s) : back_w<TS, DKP, 2>(d, p, a, ws, s);
+    if (e != hipSuccess || p.chunks == 0) return e;
+    if ((e = grad<TS, DKP>(d, p, a, ws, s)) != hipSuccess || d.Hv == d.Hk) return e;
     const int64_t blocks = (d.B * d.T * d.Hk + NT / 64 - 1) / (NT / 64), x = std::min<int64_t>(blocks, 1 << 16);
     hipLaunchKernelGGL((delta_heads_kernel<TS>), dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(NT), 0, s, d,
                        p, a, (const char*)ws);

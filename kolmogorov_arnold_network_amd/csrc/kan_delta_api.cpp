@@ -90,29 +90,30 @@ int64_t join_max_rows(int64_t D) { return int64_t(1) << (D > 4096 ? 21 : D > 102
 
 DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass) {
     DeltaPlan p = {};
+    const bool back = pass == KAN_PASS_BACKWARD;
     p.dkp = d.Dk <= 32 ? 32 : d.Dk <= 64 ? 64 : 128;
-    p.dvp = (int)round_up(d.Dv, kDeltaTile);
+    p.dvp = (int)round_up(d.Dv, 64);
     p.chunks = (d.T + kDeltaChunk - 1) / kDeltaChunk;
     p.heads = d.B * d.Hv;
+    p.waves = p.heads * ((d.Dv + 63) / 64) >= 256 ? 4 : 2;
+    // three planes of a triangular matrix hold float32, two what y keeps in bfloat16
+    p.mats = (back ? 9 : d.dtype == KAN_F32 ? 6 : 5) * int64_t(6 * 64 * 16);
     size_t off = 0;
-    auto take = [&](int64_t each) {
+    auto take = [&](int64_t bytes) {
         const size_t o = off;
-        off += (size_t)round_up(p.heads * p.chunks * each * 4, 256);
+        off += (size_t)round_up(p.heads * p.chunks * bytes, 256);
         return o;
     };
-    p.off_rows = take(8 * kDeltaChunk);
-    p.off_G = take(kDeltaChunk * kDeltaChunk);
-    p.off_P = take(kDeltaChunk * kDeltaChunk);
-    if (pass == KAN_PASS_BACKWARD) {
-        p.off_Gt = take(kDeltaChunk * kDeltaChunk);
-        p.off_Pt = take(kDeltaChunk * kDeltaChunk);
-        p.off_w = take(kDeltaChunk * p.dvp);
-        p.off_r = take(kDeltaChunk * p.dvp);
-        p.off_S = take((int64_t)p.dkp * p.dvp);
-        p.off_dS = take((int64_t)p.dkp * p.dvp);
+    p.off_rows = take(8 * kDeltaChunk * 4);
+    p.off_mats = take(p.mats);
+    if (back) {
+        p.off_w = take(kDeltaChunk * p.dvp * 4);
+        p.off_r = take(kDeltaChunk * p.dvp * 4);
+        p.off_S = take((int64_t)p.dkp * p.dvp * 4);
+        p.off_dS = take((int64_t)p.dkp * p.dvp * 4);
         if (d.Hv > d.Hk) {
-            p.off_dq = take(kDeltaChunk * d.Dk);
-            p.off_dk = take(kDeltaChunk * d.Dk);
+            p.off_dq = take(kDeltaChunk * d.Dk * 4);
+            p.off_dk = take(kDeltaChunk * d.Dk * 4);
         }
     }
     p.ws = off;
