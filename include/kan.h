@@ -547,7 +547,7 @@ int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* 
  * dbeta [B, T, Hv] and h0, hT, dhT, dh0 [B, Hv, Dk, Dv] float32, contiguous. */
 #define KAN_DELTA_UNIT 1
 typedef struct {
-    int64_t seq, row, head;         /* strides, >= 0 */
+    int64_t seq, row, head;         /* strides, >= 0; row at most 2^24 */
 } kan_heads_t;
 typedef struct {
     int64_t B;                      /* sequences, >= 0 */

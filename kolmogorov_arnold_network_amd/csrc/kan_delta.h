@@ -6,6 +6,7 @@
 namespace kan {
 
 constexpr int kDeltaChunk = 64;      // rows of a chunk
+constexpr int64_t kDeltaMaxRow = int64_t(1) << 24;      // stride of rows: 64 of them within 2^32 bytes
 constexpr int kDeltaMaxDk = 128;
 constexpr int kDeltaMaxDv = 1024;
 constexpr int64_t kDeltaMaxHeads = int64_t(1) << 18;    // B Hv

@@ -48,7 +48,17 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // What a chunk's rows have for themselves: [8][64] floats of a chunk-head.
-enum RowField { kHi, kLo, kBeta, kNk, kNq, kFrom, kTo, kFields = 8 };
+enum RowField {
+    kBeta,
+    kFk,                             // exp(c) / |k|, |k| where rows are made unit vectors, else 1
+    kTk,                             // exp(c_63 - c) / |k|
+    kFq,                             // scale exp(c) / |q|
+    kNk,                             // 1 / |k|
+    kNq,                             // 1 / |q|
+    kHi,                             // c log2(e) as the sum of two floats
+    kLo,
+    kFields
+};
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 __device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -145,31 +155,31 @@ template <>
 struct Piece<uint16_t> {
     uint32_t w[4];
 };
+__device__ __forceinline__ void load_whole(Piece<uint16_t>& p, const uint16_t* from) {
+    const Raw<uint16_t, 8> r = load_raw<uint16_t, 8>(from);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.w[i] = r.w[i];
+}
+__device__ __forceinline__ void load_whole(Piece<float>& p, const float* from) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const Raw<float, 4> r = load_raw<float, 4>(from + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p.v[4 * h + i] = raw_value(r, i);
+    }
+}
 __device__ __forceinline__ void load_piece(Piece<uint16_t>& p, const uint16_t* row, int at, int D) {
-    if (at + 8 <= D) {
-        const Raw<uint16_t, 8> r = load_raw<uint16_t, 8>(row + at);
+    if (at + 8 <= D) return load_whole(p, row + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p.w[i] = r.w[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p.w[i] = at + 2 * i < D ? row[at + 2 * i] : 0u;
-            if (at + 2 * i + 1 < D) p.w[i] |= (uint32_t)row[at + 2 * i + 1] << 16;
-        }
+    for (int i = 0; i < 4; ++i) {
+        p.w[i] = at + 2 * i < D ? row[at + 2 * i] : 0u;
+        if (at + 2 * i + 1 < D) p.w[i] |= (uint32_t)row[at + 2 * i + 1] << 16;
     }
 }
 __device__ __forceinline__ void load_piece(Piece<float>& p, const float* row, int at, int D) {
-    if (at + 8 <= D) {
+    if (at + 8 <= D) return load_whole(p, row + at);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const Raw<float, 4> r = load_raw<float, 4>(row + at + 4 * h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p.v[4 * h + i] = raw_value(r, i);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p.v[i] = at + i < D ? row[at + i] : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) p.v[i] = at + i < D ? row[at + i] : 0.0f;
 }
 __device__ __forceinline__ void no_piece(Piece<uint16_t>& p) { p.w[0] = p.w[1] = p.w[2] = p.w[3] = 0u; }
 __device__ __forceinline__ void no_piece(Piece<float>& p) {
@@ -190,29 +200,55 @@ __device__ __forceinline__ void piece_planes(const Piece<float>& p, bf16x8 (&out
 }
 
 // The 64 rows of a chunk as NT threads carry them: rows `rows` and on, and columns D
-// and on, are zero.
-template <typename TS, int W, int NT>
+// and on, are zero.  EVEN: D is a multiple of eight, and a piece is loaded whole,
+// from the last row where there is no such row and from the first columns where
+// there are none, and becomes zero on its way to LDS.
+template <typename TS, int W, int NT, bool EVEN>
 struct Carry {
-    static constexpr int CH = W / 8, N = C * CH / NT > 0 ? C * CH / NT : 1;
+    static constexpr int CH = W / 8, N = C * CH / NT, RS = NT / CH, PL = planes_of<TS>::n;
+    static_assert(N >= 1 && NT % CH == 0 && C * CH % NT == 0, "whole rounds of pieces");
     Piece<TS> p[N];
     __device__ __forceinline__ void load(const TS* base, int64_t row_stride, int rows, int D) {
+        const int row = (int)threadIdx.x / CH, at = 8 * ((int)threadIdx.x % CH);
+        if constexpr (EVEN) {
+            const TS* from = base + (at < D ? at : 0);
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-            const int e = threadIdx.x + NT * x, row = e / CH, c = e % CH;
-            if (row < rows && 8 * c < D) load_piece(p[x], base + row * row_stride, 8 * c, D);
-            else no_piece(p[x]);
+            for (int x = 0; x < N; ++x) {
+                const int i = row + RS * x;
+                load_whole(p[x], from + (uint32_t)(i < rows ? i : rows - 1) * (uint32_t)row_stride);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const int i = row + RS * x;
+                if (i < rows && at < D) load_piece(p[x], base + i * row_stride, at, D);
+                else no_piece(p[x]);
+            }
         }
     }
-    __device__ __forceinline__ void store(uint16_t* lds) const {
-        constexpr int PL = planes_of<TS>::n;
+    __device__ __forceinline__ void put(uint16_t* lds, int x) const {
+        const int e = threadIdx.x + NT * x;
+        bf16x8 v[PL];
+        piece_planes(p[x], v);
+#pragma unroll
+        for (int n = 0; n < PL; ++n) *reinterpret_cast<bf16x8*>(lds + n * C * W + piece_at<W>(e / CH, e % CH)) = v[n];
+    }
+    __device__ __forceinline__ void store(uint16_t* lds, int rows, int D) const {
+        if (!EVEN || (rows >= C && D >= W)) {          // uniform
+#pragma unroll
+            for (int x = 0; x < N; ++x) put(lds, x);
+            return;
+        }
+        const bf16x8 zero = {};
+        const int row = (int)threadIdx.x / CH, c = (int)threadIdx.x % CH;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-            const int e = threadIdx.x + NT * x;
-            if (C * CH % NT != 0 && e >= C * CH) break;
-            bf16x8 v[PL];
-            piece_planes(p[x], v);
+            if (row + RS * x < rows && 8 * c < D) {
+                put(lds, x);
+            } else {
 #pragma unroll
-            for (int n = 0; n < PL; ++n) *reinterpret_cast<bf16x8*>(lds + n * C * W + piece_at<W>(e / CH, e % CH)) = v[n];
+                for (int n = 0; n < PL; ++n) *reinterpret_cast<bf16x8*>(lds + n * C * W + piece_at<W>(row + RS * x, c)) = zero;
+            }
         }
     }
 };
@@ -237,6 +273,52 @@ struct CarryBytes {
     }
 };
 
+// 64 rows, or BYTES that follow each other, from HBM to LDS without a register in
+// between (16 bytes a lane, a wave's lanes one after the other).  A lane asks for
+// the piece that belongs in its place; rows `rows` and on, and columns D and on, become
+// zero.  What is under way has arrived after `arrived` and a barrier.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void hbm_void;
+__device__ __forceinline__ void to_lds(const void* from, char* to) {
+    __builtin_amdgcn_global_load_lds((hbm_void*)from, (lds_void*)to, 16, 0, 0);
+}
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }      // vmcnt(0)
+template <int W, int NT>
+struct Direct {
+    static constexpr int CH = W / 8, N = C * CH / NT > 0 ? C * CH / NT : 1;     // fewer pieces than threads: whole waves
+    uint32_t off[N];                                   // this thread's pieces of a chunk, in bytes
+    __device__ __forceinline__ void plan(int64_t row_stride) {
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int e = threadIdx.x + NT * x, row = e / CH;
+            off[x] = 2 * ((uint32_t)row * (uint32_t)row_stride + 8 * (uint32_t)(piece_at<W>(row, e % CH) / 8 % CH));
+        }
+    }
+    __device__ __forceinline__ void load(const uint16_t* base, int rows, int D, uint16_t* lds) const {
+        const char* from = reinterpret_cast<const char*>(base);
+        char* to = reinterpret_cast<char*>(lds) + 16 * ((int)threadIdx.x & ~63);
+        if (rows >= C && D >= W) {                     // uniform
+#pragma unroll
+            for (int x = 0; x < N; ++x) to_lds(from + off[x], to + 16 * NT * x);
+            return;
+        }
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int e = threadIdx.x + NT * x, row = e / CH, c = piece_at<W>(row, e % CH) / 8 % CH;
+            if (row < rows && 8 * c < D) to_lds(from + off[x], to + 16 * NT * x);
+            else *reinterpret_cast<u32x4v*>(reinterpret_cast<char*>(lds) + 16 * e) = u32x4v{0u, 0u, 0u, 0u};
+        }
+    }
+};
+template <int BYTES, int NT>
+__device__ __forceinline__ void bytes_to_lds(const void* from, char* lds) {
+    const int first = (int)threadIdx.x & ~63;
+#pragma unroll
+    for (int x = 0; x < (BYTES / 16 + NT - 1) / NT; ++x)
+        if (first + NT * x < BYTES / 16)               // whole waves: BYTES is a multiple of 1024
+            to_lds(static_cast<const char*>(from) + 16 * ((int)threadIdx.x + NT * x), lds + 16 * (first + NT * x));
+}
+
 // A triangular matrix of 64 x 64 as left operand: six pieces [tile][32 columns] of 64
 // lanes by eight values are not zero, a plane after the other.
 constexpr int kTri = 6 * 64 * 8;
@@ -252,13 +334,27 @@ __device__ __forceinline__ void tri_frag(const uint16_t* lds, int piece, bf16x8 
 __device__ __forceinline__ int64_t at_row(const kan_heads_t& s, int64_t b, int64_t t, int64_t h) {
     return b * s.seq + t * s.row + h * s.head;
 }
+// Head and column tile of a scan's block: a head's blocks read the same rows, so
+// they go to one XCD (blocks are dealt to the eight of them in turn) and its L2
+// (8 x 4096 x 16 x 128 bf16: MEASURE_XCD).
+__device__ __forceinline__ void head_and_tile(int heads, int tiles, int& head, int& tile) {
+    const int group = (int)blockIdx.x / (8 * tiles), at = (int)blockIdx.x % (8 * tiles);
+    const int n = heads - 8 * group < 8 ? heads - 8 * group : 8;
+    head = 8 * group + at % n;
+    tile = at / n;
+}
 __device__ __forceinline__ int length_of(const DeltaArgs& a, int64_t b, int64_t T) {
     if (!a.lengths) return (int)T;
     const int n = a.lengths[b];
     return n < 0 ? 0 : n > T ? (int)T : n;
 }
+// exp(c_i - c_j) by the hardware's 2^x; below 2^-126 it is 0.
 __device__ __forceinline__ float decay(const float* row, int i, int j) {
-    return expf((row[kHi * C + i] - row[kHi * C + j]) + (row[kLo * C + i] - row[kLo * C + j]));
+    return __builtin_amdgcn_exp2f((row[kHi * C + i] - row[kHi * C + j]) + (row[kLo * C + i] - row[kLo * C + j]));
+}
+// exp(c_63), what a chunk leaves of the state before it
+__device__ __forceinline__ float whole_decay(const float* row) {
+    return __builtin_amdgcn_exp2f(row[kHi * C + C - 1] + row[kLo * C + C - 1]);
 }
 
 // ---- a chunk's rows among themselves -------------------------------------------
@@ -393,7 +489,7 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
     const int64_t t0 = n * C, ch = bh * p.chunks + n;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
     {
-        Carry<TS, DKP, PREP_NT> k, q;
+        Carry<TS, DKP, PREP_NT, false> k, q;
         k.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, (int)d.Dk);
         q.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, (int)d.Dk);
         if (wave == 0) {
@@ -403,23 +499,22 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
                 beta = a.beta[(b * d.T + t0 + lane) * d.Hv + h];
                 g = g < -128.0f ? -128.0f : g;         // exp(-128) is 0; a NaN stays
             }
-            double c = g;
+            double c = (double)g * 1.4426950408889634;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const double before = __shfl_up(c, o, 64);
                 if (lane >= o) c += before;
             }
-            const float hi = (float)c, lo = (float)(c - (double)hi);
+            const float hi = (float)c, lo = hi - hi == 0.0f ? (float)(c - (double)hi) : 0.0f;
             row[kHi * C + lane] = hi;
-            row[kLo * C + lane] = hi - hi == 0.0f ? lo : 0.0f;
+            row[kLo * C + lane] = lo;
             row[kBeta * C + lane] = beta;
             row[kNk * C + lane] = row[kNq * C + lane] = 1.0f;
-            row[kFrom * C + lane] = (float)exp(c);
-            row[kTo * C + lane] = (float)exp(__shfl(c, 63, 64) - c);
-            row[7 * C + lane] = 0.0f;
+            row[kFk * C + lane] = __builtin_amdgcn_exp2f(hi + lo);
+            row[kTk * C + lane] = __builtin_amdgcn_exp2f((float)(__shfl(c, 63, 64) - c));
         }
-        k.store(K);
-        q.store(Q);
+        k.store(K, rows, (int)d.Dk);
+        q.store(Q, rows, (int)d.Dk);
     }
     __syncthreads();
     if (d.flags & KAN_DELTA_UNIT) {
@@ -445,17 +540,30 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
         }
     }
     __syncthreads();
+    {
+        const int i0 = 16 * wave + 4 * gq;
+        const f32x4 hi = ld4(row + kHi * C + i0), lo = ld4(row + kLo * C + i0);
+        const f32x4 ni = ld4(row + kNk * C + i0), nq = d.scale * ld4(row + kNq * C + i0);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int j = 16 * x + m;
-        const float nj = row[kNk * C + j];
+        for (int x = 0; x < 4; ++x) {
+            if (x > (wave | 1)) break;                 // blocks that no piece reaches
+            const int j = 16 * x + m;
+            const float nj = row[kNk * C + j], hj = row[kHi * C + j], lj = row[kLo * C + j];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int i = 16 * wave + 4 * gq + y;
-            const float D = j <= i ? decay(row, i, j) * nj : 0.0f;
-            A[i * LC + j] = j < i ? kk[x][y] * (D * row[kNk * C + i]) : 0.0f;
-            P[i * LC + j] = j <= i ? qk[x][y] * (D * row[kNq * C + i] * d.scale) : 0.0f;
+            for (int y = 0; y < 4; ++y) {
+                const int i = i0 + y;
+                const float D = nj * __builtin_amdgcn_exp2f((hi[y] - hj) + (lo[y] - lj));
+                A[i * LC + j] = j < i ? kk[x][y] * (D * ni[y]) : 0.0f;
+                P[i * LC + j] = j <= i ? qk[x][y] * (D * nq[y]) : 0.0f;
+            }
         }
+    }
+    __syncthreads();
+    if (tid < C) {
+        const float from = row[kFk * C + tid];
+        row[kFk * C + tid] = from * row[kNk * C + tid];
+        row[kTk * C + tid] *= row[kNk * C + tid];
+        row[kFq * C + tid] = d.scale * from * row[kNq * C + tid];
     }
     __syncthreads();
     float* const out_row = reinterpret_cast<float*>(ws + p.off_rows) + ch * kFields * C;
@@ -471,191 +579,423 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
 
 // ---- along a sequence -------------------------------------------------------------
 
-// A wave has 16 columns of the state, in registers from the sequence's start to
-// its end, and everything of a chunk's rows in these columns: what it computes is
-// an operand of its next product as it stands.  The left operands (K, Q, G, P) are
+enum Pass { kForward, kStates, kBack };
+
+#ifndef SCAN_MIN
+#define SCAN_MIN 1
+#endif
+constexpr int kan_delta_halves(int dkp, int groups) { return dkp >= 64 && groups == 2 ? 2 : 1; }
+
+// How a scan's block is laid out.  A wave has 16 columns of the state and, where
+// Dk has room for it, half of its rows, so that a pair of waves shares the
+// columns: what each contracts over its rows of the state is added to the
+// other's through LDS.  Two waves to a SIMD hide each other's latency.
+template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
+struct Scan {
+    static constexpr int PL = planes_of<TS>::n, NP = out_planes<TS>::n;
+    static constexpr bool FWD = PASS == kForward, BACK = PASS == kBack;
+    static constexpr int HALVES = kan_delta_halves(DKP, GROUPS), NT = 64 * GROUPS * HALVES, W = 16 * GROUPS;
+    static constexpr int DT = DKP / 16 / HALVES, STEPS = DKP / 32 / HALVES;     // tiles and operands of a wave's state
+    // bfloat16 rows are operands as they stand: they go to LDS by themselves, into
+    // a second buffer.  Others pass through registers into one buffer.
+    static constexpr bool DIRECT = PL == 1 && EVEN;
+    // float32 has no room for P, which the waves then read from the workspace
+    static constexpr bool P_LDS = PASS != kStates && PL == 1;
+    static constexpr int MATS = (PASS == kStates ? 3 : P_LDS ? 3 + (FWD ? NP : 3) : 3) * kTri;   // G, P (or transposed)
+    static constexpr int ROWS = PL * C * DKP;
+    static constexpr int K = 0, Q = K + ROWS * 2, V = Q + (PASS == kStates ? 0 : ROWS * 2);    // offsets in bytes
+    static constexpr int FIELDS = V + (BACK ? PL * C * W * 2 : DIRECT ? C * W * 2 : 0);
+    static constexpr int BUF = FIELDS + kFields * C * 4;
+    static constexpr int SLOT = 4 * 64 * 16, SLOTS = HALVES == 2 ? 2 * GROUPS * SLOT : 0;      // a slot: four tiles of a wave
+    // the matrices too have a second buffer where there is room, and go there directly
+    static constexpr bool MATS_DIRECT = DIRECT && 2 * (BUF + MATS * 2) + SLOTS <= 160 * 1024;
+    static constexpr int G = (DIRECT ? 2 : 1) * BUF, G_BUF = MATS_DIRECT ? MATS * 2 : 0, P = 3 * kTri * 2;
+    static constexpr int SLOT0 = G + MATS * 2 + G_BUF, LDS = SLOT0 + SLOTS;
+};
+
+// The products of a scan.  Operands are loaded a group ahead of the instructions
+// that use them, and a group goes plane by plane over its tiles, so that an
+// instruction never waits for the one before it; the compiler, left alone, loads
+// an operand, waits, and chains its planes (7 us a chunk, where this takes 4).
+#define KAN_FENCE() __builtin_amdgcn_sched_barrier(0)
+
+// acc[t] += a[t] b for T tiles
+template <int T, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(f32x4* acc, const bf16x8 (*a)[NA], const bf16x8 (&b)[NB]) {
+    constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+    for (int place = N - 1; place >= 0; --place)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (place - i >= 0 && place - i < NB)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][i], b[place - i], acc[t], 0, 0, 0);
+}
+// acc[t] += b a[t]: the result transposed
+template <int T, int NA, int NB>
+__device__ __forceinline__ void mma_tiles_t(f32x4* acc, const bf16x8 (*a)[NA], const bf16x8 (&b)[NB]) {
+    constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+    for (int place = N - 1; place >= 0; --place)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (place - i >= 0 && place - i < NB)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[place - i], a[t][i], acc[t], 0, 0, 0);
+}
+
+// T tiles of rows from `first` on, in pieces 4 s .. of K or Q.
+template <int T, int PL, int DKP>
+__device__ __forceinline__ void load_rows(const uint16_t* lds, int s, int first, bf16x8 (*f)[PL]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int t = 0; t < T; ++t) row_frag<PL, DKP>(lds, row_of((first + t) & 3, lane & 15), 4 * s + (lane >> 4), f[t]);
+}
+// The tiles of rows that have 32 columns s of a triangular matrix: lower, all four
+// for s = 0 and the last two for s = 1; upper, the first two for s = 0, all for s = 1.
+template <int PL, bool UPPER, bool ALL>
+__device__ __forceinline__ void load_tri(const uint16_t* lds, bf16x8 (*f)[PL]) {
+#pragma unroll
+    for (int t = 0; t < (ALL ? 4 : 2); ++t)
+        tri_frag<PL>(lds, UPPER ? upper_piece(t, ALL ? 1 : 0) : lower_piece(ALL ? t : t + 2, ALL ? 0 : 1), f[t]);
+}
+// Columns of K or Q for the tiles 2 g, 2 g + 1 of the state, rows 32 s and on.
+template <int PL, int DKP>
+__device__ __forceinline__ void load_cols(const uint16_t* lds, int g, int s, bf16x8 (*f)[PL]) {
+    const int m = threadIdx.x & 15;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) col_frag<PL, DKP>(lds, s, 4 * g + (m & 3), x, f[x]);
+}
+__device__ __forceinline__ f32x4 at_rows(const float* row, int field, int t) {
+    return ld4(row + field * C + row_of(t, 4 * ((threadIdx.x & 63) >> 4)));
+}
+
+// So many vector instructions beside every matrix instruction of a region.
+template <int N, int VALU>
+__device__ __forceinline__ void beside() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    }
+}
+
+// ks[t] += rows of K times a wave's part of the state, of which NS planes are kept
+// in `sp`.  `last` loads what comes next.
+template <typename L, int DKP, int NS, typename Last>
+__device__ __forceinline__ void rows_by_state(const uint16_t* K, int step0, const f32x4* S, f32x4 (&ks)[4],
+                                              bf16x8 (*sp)[NS], Last last) {
+    constexpr int PL = L::PL, TG = PL == 1 ? 4 : 2, PARTS = 4 / TG;
+    bf16x8 f[2][TG][PL], sb[2][3];
+    load_rows<TG, PL, DKP>(K, step0, 0, f[0]);
+    split8<3>(S[0], S[1], sb[0]);
+#pragma unroll
+    for (int g = 0; g < L::STEPS * PARTS; ++g) {
+        const int s = g / PARTS, at = g % PARTS * TG;
+        if (g + 1 < L::STEPS * PARTS)
+            load_rows<TG, PL, DKP>(K, step0 + (g + 1) / PARTS, (g + 1) % PARTS * TG, f[(g + 1) & 1]);
+        else
+            last();
+        KAN_FENCE();
+        mma_tiles<TG, PL, 3>(ks + at, f[g & 1], sb[s & 1]);
+        if (g % PARTS == 0) {
+#pragma unroll
+            for (int z = 0; z < NS; ++z) sp[s][z] = sb[s & 1][z];
+            if (s + 1 < L::STEPS) {
+                split8<3>(S[2 * s + 2], S[2 * s + 3], sb[(s + 1) & 1]);
+                beside<12, 4>();
+            }
+        }
+        KAN_FENCE();
+    }
+}
+// o[t] += the transposed product of rows of Q, tiles from `first` on, with the
+// state's planes; beside it goes the work of `more`, in four parts.
+template <typename L, int DKP, typename More, typename Last>
+__device__ __forceinline__ void state_by_rows(const uint16_t* Q, int step0, int first, const bf16x8 (*sp)[L::NP],
+                                              f32x4 (&o)[4], bf16x8 (*f)[L::PL == 1 ? 4 : 2][L::PL], More more, Last last) {
+    constexpr int PL = L::PL, NP = L::NP, TG = PL == 1 ? 4 : 2, PARTS = 4 / TG, N = L::STEPS * PARTS;
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+        if (g + 1 < N) load_rows<TG, PL, DKP>(Q, step0 + (g + 1) / PARTS, first + (g + 1) % PARTS * TG, f[(g + 1) & 1]);
+        else last();
+        KAN_FENCE();
+        mma_tiles_t<TG, PL, NP>(o + g % PARTS * TG, f[g & 1], sp[g / PARTS]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i * N / 4 == g) more(i);
+        beside<8, 4>();
+        KAN_FENCE();
+    }
+}
+// A wave's tiles to its slot, and the partner's added.
+__device__ __forceinline__ void give_tiles(char* slot, const f32x4* v, int n) {
+#pragma unroll
+    for (int t = 0; t < n; ++t) st4(reinterpret_cast<float*>(slot) + (t * 64 + (threadIdx.x & 63)) * 4, v[t]);
+}
+__device__ __forceinline__ void add_tiles(const char* slot, f32x4* v, int n) {
+#pragma unroll
+    for (int t = 0; t < n; ++t) v[t] = v[t] + ld4(reinterpret_cast<const float*>(slot) + (t * 64 + (threadIdx.x & 63)) * 4);
+}
+
+// Along the sequences of a head: the state stays in registers from the start to
+// the end, and what a wave computes of a chunk's rows in its columns is an
+// operand of its next product as it stands.  The left operands (K, Q, G, P) are
 // the same for the block's waves and come through LDS; the next chunk's are on
-// their way from HBM meanwhile.  BWD: keeps the chunks' first states and w for the
-// backward pass and writes no rows.
-template <typename TS, int DKP, int WAVES, bool BWD>
-__global__ void __launch_bounds__(64 * WAVES) delta_scan_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+// their way from HBM meanwhile.  PASS kStates: keeps the chunks' first states and w
+// for the backward pass and writes no rows.
+template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
+__global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_MIN)
+    delta_scan_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    typedef Scan<TS, DKP, GROUPS, PASS, EVEN> L;
     extern __shared__ __align__(16) char lds[];
-    constexpr int PL = planes_of<TS>::n, NP = out_planes<TS>::n, NT = 64 * WAVES, DT = DKP / 16;
-    constexpr int MATS = (BWD ? 3 : 3 + NP) * kTri;
-    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
-    uint16_t* const Q = K + PL * C * DKP;                          // forward alone
-    uint16_t* const G = BWD ? Q : Q + PL * C * DKP;                // [3][kTri]
-    uint16_t* const P = G + 3 * kTri;                              // [NP][kTri], forward alone
-    float* const row = reinterpret_cast<float*>(G + MATS);         // [8][64]
-    const int tiles = (int)((d.Dv + 16 * WAVES - 1) / (16 * WAVES));
-    const int64_t bh = blockIdx.x / (unsigned)tiles, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
-    const int n0 = (int)(blockIdx.x % (unsigned)tiles) * 16 * WAVES + 16 * wave;   // this wave's first column
+    constexpr bool FWD = L::FWD, DIRECT = L::DIRECT;
+    constexpr int PL = L::PL, NP = L::NP, NT = L::NT, W = L::W, DT = L::DT, HALVES = L::HALVES, OWN = 4 / HALVES;
+    int head, tile;
+    head_and_tile((int)p.heads, (int)((d.Dv + W - 1) / W), head, tile);
+    const int64_t bh = head, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave % HALVES;
+    const int nb = tile * W, n0 = nb + 16 * (wave / HALVES);       // the block's and this wave's first column
     const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), chunks = (len + C - 1) / C;
     const bool mine = n0 + m < Dv;
+    const int x0 = half * DT;                                      // this wave's first tile of the state
     f32x4 S[DT];
 #pragma unroll
     for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = row_of(x, 4 * gq) + j;
+            const int dd = row_of(x0 + x, 4 * gq) + j;
             S[x][j] = a.h0 && dd < Dk && mine ? a.h0[(bh * Dk + dd) * Dv + n0 + m] : 0.0f;
         }
     const TS* const k_base = static_cast<const TS*>(a.k) + at_row(d.k, b, 0, hk);
     const TS* const q_base = static_cast<const TS*>(a.q) + at_row(d.q, b, 0, hk);
-    const TS* const v_base = static_cast<const TS*>(a.v) + at_row(d.v, b, 0, h) + n0 + m;
+    const TS* const v_base = static_cast<const TS*>(a.v) + at_row(d.v, b, 0, h);
+    TS* const y_base = static_cast<TS*>(a.y) + (b * d.T * d.Hv + h) * Dv;
     const float* const rows_base = reinterpret_cast<const float*>(ws + p.off_rows) + bh * p.chunks * kFields * C;
     const char* const mats_base = ws + p.off_mats + bh * p.chunks * p.mats;
-    Carry<TS, DKP, NT> ck, cq;
-    CarryBytes<MATS * 2, NT> cm;
+    Carry<TS, DKP, NT, EVEN> ck, cq;
+    CarryBytes<L::MATS * 2, NT> cm;
     CarryBytes<kFields * C * 4, NT> cr;
+    Direct<DKP, NT> xk, xq;
+    Direct<W, NT> xv;
+    if (DIRECT) {
+        xk.plan(d.k.row);
+        if (FWD) xq.plan(d.q.row);
+        xv.plan(d.v.row);
+    }
+    // rows of a chunk lie at most 2^32 bytes apart: a lane's part of an address
+    const uint32_t v_row = (uint32_t)d.v.row, y_row = (uint32_t)(d.Hv * Dv), column = mine ? n0 + m : 0;
+    const uint32_t y_off = (uint32_t)row_of(0, m) * y_row + n0 + 4 * gq;
+    const uint32_t s_off = 8 * gq * (uint32_t)p.dvp + n0 + m;
     TS vn[4][4];
-    auto fetch = [&](int n) {
+    auto fetch = [&](int n, char* to) {                // chunk n on its way to LDS, or to registers
         const int64_t t0 = (int64_t)n * C;
         const int rows = len - n * C;
-        ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
-        if (!BWD) cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
-        cm.load(mats_base + n * p.mats);
-        cr.load(rows_base + (int64_t)n * kFields * C);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = row_of(t, 4 * gq) + j;
-                vn[t][j] = i < rows && mine ? v_base[(t0 + i) * d.v.row] : (TS)0;
-            }
-    };
-    if (chunks > 0) fetch(0);
-    for (int n = 0; n < chunks; ++n) {
-        const int64_t ch = bh * p.chunks + n, t0 = (int64_t)n * C;
-        const int rows = len - n * C;
-        __syncthreads();                               // the chunk before is done with LDS
-        ck.store(K);
-        if (!BWD) cq.store(Q);
-        cm.store(G);
-        cr.store(row);
-        f32x4 w[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[t][j] = load_f(&vn[t][j], 0);
-        __syncthreads();
-        if (n + 1 < chunks) fetch(n + 1);
-        // K S and Q S (the latter transposed: lanes have columns of one row)
-        f32x4 ks[4], o[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ks[t] = o[t] = zero4();
-#pragma unroll
-        for (int s = 0; s < DKP / 32; ++s) {
-            bf16x8 sb[3];
-            split8<3>(S[2 * s], S[2 * s + 1], sb);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                bf16x8 ka[PL];
-                row_frag<PL, DKP>(K, row_of(t, m), 4 * s + gq, ka);
-                mma<PL, 3>(ks[t], ka, sb);
-            }
-            if (BWD) continue;
-            bf16x8 sp[NP];
-#pragma unroll
-            for (int z = 0; z < NP; ++z) sp[z] = sb[z];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                bf16x8 qa[PL];
-                row_frag<PL, DKP>(Q, row_of(t, m), 4 * s + gq, qa);
-                mma<NP, PL>(o[t], sp, qa);
-            }
-        }
-        if (BWD) {
-            float* out = reinterpret_cast<float*>(ws + p.off_S) + ch * DKP * p.dvp + n0 + m;
-#pragma unroll
-            for (int x = 0; x < DT; ++x)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) out[(row_of(x, 4 * gq) + j) * p.dvp] = S[x][j];
-        }
-        f32x4 be[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int i = row_of(t, 4 * gq);
-            w[t] = w[t] - ld4(row + kFrom * C + i) * ld4(row + kNk * C + i) * ks[t];       // e
-            be[t] = ld4(row + kBeta * C + i) * w[t];
-        }
-        {
-            bf16x8 eb[2][3];
-            split8<3>(be[0], be[1], eb[0]);
-            split8<3>(be[2], be[3], eb[1]);
-            f32x4 ge[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                ge[t] = zero4();
-#pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    bf16x8 ga[3];
-                    tri_frag<3>(G, lower_piece(t, s), ga);
-                    mma<3, 3>(ge[t], ga, eb[s]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) w[t] = w[t] - ge[t];
-        }
-        f32x4 u[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) u[t] = ld4(row + kBeta * C + row_of(t, 4 * gq)) * w[t];
-        if (BWD) {
-            float* out = reinterpret_cast<float*>(ws + p.off_w) + ch * C * p.dvp + n0 + m;
+        if constexpr (DIRECT) {
+            xk.load(k_base + t0 * d.k.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::K));
+            if (FWD) xq.load(q_base + t0 * d.q.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::Q));
+            xv.load(v_base + t0 * d.v.row + nb, rows, Dv - nb, reinterpret_cast<uint16_t*>(to + L::V));
+            bytes_to_lds<kFields * C * 4, NT>(rows_base + (int64_t)n * kFields * C, to + L::FIELDS);
+        } else {
+            ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
+            if (FWD) cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
+            cr.load(rows_base + (int64_t)n * kFields * C);
+            const TS* v = v_base + t0 * d.v.row;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) out[(row_of(t, 4 * gq) + j) * p.dvp] = w[t][j];
-        } else {
-            bf16x8 ub[2][NP];
-            split8<NP>(u[0], u[1], ub[0]);
-            split8<NP>(u[2], u[3], ub[1]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int i = row_of(t, m);
-                o[t] = o[t] * (d.scale * row[kFrom * C + i] * row[kNq * C + i]);
-#pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    bf16x8 pa[NP];
-                    tri_frag<NP>(P, lower_piece(t, s), pa);
-                    mma<NP, NP>(o[t], ub[s], pa);
+                for (int j = 0; j < 4; ++j) {
+                    const int i = row_of(t, j) + 8 * gq;
+                    vn[t][j] = v[(uint32_t)(i < rows ? i : rows - 1) * v_row + column];
                 }
-                if (i >= rows) continue;
-                TS* y = static_cast<TS*>(a.y) + ((b * d.T + t0 + i) * d.Hv + h) * Dv + n0 + 4 * gq;
-                if (n0 + 4 * gq + 4 <= Dv) {
-                    const float v[4] = {o[t][0], o[t][1], o[t][2], o[t][3]};
-                    store_vec<4>(y, v);
-                } else {
+        }
+        if constexpr (L::MATS_DIRECT) bytes_to_lds<L::MATS * 2, NT>(mats_base + n * p.mats, lds + L::G + (n & 1) * L::G_BUF);
+        else cm.load(mats_base + n * p.mats);
+    };
+    char* const my_slot = lds + L::SLOT0 + wave * L::SLOT;
+    char* const other_slot = lds + L::SLOT0 + (wave ^ 1) * L::SLOT;
+    // The rows of a chunk are stored in the next one's time: what waits for the
+    // chunk's arrival waits for stores under way as well.  A pair of waves has two
+    // tiles of rows each, o[0] and o[1] of tiles 2 half, 2 half + 1.
+    f32x4 o[4];
+    auto put_rows = [&](int n) {
+        TS* const out = y_base + (int64_t)n * C * y_row;
+        const int rows = len - n * C;
+        if (HALVES == 2) add_tiles(my_slot, o, OWN);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (n0 + 4 * gq + j < Dv) put(y + j, o[t][j]);
-                }
+        for (int l = 0; l < OWN; ++l) {
+            const int t = HALVES == 2 ? 2 * half + l : l;
+            if (row_of(t, m) >= rows) continue;
+            TS* y = out + (uint32_t)row_of(t, 0) * y_row + y_off;
+            if (n0 + 16 <= Dv) {                       // uniform
+                const float v[4] = {o[l][0], o[l][1], o[l][2], o[l][3]};
+                store_vec<4>(y, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + 4 * gq + j < Dv) put(y + j, o[l][j]);
             }
         }
-        // S = exp(c_63) S + K^T (exp(c_63 - c) u)
-        bf16x8 ub[2][3];
+    };
+    if (chunks > 0) fetch(0, lds);
+    for (int n = 0; n < chunks; ++n) {
+        const int64_t ch = bh * p.chunks + n;
+        const int rows = len - n * C;
+        char* const buf = lds + (DIRECT ? (n & 1) * L::BUF : 0);
+        if (DIRECT) arrived();
+        __syncthreads();                               // direct: the chunk is there; else: LDS is free
+        f32x4 w[4];
+        if (!DIRECT) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[t][j] = row_of(t, j) + 8 * gq < rows ? load_f(&vn[t][j], 0) : 0.0f;
+            ck.store(reinterpret_cast<uint16_t*>(lds + L::K), rows, Dk);
+            if (FWD) cq.store(reinterpret_cast<uint16_t*>(lds + L::Q), rows, Dk);
+            cr.store(lds + L::FIELDS);
+        }
+        if constexpr (!L::MATS_DIRECT) cm.store(lds + L::G);
+        if (!DIRECT) __syncthreads();
+        // nothing may be on its way to LDS when the block ends
+        if (!DIRECT || n + 1 < chunks) fetch(n + 1 < chunks ? n + 1 : n, lds + (DIRECT ? ((n + 1) & 1) * L::BUF : 0));
+        if (FWD && n > 0) put_rows(n - 1);
+        const uint16_t* const K = reinterpret_cast<const uint16_t*>(buf + L::K);       // [PL][64][DKP]
+        const uint16_t* const Q = reinterpret_cast<const uint16_t*>(buf + L::Q);       // forward alone
+        const uint16_t* const V = reinterpret_cast<const uint16_t*>(buf + L::V);       // [64][W], direct alone
+        const float* const row = reinterpret_cast<const float*>(buf + L::FIELDS);      // [8][64]
+        const uint16_t* const G = reinterpret_cast<const uint16_t*>(lds + L::G + (n & 1) * L::G_BUF);  // [3][kTri]
+        const uint16_t* const P = G + 3 * kTri;                                        // [NP][kTri], forward alone
+        if (!FWD) {
+            float* out = reinterpret_cast<float*>(ws + p.off_S) + ch * DKP * p.dvp;
+#pragma unroll
+            for (int x = 0; x < DT; ++x)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) (out + row_of(x0 + x, j) * p.dvp)[s_off] = S[x][j];
+        }
+        // K S
+        constexpr int TG = PL == 1 ? 4 : 2, NS = FWD ? NP : 1;
+        f32x4 ks[4];
+        bf16x8 sp[L::STEPS][NS], f[2][TG][PL], ga[4][3], gb[2][3];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks[t] = o[t] = zero4();
+        rows_by_state<L, DKP, NS>(K, half * L::STEPS, S, ks, sp, [&] {
+            if constexpr (DIRECT) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_s16x4*)(V + piece_at<W>(row_of(t, 4 * gq) + (m >> 2), 2 * (wave / HALVES) + ((m & 3) >> 1)) +
+                                     4 * (m & 1)));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[t][j] = __uint_as_float((uint32_t)(uint16_t)v[j] << 16);
+                }
+            }
+            if (FWD) load_rows<TG, PL, DKP>(Q, half * L::STEPS, 2 * half, f[0]);
+        });
+        if (HALVES == 2) give_tiles(my_slot, ks, 4);
+        if (HALVES == 2 || !L::MATS_DIRECT) __syncthreads();           // G and P are there, and the partner's part
+        if (HALVES == 2) add_tiles(other_slot, ks, 4);
+        // Q S (transposed: lanes have columns of one row), and e, an operand by planes
+        f32x4 be[4];
+        bf16x8 eb[2][3];
+        auto errors = [&](int part) {
+            if (part < 2) {
+#pragma unroll
+                for (int t = 2 * part; t < 2 * part + 2; ++t) {
+                    w[t] = w[t] - at_rows(row, kFk, t) * ks[t];        // e
+                    be[t] = at_rows(row, kBeta, t) * w[t];
+                }
+            } else {
+                split8<3>(be[2 * part - 4], be[2 * part - 3], eb[part - 2]);
+            }
+        };
+        if constexpr (FWD) {
+            state_by_rows<L, DKP>(Q, half * L::STEPS, 2 * half, sp, o, f, errors, [&] { load_tri<3, false, true>(G, ga); });
+        } else {
+            load_tri<3, false, true>(G, ga);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) errors(i);
+        }
+        load_tri<3, false, false>(G, gb);
+        // P for this wave's tiles: all of them, or the first two or the last two
+        bf16x8 pa[4][NP], pb[2][NP];
+        const uint16_t* const p_at = L::P_LDS ? P : reinterpret_cast<const uint16_t*>(mats_base + n * p.mats) + 3 * kTri;
+        if (FWD && HALVES == 1) {
+            load_tri<NP, false, true>(p_at, pa);
+            load_tri<NP, false, false>(p_at, pb);
+        } else if (FWD) {
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                tri_frag<NP>(p_at, half ? lower_piece(2 + l, 0) : l, pa[l]);
+                if (half) tri_frag<NP>(p_at, lower_piece(2 + l, 1), pb[l]);
+            }
+        }
+        KAN_FENCE();
+        f32x4 ge[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ge[t] = zero4();
+        mma_tiles<4, 3, 3>(ge, ga, eb[0]);
+        mma_tiles<2, 3, 3>(ge + 2, gb, eb[1]);
+        const float whole = whole_decay(row);
+#pragma unroll
+        for (int x = 0; x < DT; ++x) S[x] = whole * S[x];
+        if (FWD) {
+#pragma unroll
+            for (int l = 0; l < 4; ++l) o[l] = o[l] * row[kFq * C + row_of((l + 2 * half) & 3, m)];
+        }
+        KAN_FENCE();
+        if (FWD && HALVES == 2) give_tiles(other_slot, o + 2, 2);      // read before; the partner adds it after the next barrier
+        bf16x8 kc[2][2][PL];
+        load_cols<PL, DKP>(K, half * L::STEPS, 0, kc[0]);
+        f32x4 u[4];
+        bf16x8 ub[2][3], uo[2][NP];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int i = row_of(t, 4 * gq);
-            u[t] = u[t] * (ld4(row + kTo * C + i) * ld4(row + kNk * C + i));
+            w[t] = w[t] - ge[t];
+            u[t] = at_rows(row, kBeta, t) * w[t];
         }
-        split8<3>(u[0], u[1], ub[0]);
-        split8<3>(u[2], u[3], ub[1]);
-        const float whole = row[kFrom * C + C - 1];
+        if (FWD) {
+            split8<NP>(u[0], u[1], uo[0]);
+            split8<NP>(u[2], u[3], uo[1]);
+            KAN_FENCE();
+            if (HALVES == 2) {
+                mma_tiles_t<2, NP, NP>(o, pa, uo[0]);
+                if (half) mma_tiles_t<2, NP, NP>(o, pb, uo[1]);
+            } else {
+                mma_tiles_t<4, NP, NP>(o, pa, uo[0]);
+                mma_tiles_t<2, NP, NP>(o + 2, pb, uo[1]);
+            }
+        } else {
+            float* out = reinterpret_cast<float*>(ws + p.off_w) + ch * C * p.dvp;
 #pragma unroll
-        for (int x = 0; x < DT; ++x) {
-            S[x] = whole * S[x];
+            for (int t = 0; t < 4; ++t) {
+                if (HALVES == 2 && t / 2 != half) continue;            // uniform
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                bf16x8 kt[PL];
-                col_frag<PL, DKP>(K, s, 4 * (x >> 1) + (m & 3), x & 1, kt);
-                mma<PL, 3>(S[x], kt, ub[s]);
+                for (int j = 0; j < 4; ++j) (out + row_of(t, j) * p.dvp)[s_off] = w[t][j];
             }
         }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t] = u[t] * at_rows(row, kTk, t);
+        split8<3>(u[0], u[1], ub[0]);
+        split8<3>(u[2], u[3], ub[1]);
+        if (FWD && HALVES == 1) beside<18, 6>();
+        // S = exp(c_63) S + K^T (exp(c_63 - c) u)
+#pragma unroll
+        for (int g = 0; g < 2 * L::STEPS; ++g) {
+            if (g + 1 < 2 * L::STEPS) load_cols<PL, DKP>(K, half * L::STEPS + (g + 1) / 2, (g + 1) & 1, kc[(g + 1) & 1]);
+            KAN_FENCE();
+            mma_tiles<2, PL, 3>(S + (g & ~1), kc[g & 1], ub[g & 1]);
+            KAN_FENCE();
+        }
     }
-    if (BWD) return;
-    for (int64_t e = lane; e < (d.T - len) * 16; e += 64) {
+    if (FWD && chunks > 0) {
+        __syncthreads();
+        put_rows(chunks - 1);
+    }
+    if (!FWD) return;
+    for (int64_t e = lane + 64 * half; e < (d.T - len) * 16; e += 64 * HALVES) {
         const int64_t t = len + e / 16;
         const int nn = n0 + (int)(e % 16);
         if (nn < Dv) put(static_cast<TS*>(a.y) + ((b * d.T + t) * d.Hv + h) * Dv + nn, 0.0f);
@@ -665,29 +1005,29 @@ __global__ void __launch_bounds__(64 * WAVES) delta_scan_kernel(kan_delta_desc_t
     for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = row_of(x, 4 * gq) + j;
+            const int dd = row_of(x0 + x, 4 * gq) + j;
             if (dd < Dk) a.hT[(bh * Dk + dd) * Dv + n0 + m] = S[x][j];
         }
 }
 
 // Backwards along a sequence: r, dv and the gradients of the chunks' last states.
-template <typename TS, int DKP, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) delta_back_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+template <typename TS, int DKP, int GROUPS, bool EVEN>
+__global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN_MIN)
+    delta_back_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    typedef Scan<TS, DKP, GROUPS, kBack, EVEN> L;
     extern __shared__ __align__(16) char lds[];
-    constexpr int PL = planes_of<TS>::n, NT = 64 * WAVES, DT = DKP / 16, W = 16 * WAVES;
-    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
-    uint16_t* const Q = K + PL * C * DKP;
-    uint16_t* const Y = Q + PL * C * DKP;                          // [PL][64][W]: dY
-    uint16_t* const G = Y + PL * C * W;                            // [3][kTri]: G^T
-    uint16_t* const P = G + 3 * kTri;                              // [3][kTri]: P^T
-    float* const row = reinterpret_cast<float*>(P + 3 * kTri);     // [8][64]
-    const int tiles = (int)((d.Dv + W - 1) / W);
-    const int64_t bh = blockIdx.x / (unsigned)tiles, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
-    const int nb = (int)(blockIdx.x % (unsigned)tiles) * W, n0 = nb + 16 * wave;
+    constexpr bool DIRECT = L::DIRECT;
+    constexpr int PL = L::PL, NT = L::NT, W = L::W, DT = L::DT, HALVES = L::HALVES;
+    int head, tile;
+    head_and_tile((int)p.heads, (int)((d.Dv + W - 1) / W), head, tile);
+    const int64_t bh = head, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave % HALVES, group = wave / HALVES;
+    const int nb = tile * W, n0 = nb + 16 * group;
     const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), chunks = (len + C - 1) / C;
     const bool mine = n0 + m < Dv;
-    for (int64_t e = lane; e < (d.T - len) * 16; e += 64) {
+    const int x0 = half * DT;
+    for (int64_t e = lane + 64 * half; e < (d.T - len) * 16; e += 64 * HALVES) {
         const int64_t t = len + e / 16;
         const int nn = n0 + (int)(e % 16);
         if (nn < Dv) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t, h) + nn, 0.0f);
@@ -697,62 +1037,97 @@ __global__ void __launch_bounds__(64 * WAVES) delta_back_kernel(kan_delta_desc_t
     for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = row_of(x, 4 * gq) + j;
+            const int dd = row_of(x0 + x, 4 * gq) + j;
             S[x][j] = a.dhT && dd < Dk && mine ? a.dhT[(bh * Dk + dd) * Dv + n0 + m] : 0.0f;
         }
     const TS* const k_base = static_cast<const TS*>(a.k) + at_row(d.k, b, 0, hk);
     const TS* const q_base = static_cast<const TS*>(a.q) + at_row(d.q, b, 0, hk);
     const TS* const y_base = static_cast<const TS*>(a.dy) + (b * d.T * d.Hv + h) * Dv + nb;
     const float* const rows_base = reinterpret_cast<const float*>(ws + p.off_rows) + bh * p.chunks * kFields * C;
-    const char* const mats_base = ws + p.off_mats + bh * p.chunks * p.mats + 3 * kTri * 2;
-    Carry<TS, DKP, NT> ck, cq;
-    Carry<TS, W, NT> cy;
-    CarryBytes<6 * kTri * 2, NT> cm;
+    const char* const mats_base = ws + p.off_mats + bh * p.chunks * p.mats + 3 * kTri * 2;     // G^T, P^T
+    Carry<TS, DKP, NT, EVEN> ck, cq;
+    Carry<TS, W, NT, EVEN> cy;
+    CarryBytes<L::MATS * 2, NT> cm;
     CarryBytes<kFields * C * 4, NT> cr;
-    auto fetch = [&](int n) {
+    Direct<DKP, NT> xk, xq;
+    Direct<W, NT> xy;
+    if (DIRECT) {
+        xk.plan(d.k.row);
+        xq.plan(d.q.row);
+        xy.plan(d.Hv * Dv);
+    }
+    const uint32_t s_off = 8 * gq * (uint32_t)p.dvp + n0 + m, v_row = (uint32_t)d.dv.row;
+    const uint32_t v_off = 8 * gq * v_row + (mine ? n0 + m : 0);
+    auto fetch = [&](int n, char* to) {
         const int64_t t0 = (int64_t)n * C;
         const int rows = len - n * C;
-        ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
-        cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
-        cy.load(y_base + t0 * d.Hv * Dv, d.Hv * Dv, rows, Dv - nb);
-        cm.load(mats_base + n * p.mats);
-        cr.load(rows_base + (int64_t)n * kFields * C);
+        if constexpr (DIRECT) {
+            xk.load(k_base + t0 * d.k.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::K));
+            xq.load(q_base + t0 * d.q.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::Q));
+            xy.load(y_base + t0 * d.Hv * Dv, rows, Dv - nb, reinterpret_cast<uint16_t*>(to + L::V));
+            bytes_to_lds<kFields * C * 4, NT>(rows_base + (int64_t)n * kFields * C, to + L::FIELDS);
+        } else {
+            ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
+            cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
+            cy.load(y_base + t0 * d.Hv * Dv, d.Hv * Dv, rows, Dv - nb);
+            cr.load(rows_base + (int64_t)n * kFields * C);
+        }
+        if constexpr (L::MATS_DIRECT) bytes_to_lds<L::MATS * 2, NT>(mats_base + n * p.mats, lds + L::G + (n & 1) * L::G_BUF);
+        else cm.load(mats_base + n * p.mats);
     };
-    if (chunks > 0) fetch(chunks - 1);
+    char* const my_slot = lds + L::SLOT0 + wave * L::SLOT;
+    const char* const other_slot = lds + L::SLOT0 + (wave ^ 1) * L::SLOT;
+    if (chunks > 0) fetch(chunks - 1, lds + (DIRECT ? ((chunks - 1) & 1) * L::BUF : 0));
     for (int n = chunks - 1; n >= 0; --n) {
         const int64_t ch = bh * p.chunks + n, t0 = (int64_t)n * C;
         const int rows = len - n * C;
+        char* const buf = lds + (DIRECT ? (n & 1) * L::BUF : 0);
+        if (DIRECT) arrived();
         __syncthreads();
-        ck.store(K);
-        cq.store(Q);
-        cy.store(Y);
-        cm.store(G);
-        cr.store(row);
-        __syncthreads();
-        if (n > 0) fetch(n - 1);
-        float* const out_S = reinterpret_cast<float*>(ws + p.off_dS) + ch * DKP * p.dvp + n0 + m;
+        if (!DIRECT) {
+            ck.store(reinterpret_cast<uint16_t*>(lds + L::K), rows, Dk);
+            cq.store(reinterpret_cast<uint16_t*>(lds + L::Q), rows, Dk);
+            cy.store(reinterpret_cast<uint16_t*>(lds + L::V), rows, Dv - nb);
+            cr.store(lds + L::FIELDS);
+        }
+        if constexpr (!L::MATS_DIRECT) cm.store(lds + L::G);
+        if (!DIRECT) __syncthreads();
+        if (n > 0 || !DIRECT) fetch(n > 0 ? n - 1 : 0, lds + (DIRECT ? ((n + 1) & 1) * L::BUF : 0));
+        const uint16_t* const K = reinterpret_cast<const uint16_t*>(buf + L::K);       // [PL][64][DKP]
+        const uint16_t* const Q = reinterpret_cast<const uint16_t*>(buf + L::Q);
+        const uint16_t* const Y = reinterpret_cast<const uint16_t*>(buf + L::V);       // [PL][64][W]: dY
+        const float* const row = reinterpret_cast<const float*>(buf + L::FIELDS);
+        const uint16_t* const G = reinterpret_cast<const uint16_t*>(lds + L::G + (n & 1) * L::G_BUF);  // [3][kTri]: G^T
+        const uint16_t* const P = L::P_LDS ? G + 3 * kTri : reinterpret_cast<const uint16_t*>(mats_base + n * p.mats) + 3 * kTri;
+        float* const out_S = reinterpret_cast<float*>(ws + p.off_dS) + ch * DKP * p.dvp;
 #pragma unroll
         for (int x = 0; x < DT; ++x)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) out_S[(row_of(x, 4 * gq) + j) * p.dvp] = S[x][j];
+            for (int j = 0; j < 4; ++j) (out_S + row_of(x0 + x, j) * p.dvp)[s_off] = S[x][j];
         f32x4 kd[4], py[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) kd[t] = py[t] = zero4();
-#pragma unroll
-        for (int s = 0; s < DKP / 32; ++s) {
-            bf16x8 sb[3];
-            split8<3>(S[2 * s], S[2 * s + 1], sb);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                bf16x8 ka[PL];
-                row_frag<PL, DKP>(K, row_of(t, m), 4 * s + gq, ka);
-                mma<PL, 3>(kd[t], ka, sb);
-            }
-        }
         bf16x8 yb[2][PL];                              // dY in this wave's columns
-        col_frag<PL, W>(Y, 0, 2 * wave + ((m & 3) >> 1), m & 1, yb[0]);
-        col_frag<PL, W>(Y, 1, 2 * wave + ((m & 3) >> 1), m & 1, yb[1]);
-        f32x4 y[4];                                    // the same as floats
+        bf16x8 unused[L::STEPS][1];
+        rows_by_state<L, DKP, 1>(K, half * L::STEPS, S, kd, unused, [&] {
+            col_frag<PL, W>(Y, 0, 2 * group + ((m & 3) >> 1), m & 1, yb[0]);
+            col_frag<PL, W>(Y, 1, 2 * group + ((m & 3) >> 1), m & 1, yb[1]);
+        });
+        if (HALVES == 2) give_tiles(my_slot, kd, 4);
+        if (HALVES == 2 || !L::MATS_DIRECT) __syncthreads();           // G^T and P^T are there, and the partner's part
+        {
+            bf16x8 pa[4][3], pb[2][3];
+            load_tri<3, true, true>(P, pa);
+            load_tri<3, true, false>(P, pb);
+            if (HALVES == 2) add_tiles(other_slot, kd, 4);
+            mma_tiles<4, 3, PL>(py, pa, yb[1]);
+            mma_tiles<2, 3, PL>(py, pb, yb[0]);
+        }
+        bf16x8 ga[4][3], gb[2][3];
+        load_tri<3, true, true>(G, ga);
+        load_tri<3, true, false>(G, gb);
+        KAN_FENCE();
+        f32x4 y[4];                                    // dY as floats
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -765,66 +1140,59 @@ __global__ void __launch_bounds__(64 * WAVES) delta_back_kernel(kan_delta_desc_t
                     y[2 * s + (j >> 2)][j & 3] = z ? y[2 * s + (j >> 2)][j & 3] + v : v;
                 }
             }
-        f32x4 du[4], r[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-#pragma unroll
-            for (int s = t / 2; s < 2; ++s) {
-                bf16x8 pa[3];
-                tri_frag<3>(P, upper_piece(t, s), pa);
-                mma<3, PL>(py[t], pa, yb[s]);
-            }
-            const int i = row_of(t, 4 * gq);
-            du[t] = py[t] + ld4(row + kTo * C + i) * ld4(row + kNk * C + i) * kd[t];
-            r[t] = ld4(row + kBeta * C + i) * du[t];
-        }
+        f32x4 r[4];
         {
+            f32x4 gu[4], bu[4];
             bf16x8 ub[2][3];
-            split8<3>(r[0], r[1], ub[0]);
-            split8<3>(r[2], r[3], ub[1]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                f32x4 gu = zero4();
-#pragma unroll
-                for (int s = t / 2; s < 2; ++s) {
-                    bf16x8 ga[3];
-                    tri_frag<3>(G, upper_piece(t, s), ga);
-                    mma<3, 3>(gu, ga, ub[s]);
-                }
-                r[t] = du[t] - gu;
+                r[t] = py[t] + at_rows(row, kTk, t) * kd[t];           // du
+                bu[t] = at_rows(row, kBeta, t) * r[t];
+                gu[t] = zero4();
             }
+            split8<3>(bu[2], bu[3], ub[1]);
+            split8<3>(bu[0], bu[1], ub[0]);
+            mma_tiles<4, 3, 3>(gu, ga, ub[1]);
+            mma_tiles<2, 3, 3>(gu, gb, ub[0]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) r[t] = r[t] - gu[t];
         }
-        float* const out_r = reinterpret_cast<float*>(ws + p.off_r) + ch * C * p.dvp + n0 + m;
+        bf16x8 kc[2][2][PL];
+        load_cols<PL, DKP>(K, half * L::STEPS, 0, kc[0]);
+        KAN_FENCE();
+        float* const out_r = reinterpret_cast<float*>(ws + p.off_r) + ch * C * p.dvp;
+        TS* const out_v = static_cast<TS*>(a.dv) + at_row(d.dv, b, t0, h);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int i = row_of(t, 4 * gq);
-            const f32x4 dv = ld4(row + kBeta * C + i) * r[t], from = ld4(row + kFrom * C + i);
+            const f32x4 dv = at_rows(row, kBeta, t) * r[t];
+            if (HALVES == 1 || t / 2 == half) {                        // uniform
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                out_r[(i + j) * p.dvp] = r[t][j];
-                if (i + j < rows && mine) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t0 + i + j, h) + n0 + m, dv[j]);
+                for (int j = 0; j < 4; ++j) {
+                    (out_r + row_of(t, j) * p.dvp)[s_off] = r[t][j];
+                    if (rows >= C ? mine : mine && row_of(t, j) + 8 * gq < rows)
+                        put(out_v + (uint32_t)row_of(t, j) * v_row + v_off, dv[j]);
+                }
             }
             // rows of exp(c) (scale Q^T dY - K^T dv)
-            y[t] = y[t] * (d.scale * from * ld4(row + kNq * C + i));
-            r[t] = -dv * from * ld4(row + kNk * C + i);
+            y[t] = y[t] * at_rows(row, kFq, t);
+            r[t] = -dv * at_rows(row, kFk, t);
         }
         bf16x8 ys[2][3], vs[2][3];
-        split8<3>(y[0], y[1], ys[0]);
-        split8<3>(y[2], y[3], ys[1]);
         split8<3>(r[0], r[1], vs[0]);
         split8<3>(r[2], r[3], vs[1]);
-        const float whole = row[kFrom * C + C - 1];
+        split8<3>(y[0], y[1], ys[0]);
+        split8<3>(y[2], y[3], ys[1]);
+        const float whole = whole_decay(row);
 #pragma unroll
-        for (int x = 0; x < DT; ++x) {
-            S[x] = whole * S[x];
+        for (int x = 0; x < DT; ++x) S[x] = whole * S[x];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                bf16x8 kt[PL], qt[PL];
-                col_frag<PL, DKP>(K, s, 4 * (x >> 1) + (m & 3), x & 1, kt);
-                col_frag<PL, DKP>(Q, s, 4 * (x >> 1) + (m & 3), x & 1, qt);
-                mma<PL, 3>(S[x], kt, vs[s]);
-                mma<PL, 3>(S[x], qt, ys[s]);
-            }
+        for (int g = 0; g < 4 * L::STEPS; ++g) {       // two tiles of the state by K, then by Q
+            const int next = g + 1;
+            if (next < 4 * L::STEPS)
+                load_cols<PL, DKP>(next & 2 ? Q : K, half * L::STEPS + next / 4, next & 1, kc[next & 1]);
+            KAN_FENCE();
+            mma_tiles<2, PL, 3>(S + 2 * (g / 4), kc[g & 1], g & 2 ? ys[g & 1] : vs[g & 1]);
+            KAN_FENCE();
         }
     }
     if (!a.dh0 || !mine) return;
@@ -832,7 +1200,7 @@ __global__ void __launch_bounds__(64 * WAVES) delta_back_kernel(kan_delta_desc_t
     for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int dd = row_of(x, 4 * gq) + j;
+            const int dd = row_of(x0 + x, 4 * gq) + j;
             if (dd < Dk) a.dh0[(bh * Dk + dd) * Dv + n0 + m] = S[x][j];
         }
 }
@@ -915,13 +1283,13 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
         return;
     }
     {
-        Carry<TS, DKP, NT> ck, cq;
+        Carry<TS, DKP, NT, false> ck, cq;
         CarryBytes<kFields * C * 4, NT> cr;
         ck.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
         cq.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, Dk);
         cr.load(reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C);
-        ck.store(K);
-        cq.store(Q);
+        ck.store(K, rows, Dk);
+        cq.store(Q, rows, Dk);
         cr.store(row);
     }
     const float* const in_S = reinterpret_cast<const float*>(ws + p.off_S) + ch * DKP * p.dvp;
@@ -1014,7 +1382,8 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
     if (lane == 0) part[wave] = ss;
     __syncthreads();                                   // the states' slices are done with
     // the states' parts, with their factors; gradients of q and k as they were divided
-    const float from = row[kFrom * C + im], to = row[kTo * C + im], nk = row[kNk * C + im], nq = row[kNq * C + im];
+    const float from = __builtin_amdgcn_exp2f(row[kHi * C + im] + row[kLo * C + im]), to = decay(row, C - 1, im);
+    const float nk = row[kNk * C + im], nq = row[kNq * C + im];
     float xr = 0.0f, zr = 0.0f;
 #pragma unroll
     for (int x = 0; x < DT; ++x) {
@@ -1117,7 +1486,7 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
         float dg = 0.0f;
         for (int i = C - 1; i >= lane; --i) dg += E[i * LC + lane] + xs[i];
         for (int j = 0; j < lane; ++j) dg += zs[j];
-        dg += row[kFrom * C + C - 1] * (part[0] + part[1] + part[2] + part[3]);
+        dg += whole_decay(row) * (part[0] + part[1] + part[2] + part[3]);
         if (lane < inside) a.dg[(b * d.T + t0 + lane) * d.Hv + h] = lane < rows ? dg : 0.0f;
     }
     if (im >= inside) return;
@@ -1313,18 +1682,29 @@ hipError_t prep(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& 
     return launch(delta_prep_kernel<TS, DKP, BWD>, p.heads * p.chunks, PREP_NT,
                   (rows > pairs ? rows : pairs) + 4 * kFields * C, s, d, p, a, ws);
 }
-template <typename TS, int DKP, int WAVES, bool BWD>
-hipError_t scan_w(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    constexpr size_t lds = (size_t)(BWD ? 1 : 2) * planes_of<TS>::n * C * DKP * 2 +
-                           (BWD ? 3 : 3 + out_planes<TS>::n) * kTri * 2 + 4 * kFields * C;
-    return launch(delta_scan_kernel<TS, DKP, WAVES, BWD>, p.heads * ((d.Dv + 16 * WAVES - 1) / (16 * WAVES)), 64 * WAVES,
-                  lds, s, d, p, a, ws);
+template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
+hipError_t scan_e(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    typedef Scan<TS, DKP, GROUPS, PASS, EVEN> L;
+    static_assert(L::LDS <= 160 * 1024, "LDS of a compute unit");
+    const int64_t blocks = p.heads * ((d.Dv + L::W - 1) / L::W);
+    if constexpr (PASS == kBack)
+        return launch(delta_back_kernel<TS, DKP, GROUPS, EVEN>, blocks, L::NT, L::LDS, s, d, p, a, ws);
+    else
+        return launch(delta_scan_kernel<TS, DKP, GROUPS, PASS, EVEN>, blocks, L::NT, L::LDS, s, d, p, a, ws);
 }
-template <typename TS, int DKP, int WAVES>
-hipError_t back_w(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    constexpr size_t lds = planes_of<TS>::n * C * (2 * DKP + 16 * WAVES) * 2 + 6 * kTri * 2 + 4 * kFields * C;
-    return launch(delta_back_kernel<TS, DKP, WAVES>, p.heads * ((d.Dv + 16 * WAVES - 1) / (16 * WAVES)), 64 * WAVES, lds,
-                  s, d, p, a, ws);
+template <typename TS, int DKP, int PASS>
+hipError_t scan(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    // pieces of eight, on 16 bytes where they go to LDS directly
+    auto direct = [](const void* at, const kan_heads_t& s) {
+        return aligned(at, 16) && s.seq % 8 == 0 && s.row % 8 == 0 && s.head % 8 == 0;
+    };
+    bool even = d.Dk % 8 == 0 && d.Dv % 8 == 0;
+    if (sizeof(TS) == 2)
+        even = even && direct(a.k, d.k) && (PASS == kStates || direct(a.q, d.q)) && (PASS == kBack || direct(a.v, d.v));
+    constexpr int WIDE = sizeof(TS) == 4 && PASS == kBack ? 2 : 4;     // groups of 16 columns that LDS has room for
+    if (p.waves == 4 && WIDE == 4)
+        return even ? scan_e<TS, DKP, WIDE, PASS, true>(d, p, a, ws, s) : scan_e<TS, DKP, WIDE, PASS, false>(d, p, a, ws, s);
+    return even ? scan_e<TS, DKP, 2, PASS, true>(d, p, a, ws, s) : scan_e<TS, DKP, 2, PASS, false>(d, p, a, ws, s);
 }
 template <typename TS, int DKP>
 hipError_t grad(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
@@ -1339,17 +1719,16 @@ hipError_t forward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArg
         const hipError_t e = prep<TS, DKP, false>(d, p, a, ws, s);
         if (e != hipSuccess) return e;
     }
-    return p.waves == 4 ? scan_w<TS, DKP, 4, false>(d, p, a, ws, s) : scan_w<TS, DKP, 2, false>(d, p, a, ws, s);
+    return scan<TS, DKP, kForward>(d, p, a, ws, s);
 }
 template <typename TS, int DKP>
 hipError_t backward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
     hipError_t e;
     if (p.chunks > 0) {
         if ((e = prep<TS, DKP, true>(d, p, a, ws, s)) != hipSuccess) return e;
-        e = p.waves == 4 ? scan_w<TS, DKP, 4, true>(d, p, a, ws, s) : scan_w<TS, DKP, 2, true>(d, p, a, ws, s);
-        if (e != hipSuccess) return e;
+        if ((e = scan<TS, DKP, kStates>(d, p, a, ws, s)) != hipSuccess) return e;
     }
-    e = p.waves == 4 ? back_w<TS, DKP, 4>(d, p, a, ws, s) : back_w<TS, DKP, 2>(d, p, a, ws, s);
+    e = scan<TS, DKP, kBack>(d, p, a, ws, s);
     if (e != hipSuccess || p.chunks == 0) return e;
     if ((e = grad<TS, DKP>(d, p, a, ws, s)) != hipSuccess || d.Hv == d.Hk) return e;
     const int64_t blocks = (d.B * d.T * d.Hk + NT / 64 - 1) / (NT / 64), x = std::min<int64_t>(blocks, 1 << 16);

@@ -12,7 +12,9 @@ namespace kan {
 namespace {
 
 // Strided rows [B][T][H][D].
-bool strides_ok(const kan_heads_t& s) { return stride_ok(s.seq) && stride_ok(s.row) && stride_ok(s.head); }
+bool strides_ok(const kan_heads_t& s) {
+    return stride_ok(s.seq) && s.row >= 0 && s.row <= kDeltaMaxRow && stride_ok(s.head);
+}
 // Elements from the first to the last of the array, or -1 past 2^60.
 int64_t extent4(int64_t B, int64_t T, int64_t H, int64_t D, const kan_heads_t& s) {
     if (B == 0 || T == 0) return 0;
@@ -57,7 +59,7 @@ int delta_check(const kan_delta_desc_t* d) {
     if (!size_ok(d->B, 0) || !size_ok(d->T, 0) || !size_ok(d->Hk, 1) || !size_ok(d->Hv, 1) || d->Hv % d->Hk != 0)
         return KAN_ERR_SHAPE;
     if (d->Dk < 1 || d->Dk > kDeltaMaxDk || d->Dv < 1 || d->Dv > kDeltaMaxDv) return KAN_ERR_SHAPE;
-    if (d->B > kDeltaMaxHeads / d->Hv) return KAN_ERR_SHAPE;
+    if (d->B > kDeltaMaxHeads / d->Hv || d->Hv * d->Dv > kDeltaMaxRow) return KAN_ERR_SHAPE;
     const int64_t chunks = (d->T + kDeltaChunk - 1) / kDeltaChunk;
     if (chunks > 0 && d->B * d->Hv > kDeltaMaxChunks / chunks) return KAN_ERR_SHAPE;
     if (!dtype_ok(d->dtype)) return KAN_ERR_DTYPE;
