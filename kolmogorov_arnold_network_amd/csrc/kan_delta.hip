@@ -208,23 +208,18 @@ struct Carry {
     static constexpr int CH = W / 8, N = C * CH / NT, RS = NT / CH, PL = planes_of<TS>::n;
     static_assert(N >= 1 && NT % CH == 0 && C * CH % NT == 0, "whole rounds of pieces");
     Piece<TS> p[N];
-    __device__ __forceinline__ void load(const TS* base, int64_t row_stride, int rows, int D) {
-        const int row = (int)threadIdx.x / CH, at = 8 * ((int)threadIdx.x % CH);
+    __device__ __forceinline__ void load(int x, const TS* base, int64_t row_stride, int rows, int D) {
+        const int i = (int)threadIdx.x / CH + RS * x, at = 8 * ((int)threadIdx.x % CH);
         if constexpr (EVEN) {
-            const TS* from = base + (at < D ? at : 0);
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-                const int i = row + RS * x;
-                load_whole(p[x], from + (uint32_t)(i < rows ? i : rows - 1) * (uint32_t)row_stride);
-            }
+            load_whole(p[x], base + (at < D ? at : 0) + (uint32_t)(i < rows ? i : rows - 1) * (uint32_t)row_stride);
         } else {
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-                const int i = row + RS * x;
-                if (i < rows && at < D) load_piece(p[x], base + i * row_stride, at, D);
-                else no_piece(p[x]);
-            }
+            if (i < rows && at < D) load_piece(p[x], base + i * row_stride, at, D);
+            else no_piece(p[x]);
         }
+    }
+    __device__ __forceinline__ void load(const TS* base, int64_t row_stride, int rows, int D) {
+#pragma unroll
+        for (int x = 0; x < N; ++x) load(x, base, row_stride, rows, D);
     }
     __device__ __forceinline__ void put(uint16_t* lds, int x) const {
         const int e = threadIdx.x + NT * x;
@@ -257,12 +252,13 @@ template <int BYTES, int NT>
 struct CarryBytes {
     static constexpr int N = (BYTES / 16 + NT - 1) / NT;
     u32x4v v[N];
+    __device__ __forceinline__ void load(int x, const void* from) {
+        const int e = threadIdx.x + NT * x;
+        if (BYTES / 16 % NT == 0 || e < BYTES / 16) v[x] = static_cast<const u32x4v*>(from)[e];
+    }
     __device__ __forceinline__ void load(const void* from) {
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-            const int e = threadIdx.x + NT * x;
-            if (e < BYTES / 16) v[x] = static_cast<const u32x4v*>(from)[e];
-        }
+        for (int x = 0; x < N; ++x) load(x, from);
     }
     __device__ __forceinline__ void store(void* to) const {
 #pragma unroll
@@ -283,41 +279,37 @@ __device__ __forceinline__ void to_lds(const void* from, char* to) {
     __builtin_amdgcn_global_load_lds((hbm_void*)from, (lds_void*)to, 16, 0, 0);
 }
 __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0f70); }      // vmcnt(0)
+__device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
 template <int W, int NT>
 struct Direct {
-    static constexpr int CH = W / 8, N = C * CH / NT > 0 ? C * CH / NT : 1;     // fewer pieces than threads: whole waves
+    static constexpr int CH = W / 8, N = C * CH / NT;
+    static_assert(N >= 1, "a piece for every thread");
     uint32_t off[N];                                   // this thread's pieces of a chunk, in bytes
-    __device__ __forceinline__ void plan(int64_t row_stride) {
+    int row[N];                                        // and their rows; past the last one where there is no such column
+    __device__ __forceinline__ void plan(int64_t row_stride, int D) {
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-            const int e = threadIdx.x + NT * x, row = e / CH;
-            off[x] = 2 * ((uint32_t)row * (uint32_t)row_stride + 8 * (uint32_t)(piece_at<W>(row, e % CH) / 8 % CH));
+            const int e = threadIdx.x + NT * x, i = e / CH, c = piece_at<W>(i, e % CH) / 8 % CH;
+            off[x] = 2 * ((uint32_t)i * (uint32_t)row_stride + 8 * (uint32_t)c);
+            row[x] = 8 * c < D ? i : C;
         }
     }
-    __device__ __forceinline__ void load(const uint16_t* base, int rows, int D, uint16_t* lds) const {
-        const char* from = reinterpret_cast<const char*>(base);
-        char* to = reinterpret_cast<char*>(lds) + 16 * ((int)threadIdx.x & ~63);
-        if (rows >= C && D >= W) {                     // uniform
-#pragma unroll
-            for (int x = 0; x < N; ++x) to_lds(from + off[x], to + 16 * NT * x);
-            return;
-        }
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-            const int e = threadIdx.x + NT * x, row = e / CH, c = piece_at<W>(row, e % CH) / 8 % CH;
-            if (row < rows && 8 * c < D) to_lds(from + off[x], to + 16 * NT * x);
-            else *reinterpret_cast<u32x4v*>(reinterpret_cast<char*>(lds) + 16 * e) = u32x4v{0u, 0u, 0u, 0u};
-        }
+    __device__ __forceinline__ void load(int x, const uint16_t* base, int rows, char* lds) const {
+        const char* from = reinterpret_cast<const char*>(base) + off[x];
+        if (row[x] >= rows) from = reinterpret_cast<const char*>(&kZeros);
+        to_lds(from, lds + 16 * ((int)(threadIdx.x & ~63) + NT * x));
     }
 };
 template <int BYTES, int NT>
-__device__ __forceinline__ void bytes_to_lds(const void* from, char* lds) {
-    const int first = (int)threadIdx.x & ~63;
-#pragma unroll
-    for (int x = 0; x < (BYTES / 16 + NT - 1) / NT; ++x)
-        if (first + NT * x < BYTES / 16)               // whole waves: BYTES is a multiple of 1024
-            to_lds(static_cast<const char*>(from) + 16 * ((int)threadIdx.x + NT * x), lds + 16 * (first + NT * x));
-}
+struct DirectBytes {
+    static constexpr int N = (BYTES / 16 + NT - 1) / NT;
+    static_assert(BYTES % 1024 == 0, "whole waves");
+    static __device__ __forceinline__ void load(int x, const void* from, char* lds) {
+        const int first = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~63) + NT * x;
+        if (BYTES / 16 % NT != 0 && first >= BYTES / 16) return;       // uniform
+        to_lds(static_cast<const char*>(from) + 16 * (first + ((int)threadIdx.x & 63)), lds + 16 * first);
+    }
+};
 
 // A triangular matrix of 64 x 64 as left operand: six pieces [tile][32 columns] of 64
 // lanes by eight values are not zero, a plane after the other.
@@ -581,9 +573,6 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
 
 enum Pass { kForward, kStates, kBack };
 
-#ifndef SCAN_MIN
-#define SCAN_MIN 1
-#endif
 constexpr int kan_delta_halves(int dkp, int groups) { return dkp >= 64 && groups == 2 ? 2 : 1; }
 
 // How a scan's block is laid out.  A wave has 16 columns of the state and, where
@@ -683,10 +672,10 @@ __device__ __forceinline__ void beside() {
 }
 
 // ks[t] += rows of K times a wave's part of the state, of which NS planes are kept
-// in `sp`.  `last` loads what comes next.
-template <typename L, int DKP, int NS, typename Last>
+// in `sp`.  `last` loads what comes next, `ahead` parts of the next chunk.
+template <typename L, int DKP, int NS, typename Ahead, typename Last>
 __device__ __forceinline__ void rows_by_state(const uint16_t* K, int step0, const f32x4* S, f32x4 (&ks)[4],
-                                              bf16x8 (*sp)[NS], Last last) {
+                                              bf16x8 (*sp)[NS], Ahead ahead, Last last) {
     constexpr int PL = L::PL, TG = PL == 1 ? 4 : 2, PARTS = 4 / TG;
     bf16x8 f[2][TG][PL], sb[2][3];
     load_rows<TG, PL, DKP>(K, step0, 0, f[0]);
@@ -709,6 +698,8 @@ __device__ __forceinline__ void rows_by_state(const uint16_t* K, int step0, cons
             }
         }
         KAN_FENCE();
+        if (g == 0) ahead(1);                          // parts 1 and 2 of what comes
+        if (g == L::STEPS * PARTS / 2) ahead(2);
     }
 }
 // o[t] += the transposed product of rows of Q, tiles from `first` on, with the
@@ -747,7 +738,7 @@ __device__ __forceinline__ void add_tiles(const char* slot, f32x4* v, int n) {
 // their way from HBM meanwhile.  PASS kStates: keeps the chunks' first states and w
 // for the backward pass and writes no rows.
 template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
-__global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_MIN)
+__global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
     delta_scan_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
     typedef Scan<TS, DKP, GROUPS, PASS, EVEN> L;
     extern __shared__ __align__(16) char lds[];
@@ -782,45 +773,62 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
     Direct<DKP, NT> xk, xq;
     Direct<W, NT> xv;
     if (DIRECT) {
-        xk.plan(d.k.row);
-        if (FWD) xq.plan(d.q.row);
-        xv.plan(d.v.row);
+        xk.plan(d.k.row, Dk);
+        if (FWD) xq.plan(d.q.row, Dk);
+        xv.plan(d.v.row, Dv - nb);
     }
     // rows of a chunk lie at most 2^32 bytes apart: a lane's part of an address
     const uint32_t v_row = (uint32_t)d.v.row, y_row = (uint32_t)(d.Hv * Dv), column = mine ? n0 + m : 0;
     const uint32_t y_off = (uint32_t)row_of(0, m) * y_row + n0 + 4 * gq;
     const uint32_t s_off = 8 * gq * (uint32_t)p.dvp + n0 + m;
     TS vn[4][4];
-    auto fetch = [&](int n, char* to) {                // chunk n on its way to LDS, or to registers
+    // Chunk n on its way to LDS, or to registers.  Through registers it goes a few
+    // loads at a time between the products (1 x 32768 x 8 x 128 float32: scan 3215 us
+    // at once, 2927 in eight parts); directly to LDS all of it at once, since loads
+    // between the products hold those up as well (8 x 4096 x 16 x 128 bf16: 332 us at
+    // once, 351 in parts).
+    constexpr int PARTS = DIRECT ? 1 : 8;
+    auto fetch = [&](int part, int n) {
         const int64_t t0 = (int64_t)n * C;
         const int rows = len - n * C;
-        if constexpr (DIRECT) {
-            xk.load(k_base + t0 * d.k.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::K));
-            if (FWD) xq.load(q_base + t0 * d.q.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::Q));
-            xv.load(v_base + t0 * d.v.row + nb, rows, Dv - nb, reinterpret_cast<uint16_t*>(to + L::V));
-            bytes_to_lds<kFields * C * 4, NT>(rows_base + (int64_t)n * kFields * C, to + L::FIELDS);
-        } else {
-            ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
-            if (FWD) cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
-            cr.load(rows_base + (int64_t)n * kFields * C);
-            const TS* v = v_base + t0 * d.v.row;
+        char* const to = lds + (DIRECT ? (n & 1) * L::BUF : 0);
+        const char* const mats = mats_base + n * p.mats;
+        const float* const fields = rows_base + (int64_t)n * kFields * C;
+        constexpr int NK = ck.N, NQ = FWD ? NK : 0, NV = DIRECT ? xv.N : 16, NM = cm.N, NF = cr.N;
+        constexpr int ALL = NK + NQ + NV + NM + NF;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = row_of(t, j) + 8 * gq;
-                    vn[t][j] = v[(uint32_t)(i < rows ? i : rows - 1) * v_row + column];
+        for (int j = 0; j < ALL; ++j) {
+            if (j * PARTS / ALL != part) continue;
+            const int q = j - NK, v = q - NQ, x = v - NV, f = x - NM;
+            if (j < NK) {
+                if constexpr (DIRECT) xk.load(j, k_base + t0 * d.k.row, rows, to + L::K);
+                else ck.load(j, k_base + t0 * d.k.row, d.k.row, rows, Dk);
+            } else if (q < NQ) {
+                if constexpr (DIRECT) xq.load(q, q_base + t0 * d.q.row, rows, to + L::Q);
+                else cq.load(q, q_base + t0 * d.q.row, d.q.row, rows, Dk);
+            } else if (v < NV) {
+                if constexpr (DIRECT) {
+                    xv.load(v, v_base + t0 * d.v.row + nb, rows, to + L::V);
+                } else {
+                    const int i = row_of(v / 4, v % 4) + 8 * gq;
+                    vn[v / 4][v % 4] = (v_base + t0 * d.v.row)[(uint32_t)(i < rows ? i : rows - 1) * v_row + column];
                 }
+            } else if (x < NM) {
+                if constexpr (L::MATS_DIRECT)
+                    DirectBytes<L::MATS * 2, NT>::load(x, mats, lds + L::G + (n & 1) * L::G_BUF);
+                else cm.load(x, mats);
+            } else {
+                if constexpr (DIRECT) DirectBytes<kFields * C * 4, NT>::load(f, fields, to + L::FIELDS);
+                else cr.load(f, fields);
+            }
         }
-        if constexpr (L::MATS_DIRECT) bytes_to_lds<L::MATS * 2, NT>(mats_base + n * p.mats, lds + L::G + (n & 1) * L::G_BUF);
-        else cm.load(mats_base + n * p.mats);
     };
     char* const my_slot = lds + L::SLOT0 + wave * L::SLOT;
     char* const other_slot = lds + L::SLOT0 + (wave ^ 1) * L::SLOT;
     // The rows of a chunk are stored in the next one's time: what waits for the
     // chunk's arrival waits for stores under way as well.  A pair of waves has two
     // tiles of rows each, o[0] and o[1] of tiles 2 half, 2 half + 1.
-    f32x4 o[4];
+    f32x4 o[4], w[4];
     auto put_rows = [&](int n) {
         TS* const out = y_base + (int64_t)n * C * y_row;
         const int rows = len - n * C;
@@ -840,14 +848,16 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
             }
         }
     };
-    if (chunks > 0) fetch(0, lds);
+    if (chunks > 0) {
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) fetch(part, 0);
+    }
     for (int n = 0; n < chunks; ++n) {
         const int64_t ch = bh * p.chunks + n;
         const int rows = len - n * C;
         char* const buf = lds + (DIRECT ? (n & 1) * L::BUF : 0);
         if (DIRECT) arrived();
         __syncthreads();                               // direct: the chunk is there; else: LDS is free
-        f32x4 w[4];
         if (!DIRECT) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -860,7 +870,10 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
         if constexpr (!L::MATS_DIRECT) cm.store(lds + L::G);
         if (!DIRECT) __syncthreads();
         // nothing may be on its way to LDS when the block ends
-        if (!DIRECT || n + 1 < chunks) fetch(n + 1 < chunks ? n + 1 : n, lds + (DIRECT ? ((n + 1) & 1) * L::BUF : 0));
+        auto ahead = [&](int part) {
+            if (part < PARTS && (!DIRECT || n + 1 < chunks)) fetch(part, n + 1 < chunks ? n + 1 : n);
+        };
+        ahead(0);
         if (FWD && n > 0) put_rows(n - 1);
         const uint16_t* const K = reinterpret_cast<const uint16_t*>(buf + L::K);       // [PL][64][DKP]
         const uint16_t* const Q = reinterpret_cast<const uint16_t*>(buf + L::Q);       // forward alone
@@ -875,13 +888,23 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) (out + row_of(x0 + x, j) * p.dvp)[s_off] = S[x][j];
         }
+        f32x4 fk[4], beta[4], tk[4];                   // the rows' factors, on their way meanwhile
+        float fq[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            fk[t] = at_rows(row, kFk, t);
+            beta[t] = at_rows(row, kBeta, t);
+            tk[t] = at_rows(row, kTk, t);
+            fq[t] = FWD ? row[kFq * C + row_of((t + 2 * half) & 3, m)] : 0.0f;
+        }
+        const float whole = whole_decay(row);
         // K S
         constexpr int TG = PL == 1 ? 4 : 2, NS = FWD ? NP : 1;
         f32x4 ks[4];
         bf16x8 sp[L::STEPS][NS], f[2][TG][PL], ga[4][3], gb[2][3];
 #pragma unroll
         for (int t = 0; t < 4; ++t) ks[t] = o[t] = zero4();
-        rows_by_state<L, DKP, NS>(K, half * L::STEPS, S, ks, sp, [&] {
+        rows_by_state<L, DKP, NS>(K, half * L::STEPS, S, ks, sp, ahead, [&] {
             if constexpr (DIRECT) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -893,7 +916,9 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
                 }
             }
             if (FWD) load_rows<TG, PL, DKP>(Q, half * L::STEPS, 2 * half, f[0]);
+            if (L::MATS_DIRECT) load_tri<3, false, true>(G, ga);
         });
+        ahead(3);
         if (HALVES == 2) give_tiles(my_slot, ks, 4);
         if (HALVES == 2 || !L::MATS_DIRECT) __syncthreads();           // G and P are there, and the partner's part
         if (HALVES == 2) add_tiles(other_slot, ks, 4);
@@ -904,21 +929,22 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
             if (part < 2) {
 #pragma unroll
                 for (int t = 2 * part; t < 2 * part + 2; ++t) {
-                    w[t] = w[t] - at_rows(row, kFk, t) * ks[t];        // e
-                    be[t] = at_rows(row, kBeta, t) * w[t];
+                    w[t] = w[t] - fk[t] * ks[t];       // e
+                    be[t] = beta[t] * w[t];
                 }
             } else {
                 split8<3>(be[2 * part - 4], be[2 * part - 3], eb[part - 2]);
             }
         };
+        if (!L::MATS_DIRECT) load_tri<3, false, true>(G, ga);
         if constexpr (FWD) {
-            state_by_rows<L, DKP>(Q, half * L::STEPS, 2 * half, sp, o, f, errors, [&] { load_tri<3, false, true>(G, ga); });
+            state_by_rows<L, DKP>(Q, half * L::STEPS, 2 * half, sp, o, f, errors, [&] { load_tri<3, false, false>(G, gb); });
         } else {
-            load_tri<3, false, true>(G, ga);
+            load_tri<3, false, false>(G, gb);
 #pragma unroll
             for (int i = 0; i < 4; ++i) errors(i);
         }
-        load_tri<3, false, false>(G, gb);
+        ahead(4);
         // P for this wave's tiles: all of them, or the first two or the last two
         bf16x8 pa[4][NP], pb[2][NP];
         const uint16_t* const p_at = L::P_LDS ? P : reinterpret_cast<const uint16_t*>(mats_base + n * p.mats) + 3 * kTri;
@@ -938,23 +964,26 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
         for (int t = 0; t < 4; ++t) ge[t] = zero4();
         mma_tiles<4, 3, 3>(ge, ga, eb[0]);
         mma_tiles<2, 3, 3>(ge + 2, gb, eb[1]);
-        const float whole = whole_decay(row);
 #pragma unroll
         for (int x = 0; x < DT; ++x) S[x] = whole * S[x];
         if (FWD) {
 #pragma unroll
-            for (int l = 0; l < 4; ++l) o[l] = o[l] * row[kFq * C + row_of((l + 2 * half) & 3, m)];
+            for (int l = 0; l < 4; ++l) o[l] = o[l] * fq[l];
         }
+        // columns of K: all of them at once, or two groups ahead
+        constexpr int GROUP_N = 2 * L::STEPS, AHEAD = PL == 1 ? GROUP_N : 2;
+        bf16x8 kc[AHEAD][2][PL];
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) load_cols<PL, DKP>(K, half * L::STEPS + g / 2, g & 1, kc[g]);
         KAN_FENCE();
+        ahead(5);
         if (FWD && HALVES == 2) give_tiles(other_slot, o + 2, 2);      // read before; the partner adds it after the next barrier
-        bf16x8 kc[2][2][PL];
-        load_cols<PL, DKP>(K, half * L::STEPS, 0, kc[0]);
         f32x4 u[4];
         bf16x8 ub[2][3], uo[2][NP];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             w[t] = w[t] - ge[t];
-            u[t] = at_rows(row, kBeta, t) * w[t];
+            u[t] = beta[t] * w[t];
         }
         if (FWD) {
             split8<NP>(u[0], u[1], uo[0]);
@@ -977,16 +1006,19 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
             }
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) u[t] = u[t] * at_rows(row, kTk, t);
+        for (int t = 0; t < 4; ++t) u[t] = u[t] * tk[t];
         split8<3>(u[0], u[1], ub[0]);
         split8<3>(u[2], u[3], ub[1]);
         if (FWD && HALVES == 1) beside<18, 6>();
         // S = exp(c_63) S + K^T (exp(c_63 - c) u)
+        KAN_FENCE();
+        ahead(6);
 #pragma unroll
-        for (int g = 0; g < 2 * L::STEPS; ++g) {
-            if (g + 1 < 2 * L::STEPS) load_cols<PL, DKP>(K, half * L::STEPS + (g + 1) / 2, (g + 1) & 1, kc[(g + 1) & 1]);
+        for (int g = 0; g < GROUP_N; ++g) {
+            if (g == GROUP_N / 2) ahead(7);
+            mma_tiles<2, PL, 3>(S + (g & ~1), kc[g % AHEAD], ub[g & 1]);
             KAN_FENCE();
-            mma_tiles<2, PL, 3>(S + (g & ~1), kc[g & 1], ub[g & 1]);
+            if (g + AHEAD < GROUP_N) load_cols<PL, DKP>(K, half * L::STEPS + (g + AHEAD) / 2, g & 1, kc[g % AHEAD]);
             KAN_FENCE();
         }
     }
@@ -1012,7 +1044,7 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT), SCAN_
 
 // Backwards along a sequence: r, dv and the gradients of the chunks' last states.
 template <typename TS, int DKP, int GROUPS, bool EVEN>
-__global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN_MIN)
+__global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
     delta_back_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
     typedef Scan<TS, DKP, GROUPS, kBack, EVEN> L;
     extern __shared__ __align__(16) char lds[];
@@ -1052,32 +1084,66 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN
     Direct<DKP, NT> xk, xq;
     Direct<W, NT> xy;
     if (DIRECT) {
-        xk.plan(d.k.row);
-        xq.plan(d.q.row);
-        xy.plan(d.Hv * Dv);
+        xk.plan(d.k.row, Dk);
+        xq.plan(d.q.row, Dk);
+        xy.plan(d.Hv * Dv, Dv - nb);
     }
     const uint32_t s_off = 8 * gq * (uint32_t)p.dvp + n0 + m, v_row = (uint32_t)d.dv.row;
     const uint32_t v_off = 8 * gq * v_row + (mine ? n0 + m : 0);
-    auto fetch = [&](int n, char* to) {
+    constexpr int PARTS = DIRECT ? 1 : 8;
+    auto fetch = [&](int part, int n) {                // as in the scan above
         const int64_t t0 = (int64_t)n * C;
         const int rows = len - n * C;
-        if constexpr (DIRECT) {
-            xk.load(k_base + t0 * d.k.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::K));
-            xq.load(q_base + t0 * d.q.row, rows, Dk, reinterpret_cast<uint16_t*>(to + L::Q));
-            xy.load(y_base + t0 * d.Hv * Dv, rows, Dv - nb, reinterpret_cast<uint16_t*>(to + L::V));
-            bytes_to_lds<kFields * C * 4, NT>(rows_base + (int64_t)n * kFields * C, to + L::FIELDS);
-        } else {
-            ck.load(k_base + t0 * d.k.row, d.k.row, rows, Dk);
-            cq.load(q_base + t0 * d.q.row, d.q.row, rows, Dk);
-            cy.load(y_base + t0 * d.Hv * Dv, d.Hv * Dv, rows, Dv - nb);
-            cr.load(rows_base + (int64_t)n * kFields * C);
+        char* const to = lds + (DIRECT ? (n & 1) * L::BUF : 0);
+        const char* const mats = mats_base + n * p.mats;
+        const float* const fields = rows_base + (int64_t)n * kFields * C;
+        constexpr int NK = ck.N, NY = cy.N, NM = cm.N, NF = cr.N, ALL = 2 * NK + NY + NM + NF;
+#pragma unroll
+        for (int j = 0; j < ALL; ++j) {
+            if (j * PARTS / ALL != part) continue;
+            const int q = j - NK, v = q - NK, x = v - NY, f = x - NM;
+            if (j < NK) {
+                if constexpr (DIRECT) xk.load(j, k_base + t0 * d.k.row, rows, to + L::K);
+                else ck.load(j, k_base + t0 * d.k.row, d.k.row, rows, Dk);
+            } else if (q < NK) {
+                if constexpr (DIRECT) xq.load(q, q_base + t0 * d.q.row, rows, to + L::Q);
+                else cq.load(q, q_base + t0 * d.q.row, d.q.row, rows, Dk);
+            } else if (v < NY) {
+                if constexpr (DIRECT) xy.load(v, y_base + t0 * d.Hv * Dv, rows, to + L::V);
+                else cy.load(v, y_base + t0 * d.Hv * Dv, d.Hv * Dv, rows, Dv - nb);
+            } else if (x < NM) {
+                if constexpr (L::MATS_DIRECT)
+                    DirectBytes<L::MATS * 2, NT>::load(x, mats, lds + L::G + (n & 1) * L::G_BUF);
+                else cm.load(x, mats);
+            } else {
+                if constexpr (DIRECT) DirectBytes<kFields * C * 4, NT>::load(f, fields, to + L::FIELDS);
+                else cr.load(f, fields);
+            }
         }
-        if constexpr (L::MATS_DIRECT) bytes_to_lds<L::MATS * 2, NT>(mats_base + n * p.mats, lds + L::G + (n & 1) * L::G_BUF);
-        else cm.load(mats_base + n * p.mats);
     };
     char* const my_slot = lds + L::SLOT0 + wave * L::SLOT;
     const char* const other_slot = lds + L::SLOT0 + (wave ^ 1) * L::SLOT;
-    if (chunks > 0) fetch(chunks - 1, lds + (DIRECT ? ((chunks - 1) & 1) * L::BUF : 0));
+    // r and dv of a chunk, stored in the next one's time
+    f32x4 r[4], dv[4];
+    auto put_rows = [&](int n) {
+        const int rows = len - n * C;
+        float* const out_r = reinterpret_cast<float*>(ws + p.off_r) + (bh * p.chunks + n) * C * p.dvp;
+        TS* const out_v = static_cast<TS*>(a.dv) + at_row(d.dv, b, (int64_t)n * C, h);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (HALVES == 2 && t / 2 != half) continue;                // uniform
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                (out_r + row_of(t, j) * p.dvp)[s_off] = r[t][j];
+                if (rows >= C ? mine : mine && row_of(t, j) + 8 * gq < rows)
+                    put(out_v + (uint32_t)row_of(t, j) * v_row + v_off, dv[t][j]);
+            }
+        }
+    };
+    if (chunks > 0) {
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) fetch(part, chunks - 1);
+    }
     for (int n = chunks - 1; n >= 0; --n) {
         const int64_t ch = bh * p.chunks + n, t0 = (int64_t)n * C;
         const int rows = len - n * C;
@@ -1092,7 +1158,11 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN
         }
         if constexpr (!L::MATS_DIRECT) cm.store(lds + L::G);
         if (!DIRECT) __syncthreads();
-        if (n > 0 || !DIRECT) fetch(n > 0 ? n - 1 : 0, lds + (DIRECT ? ((n + 1) & 1) * L::BUF : 0));
+        auto ahead = [&](int part) {
+            if (part < PARTS && (!DIRECT || n > 0)) fetch(part, n > 0 ? n - 1 : 0);
+        };
+        ahead(0);
+        if (n + 1 < chunks) put_rows(n + 1);
         const uint16_t* const K = reinterpret_cast<const uint16_t*>(buf + L::K);       // [PL][64][DKP]
         const uint16_t* const Q = reinterpret_cast<const uint16_t*>(buf + L::Q);
         const uint16_t* const Y = reinterpret_cast<const uint16_t*>(buf + L::V);       // [PL][64][W]: dY
@@ -1104,15 +1174,25 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN
         for (int x = 0; x < DT; ++x)
 #pragma unroll
             for (int j = 0; j < 4; ++j) (out_S + row_of(x0 + x, j) * p.dvp)[s_off] = S[x][j];
+        f32x4 fk[4], beta[4], tk[4], fq[4];            // the rows' factors, on their way meanwhile
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            fk[t] = at_rows(row, kFk, t);
+            beta[t] = at_rows(row, kBeta, t);
+            tk[t] = at_rows(row, kTk, t);
+            fq[t] = at_rows(row, kFq, t);
+        }
+        const float whole = whole_decay(row);
         f32x4 kd[4], py[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) kd[t] = py[t] = zero4();
         bf16x8 yb[2][PL];                              // dY in this wave's columns
         bf16x8 unused[L::STEPS][1];
-        rows_by_state<L, DKP, 1>(K, half * L::STEPS, S, kd, unused, [&] {
+        rows_by_state<L, DKP, 1>(K, half * L::STEPS, S, kd, unused, ahead, [&] {
             col_frag<PL, W>(Y, 0, 2 * group + ((m & 3) >> 1), m & 1, yb[0]);
             col_frag<PL, W>(Y, 1, 2 * group + ((m & 3) >> 1), m & 1, yb[1]);
         });
+        ahead(3);
         if (HALVES == 2) give_tiles(my_slot, kd, 4);
         if (HALVES == 2 || !L::MATS_DIRECT) __syncthreads();           // G^T and P^T are there, and the partner's part
         {
@@ -1127,6 +1207,7 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN
         load_tri<3, true, true>(G, ga);
         load_tri<3, true, false>(G, gb);
         KAN_FENCE();
+        ahead(4);
         f32x4 y[4];                                    // dY as floats
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -1140,14 +1221,13 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN
                     y[2 * s + (j >> 2)][j & 3] = z ? y[2 * s + (j >> 2)][j & 3] + v : v;
                 }
             }
-        f32x4 r[4];
         {
             f32x4 gu[4], bu[4];
             bf16x8 ub[2][3];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                r[t] = py[t] + at_rows(row, kTk, t) * kd[t];           // du
-                bu[t] = at_rows(row, kBeta, t) * r[t];
+                r[t] = py[t] + tk[t] * kd[t];          // du
+                bu[t] = beta[t] * r[t];
                 gu[t] = zero4();
             }
             split8<3>(bu[2], bu[3], ub[1]);
@@ -1157,44 +1237,43 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT), SCAN
 #pragma unroll
             for (int t = 0; t < 4; ++t) r[t] = r[t] - gu[t];
         }
-        bf16x8 kc[2][2][PL];
-        load_cols<PL, DKP>(K, half * L::STEPS, 0, kc[0]);
+        // columns of K and Q in turn, two groups ahead
+        constexpr int GROUP_N = 4 * L::STEPS, AHEAD = PL == 1 ? 4 : 2;
+        bf16x8 kc[AHEAD][2][PL];
+        auto load_group = [&](int g) {
+            load_cols<PL, DKP>(g & 2 ? Q : K, half * L::STEPS + g / 4, g & 1, kc[g % AHEAD]);
+        };
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) load_group(g);
         KAN_FENCE();
-        float* const out_r = reinterpret_cast<float*>(ws + p.off_r) + ch * C * p.dvp;
-        TS* const out_v = static_cast<TS*>(a.dv) + at_row(d.dv, b, t0, h);
+        ahead(5);
+        f32x4 v[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const f32x4 dv = at_rows(row, kBeta, t) * r[t];
-            if (HALVES == 1 || t / 2 == half) {                        // uniform
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    (out_r + row_of(t, j) * p.dvp)[s_off] = r[t][j];
-                    if (rows >= C ? mine : mine && row_of(t, j) + 8 * gq < rows)
-                        put(out_v + (uint32_t)row_of(t, j) * v_row + v_off, dv[j]);
-                }
-            }
+            dv[t] = beta[t] * r[t];
             // rows of exp(c) (scale Q^T dY - K^T dv)
-            y[t] = y[t] * at_rows(row, kFq, t);
-            r[t] = -dv * at_rows(row, kFk, t);
+            y[t] = y[t] * fq[t];
+            v[t] = -dv[t] * fk[t];
         }
         bf16x8 ys[2][3], vs[2][3];
-        split8<3>(r[0], r[1], vs[0]);
-        split8<3>(r[2], r[3], vs[1]);
+        split8<3>(v[0], v[1], vs[0]);
+        split8<3>(v[2], v[3], vs[1]);
         split8<3>(y[0], y[1], ys[0]);
         split8<3>(y[2], y[3], ys[1]);
-        const float whole = whole_decay(row);
 #pragma unroll
         for (int x = 0; x < DT; ++x) S[x] = whole * S[x];
+        KAN_FENCE();
+        ahead(6);
 #pragma unroll
-        for (int g = 0; g < 4 * L::STEPS; ++g) {       // two tiles of the state by K, then by Q
-            const int next = g + 1;
-            if (next < 4 * L::STEPS)
-                load_cols<PL, DKP>(next & 2 ? Q : K, half * L::STEPS + next / 4, next & 1, kc[next & 1]);
+        for (int g = 0; g < GROUP_N; ++g) {            // two tiles of the state by K, then by Q
+            if (g == GROUP_N / 2) ahead(7);
+            mma_tiles<2, PL, 3>(S + 2 * (g / 4), kc[g % AHEAD], g & 2 ? ys[g & 1] : vs[g & 1]);
             KAN_FENCE();
-            mma_tiles<2, PL, 3>(S + 2 * (g / 4), kc[g & 1], g & 2 ? ys[g & 1] : vs[g & 1]);
+            if (g + AHEAD < GROUP_N) load_group(g + AHEAD);
             KAN_FENCE();
         }
     }
+    if (chunks > 0) put_rows(0);
     if (!a.dh0 || !mine) return;
 #pragma unroll
     for (int x = 0; x < DT; ++x)
