@@ -16,7 +16,8 @@ constexpr int64_t kDeltaMaxChunks = int64_t(1) << 23;   // chunks of all heads, 
 // is one chunk of one value head: number (b Hv + h) chunks + n.
 struct DeltaPlan {
     int dkp, dvp;                    // Dk up to 32, 64 or 128; Dv up to a multiple of 64
-    int waves;                       // of a scan's block, 16 state columns each
+    int groups;                      // of 16 state columns, of a scan's block
+    int segs, runs, seg_chunks;      // segments of a sequence (1: whole), those whose run is composed, chunks of one
     int64_t chunks, heads;           // of a sequence; B Hv
     int64_t mats;                    // bytes of a chunk-head's matrices
     size_t off_rows;                 // [chunk-head][8][64] float32
@@ -24,6 +25,8 @@ struct DeltaPlan {
     size_t off_w, off_r;             // [chunk-head][64][dvp] float32 (backward)
     size_t off_S, off_dS;            // [chunk-head][dkp][dvp] float32 (backward)
     size_t off_dq, off_dk;           // [B][T][Hv][Dk] float32, where heads share keys (backward)
+    size_t off_runs;                 // [segment][head][dkp][dvp + dkp] float32: runs of the segments
+    size_t off_starts, off_ends;     // [segment][head][dkp][dvp] float32: their first states; dS at their ends (backward)
     size_t ws;
 };
 DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass);

@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
 
 // ---- along a sequence -------------------------------------------------------------
 
-enum Pass { kForward, kStates, kBack };
+enum Pass { kForward, kStates, kRuns, kBack };
 
 constexpr int kan_delta_halves(int dkp, int groups) { return dkp >= 64 && groups == 2 ? 2 : 1; }
 
@@ -589,10 +589,10 @@ struct Scan {
     // a second buffer.  Others pass through registers into one buffer.
     static constexpr bool DIRECT = PL == 1 && EVEN;
     // float32 has no room for P, which the waves then read from the workspace
-    static constexpr bool P_LDS = PASS != kStates && PL == 1;
-    static constexpr int MATS = (PASS == kStates ? 3 : P_LDS ? 3 + (FWD ? NP : 3) : 3) * kTri;   // G, P (or transposed)
+    static constexpr bool P_LDS = (FWD || BACK) && PL == 1;
+    static constexpr int MATS = (P_LDS ? 3 + (FWD ? NP : 3) : 3) * kTri;   // G, P (or transposed)
     static constexpr int ROWS = PL * C * DKP;
-    static constexpr int K = 0, Q = K + ROWS * 2, V = Q + (PASS == kStates ? 0 : ROWS * 2);    // offsets in bytes
+    static constexpr int K = 0, Q = K + ROWS * 2, V = Q + (FWD || BACK ? ROWS * 2 : 0);        // offsets in bytes
     static constexpr int FIELDS = V + (BACK ? PL * C * W * 2 : DIRECT ? C * W * 2 : 0);
     static constexpr int BUF = FIELDS + kFields * C * 4;
     static constexpr int SLOT = 4 * 64 * 16, SLOTS = HALVES == 2 ? 2 * GROUPS * SLOT : 0;      // a slot: four tiles of a wave
@@ -737,6 +737,12 @@ __device__ __forceinline__ void add_tiles(const char* slot, f32x4* v, int n) {
 // the same for the block's waves and come through LDS; the next chunk's are on
 // their way from HBM meanwhile.  PASS kStates: keeps the chunks' first states and w
 // for the backward pass and writes no rows.
+//
+// Where heads are too few to fill the GPU their chunks are cut into segments.  A
+// segment takes the state before it to M S + B; PASS kRuns finds M, which is what
+// becomes of the columns of the identity without values, and B, which is what
+// becomes of no state; the starts of the segments follow from these one after the
+// other (delta_link_kernel), and the pass itself runs all segments at once.
 template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
 __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
     delta_scan_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
@@ -744,26 +750,40 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
     extern __shared__ __align__(16) char lds[];
     constexpr bool FWD = L::FWD, DIRECT = L::DIRECT;
     constexpr int PL = L::PL, NP = L::NP, NT = L::NT, W = L::W, DT = L::DT, HALVES = L::HALVES, OWN = 4 / HALVES;
+    constexpr bool RUNS = PASS == kRuns;
+    const int vtiles = (int)((d.Dv + W - 1) / W), mtiles = RUNS ? (DKP + W - 1) / W : 0;
     int head, tile;
-    head_and_tile((int)p.heads, (int)((d.Dv + W - 1) / W), head, tile);
-    const int64_t bh = head, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
+    head_and_tile((int)p.heads * (RUNS ? p.runs : p.segs), vtiles + mtiles, head, tile);
+    const int seg = head / (int)p.heads;
+    const int64_t bh = head % (int)p.heads, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave % HALVES;
-    const int nb = tile * W, n0 = nb + 16 * (wave / HALVES);       // the block's and this wave's first column
-    const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), chunks = (len + C - 1) / C;
-    const bool mine = n0 + m < Dv;
+    const bool of_m = RUNS && tile >= vtiles;                      // columns of the identity
+    if (of_m && seg == 0) return;                                  // the first segment starts from h0
+    const int nb = (of_m ? tile - vtiles : tile) * W, n0 = nb + 16 * (wave / HALVES);   // the block's and this wave's first column
+    const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), all = (len + C - 1) / C;
+    // this segment's chunks
+    const int first = seg * p.seg_chunks, chunks = all < first + p.seg_chunks ? all : first + p.seg_chunks;
+    const bool mine = n0 + m < (of_m ? Dk : Dv);
     const int x0 = half * DT;                                      // this wave's first tile of the state
+    const float* start = a.h0 ? a.h0 + bh * Dk * Dv : nullptr;     // [Dk][Dv], or of the workspace [dkp][dvp]
+    int start_row = Dv;
+    if (seg > 0) {
+        start = RUNS ? nullptr : reinterpret_cast<const float*>(ws + p.off_starts) + (seg * p.heads + bh) * DKP * p.dvp;
+        start_row = p.dvp;
+    }
     f32x4 S[DT];
 #pragma unroll
     for (int x = 0; x < DT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int dd = row_of(x0 + x, 4 * gq) + j;
-            S[x][j] = a.h0 && dd < Dk && mine ? a.h0[(bh * Dk + dd) * Dv + n0 + m] : 0.0f;
+            S[x][j] = of_m ? (dd == n0 + m && mine ? 1.0f : 0.0f)
+                           : start && dd < Dk && mine ? start[(int64_t)dd * start_row + n0 + m] : 0.0f;
         }
     const TS* const k_base = static_cast<const TS*>(a.k) + at_row(d.k, b, 0, hk);
     const TS* const q_base = static_cast<const TS*>(a.q) + at_row(d.q, b, 0, hk);
-    const TS* const v_base = static_cast<const TS*>(a.v) + at_row(d.v, b, 0, h);
+    const TS* const v_base = static_cast<const TS*>(a.v) + at_row(d.v, b, 0, h);      // not used where of_m
     TS* const y_base = static_cast<TS*>(a.y) + (b * d.T * d.Hv + h) * Dv;
     const float* const rows_base = reinterpret_cast<const float*>(ws + p.off_rows) + bh * p.chunks * kFields * C;
     const char* const mats_base = ws + p.off_mats + bh * p.chunks * p.mats;
@@ -775,10 +795,10 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
     if (DIRECT) {
         xk.plan(d.k.row, Dk);
         if (FWD) xq.plan(d.q.row, Dk);
-        xv.plan(d.v.row, Dv - nb);
+        xv.plan(d.v.row, of_m ? 0 : Dv - nb);          // no values: zeros
     }
     // rows of a chunk lie at most 2^32 bytes apart: a lane's part of an address
-    const uint32_t v_row = (uint32_t)d.v.row, y_row = (uint32_t)(d.Hv * Dv), column = mine ? n0 + m : 0;
+    const uint32_t v_row = (uint32_t)d.v.row, y_row = (uint32_t)(d.Hv * Dv), column = mine && !of_m ? n0 + m : 0;
     const uint32_t y_off = (uint32_t)row_of(0, m) * y_row + n0 + 4 * gq;
     const uint32_t s_off = 8 * gq * (uint32_t)p.dvp + n0 + m;
     TS vn[4][4];
@@ -848,11 +868,11 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
             }
         }
     };
-    if (chunks > 0) {
+    if (first < chunks) {
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) fetch(part, 0);
+        for (int part = 0; part < PARTS; ++part) fetch(part, first);
     }
-    for (int n = 0; n < chunks; ++n) {
+    for (int n = first; n < chunks; ++n) {
         const int64_t ch = bh * p.chunks + n;
         const int rows = len - n * C;
         char* const buf = lds + (DIRECT ? (n & 1) * L::BUF : 0);
@@ -862,7 +882,7 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[t][j] = row_of(t, j) + 8 * gq < rows ? load_f(&vn[t][j], 0) : 0.0f;
+                for (int j = 0; j < 4; ++j) w[t][j] = !of_m && row_of(t, j) + 8 * gq < rows ? load_f(&vn[t][j], 0) : 0.0f;
             ck.store(reinterpret_cast<uint16_t*>(lds + L::K), rows, Dk);
             if (FWD) cq.store(reinterpret_cast<uint16_t*>(lds + L::Q), rows, Dk);
             cr.store(lds + L::FIELDS);
@@ -874,14 +894,14 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
             if (part < PARTS && (!DIRECT || n + 1 < chunks)) fetch(part, n + 1 < chunks ? n + 1 : n);
         };
         ahead(0);
-        if (FWD && n > 0) put_rows(n - 1);
+        if (FWD && n > first) put_rows(n - 1);
         const uint16_t* const K = reinterpret_cast<const uint16_t*>(buf + L::K);       // [PL][64][DKP]
         const uint16_t* const Q = reinterpret_cast<const uint16_t*>(buf + L::Q);       // forward alone
         const uint16_t* const V = reinterpret_cast<const uint16_t*>(buf + L::V);       // [64][W], direct alone
         const float* const row = reinterpret_cast<const float*>(buf + L::FIELDS);      // [8][64]
         const uint16_t* const G = reinterpret_cast<const uint16_t*>(lds + L::G + (n & 1) * L::G_BUF);  // [3][kTri]
         const uint16_t* const P = G + 3 * kTri;                                        // [NP][kTri], forward alone
-        if (!FWD) {
+        if (PASS == kStates) {
             float* out = reinterpret_cast<float*>(ws + p.off_S) + ch * DKP * p.dvp;
 #pragma unroll
             for (int x = 0; x < DT; ++x)
@@ -996,7 +1016,7 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
                 mma_tiles_t<4, NP, NP>(o, pa, uo[0]);
                 mma_tiles_t<2, NP, NP>(o + 2, pb, uo[1]);
             }
-        } else {
+        } else if (PASS == kStates) {
             float* out = reinterpret_cast<float*>(ws + p.off_w) + ch * C * p.dvp;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -1022,17 +1042,30 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
             KAN_FENCE();
         }
     }
-    if (FWD && chunks > 0) {
+    if constexpr (RUNS) {                              // [dkp][dvp + dkp]: B, then M
+        float* const out = reinterpret_cast<float*>(ws + p.off_runs) + (seg * p.heads + bh) * DKP * (p.dvp + DKP) +
+                           (of_m ? p.dvp : 0) + n0 + m;
+        if (!of_m || n0 < DKP)
+#pragma unroll
+            for (int x = 0; x < DT; ++x)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) out[(row_of(x0 + x, 4 * gq) + j) * (p.dvp + DKP)] = S[x][j];
+    }
+    if (!FWD) return;
+    if (first < chunks) {
         __syncthreads();
         put_rows(chunks - 1);
     }
-    if (!FWD) return;
-    for (int64_t e = lane + 64 * half; e < (d.T - len) * 16; e += 64 * HALVES) {
-        const int64_t t = len + e / 16;
+    // rows of this segment behind the sequence's end
+    const int64_t past = len > (int64_t)first * C ? len : (int64_t)first * C;
+    const int64_t last_row = seg + 1 < p.segs ? (int64_t)(first + p.seg_chunks) * C : d.T;
+    for (int64_t e = lane + 64 * half; e < (last_row - past) * 16; e += 64 * HALVES) {
+        const int64_t t = past + e / 16;
         const int nn = n0 + (int)(e % 16);
         if (nn < Dv) put(static_cast<TS*>(a.y) + ((b * d.T + t) * d.Hv + h) * Dv + nn, 0.0f);
     }
-    if (!a.hT || !mine) return;
+    // the last state is that of the segment with the sequence's end
+    if (!a.hT || !mine || all > first + p.seg_chunks || (all <= first && seg > 0)) return;
 #pragma unroll
     for (int x = 0; x < DT; ++x)
 #pragma unroll
@@ -1043,7 +1076,9 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
 }
 
 // Backwards along a sequence: r, dv and the gradients of the chunks' last states.
-template <typename TS, int DKP, int GROUPS, bool EVEN>
+// In segments the gradient of the state goes through one as M^T dS + F; RUNS finds
+// F, what becomes of no gradient.
+template <typename TS, int DKP, int GROUPS, bool EVEN, bool RUNS>
 __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
     delta_back_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
     typedef Scan<TS, DKP, GROUPS, kBack, EVEN> L;
@@ -1051,18 +1086,33 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
     constexpr bool DIRECT = L::DIRECT;
     constexpr int PL = L::PL, NT = L::NT, W = L::W, DT = L::DT, HALVES = L::HALVES;
     int head, tile;
-    head_and_tile((int)p.heads, (int)((d.Dv + W - 1) / W), head, tile);
-    const int64_t bh = head, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
+    head_and_tile((int)p.heads * p.segs, (int)((d.Dv + W - 1) / W), head, tile);
+    const int seg = head / (int)p.heads;
+    if (RUNS && seg == 0) return;                      // nothing comes before it
+    const int64_t bh = head % (int)p.heads, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, gq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave % HALVES, group = wave / HALVES;
     const int nb = tile * W, n0 = nb + 16 * group;
-    const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), chunks = (len + C - 1) / C;
+    const int Dk = (int)d.Dk, Dv = (int)d.Dv, len = length_of(a, b, d.T), all = (len + C - 1) / C;
+    const int first = seg * p.seg_chunks, chunks = all < first + p.seg_chunks ? all : first + p.seg_chunks;
     const bool mine = n0 + m < Dv;
     const int x0 = half * DT;
-    for (int64_t e = lane + 64 * half; e < (d.T - len) * 16; e += 64 * HALVES) {
-        const int64_t t = len + e / 16;
-        const int nn = n0 + (int)(e % 16);
-        if (nn < Dv) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t, h) + nn, 0.0f);
+    if (!RUNS) {                                       // rows of this segment behind the sequence's end
+        const int64_t past = len > (int64_t)first * C ? len : (int64_t)first * C;
+        const int64_t last_row = seg + 1 < p.segs ? (int64_t)(first + p.seg_chunks) * C : d.T;
+        for (int64_t e = lane + 64 * half; e < (last_row - past) * 16; e += 64 * HALVES) {
+            const int64_t t = past + e / 16;
+            const int nn = n0 + (int)(e % 16);
+            if (nn < Dv) put(static_cast<TS*>(a.dv) + at_row(d.dv, b, t, h) + nn, 0.0f);
+        }
+    }
+    const float* start = a.dhT ? a.dhT + bh * Dk * Dv : nullptr;       // [Dk][Dv], or of the workspace [dkp][dvp]
+    int start_row = Dv;
+    if (RUNS) {
+        start = nullptr;
+    } else if (seg + 1 < p.segs) {
+        start = reinterpret_cast<const float*>(ws + p.off_ends) + (seg * p.heads + bh) * DKP * p.dvp;
+        start_row = p.dvp;
     }
     f32x4 S[DT];
 #pragma unroll
@@ -1070,7 +1120,7 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int dd = row_of(x0 + x, 4 * gq) + j;
-            S[x][j] = a.dhT && dd < Dk && mine ? a.dhT[(bh * Dk + dd) * Dv + n0 + m] : 0.0f;
+            S[x][j] = start && dd < Dk && mine ? start[(int64_t)dd * start_row + n0 + m] : 0.0f;
         }
     const TS* const k_base = static_cast<const TS*>(a.k) + at_row(d.k, b, 0, hk);
     const TS* const q_base = static_cast<const TS*>(a.q) + at_row(d.q, b, 0, hk);
@@ -1140,11 +1190,11 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
             }
         }
     };
-    if (chunks > 0) {
+    if (first < chunks) {
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) fetch(part, chunks - 1);
     }
-    for (int n = chunks - 1; n >= 0; --n) {
+    for (int n = chunks - 1; n >= first; --n) {
         const int64_t ch = bh * p.chunks + n, t0 = (int64_t)n * C;
         const int rows = len - n * C;
         char* const buf = lds + (DIRECT ? (n & 1) * L::BUF : 0);
@@ -1159,21 +1209,23 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
         if constexpr (!L::MATS_DIRECT) cm.store(lds + L::G);
         if (!DIRECT) __syncthreads();
         auto ahead = [&](int part) {
-            if (part < PARTS && (!DIRECT || n > 0)) fetch(part, n > 0 ? n - 1 : 0);
+            if (part < PARTS && (!DIRECT || n > first)) fetch(part, n > first ? n - 1 : n);
         };
         ahead(0);
-        if (n + 1 < chunks) put_rows(n + 1);
+        if (!RUNS && n + 1 < chunks) put_rows(n + 1);
         const uint16_t* const K = reinterpret_cast<const uint16_t*>(buf + L::K);       // [PL][64][DKP]
         const uint16_t* const Q = reinterpret_cast<const uint16_t*>(buf + L::Q);
         const uint16_t* const Y = reinterpret_cast<const uint16_t*>(buf + L::V);       // [PL][64][W]: dY
         const float* const row = reinterpret_cast<const float*>(buf + L::FIELDS);
         const uint16_t* const G = reinterpret_cast<const uint16_t*>(lds + L::G + (n & 1) * L::G_BUF);  // [3][kTri]: G^T
         const uint16_t* const P = L::P_LDS ? G + 3 * kTri : reinterpret_cast<const uint16_t*>(mats_base + n * p.mats) + 3 * kTri;
-        float* const out_S = reinterpret_cast<float*>(ws + p.off_dS) + ch * DKP * p.dvp;
+        if (!RUNS) {
+            float* const out_S = reinterpret_cast<float*>(ws + p.off_dS) + ch * DKP * p.dvp;
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
+            for (int x = 0; x < DT; ++x)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) (out_S + row_of(x0 + x, j) * p.dvp)[s_off] = S[x][j];
+                for (int j = 0; j < 4; ++j) (out_S + row_of(x0 + x, j) * p.dvp)[s_off] = S[x][j];
+        }
         f32x4 fk[4], beta[4], tk[4], fq[4];            // the rows' factors, on their way meanwhile
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -1273,8 +1325,16 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
             KAN_FENCE();
         }
     }
-    if (chunks > 0) put_rows(0);
-    if (!a.dh0 || !mine) return;
+    if constexpr (RUNS) {
+        float* const out = reinterpret_cast<float*>(ws + p.off_ends) + (seg * p.heads + bh) * DKP * p.dvp + n0 + m;
+#pragma unroll
+        for (int x = 0; x < DT; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[(row_of(x0 + x, 4 * gq) + j) * p.dvp] = S[x][j];
+        return;
+    }
+    if (first < chunks) put_rows(first);
+    if (!a.dh0 || !mine || seg > 0) return;
 #pragma unroll
     for (int x = 0; x < DT; ++x)
 #pragma unroll
@@ -1282,6 +1342,78 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, kBack, EVEN>::NT))
             const int dd = row_of(x0 + x, 4 * gq) + j;
             if (dd < Dk) a.dh0[(bh * Dk + dd) * Dv + n0 + m] = S[x][j];
         }
+}
+
+// The segments' starts, forward: S_1 = B_0, S_{s + 1} = M_s S_s + B_s; or their ends,
+// BACK, in the place of F_s: dS_s = dhT for the last one, dS_{s - 1} = M_s^T dS_s + F_s.
+// A block has 16 columns of a head, a wave 16 rows of them; the state is in LDS, as
+// the right operand of the next product.
+template <int DKP, bool BACK>
+__global__ void __launch_bounds__(4 * DKP) delta_link_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+    constexpr int STEPS = DKP / 32;
+    __shared__ __align__(16) uint16_t S[2][3][16][DKP + 8];
+    const int64_t bh = blockIdx.x % (unsigned)p.heads;
+    const int n0 = (int)(blockIdx.x / (unsigned)p.heads) * 16, Dk = (int)d.Dk, Dv = (int)d.Dv;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4, row = 16 * wave + 4 * gq;
+    const int64_t state = (int64_t)DKP * p.dvp, run = (int64_t)DKP * (p.dvp + DKP), at = (int64_t)row * p.dvp + n0 + m;
+    const float* const runs = reinterpret_cast<const float*>(ws + p.off_runs);
+    float* const ends = reinterpret_cast<float*>(ws + p.off_ends);
+    float* const starts = reinterpret_cast<float*>(ws + p.off_starts);
+    f32x4 v, next = zero4();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (BACK) v[j] = a.dhT && row + j < Dk && n0 + m < Dv ? a.dhT[(bh * Dk + row + j) * Dv + n0 + m] : 0.0f;
+        else v[j] = runs[bh * run + (int64_t)(row + j) * (p.dvp + DKP) + n0 + m];
+        if (BACK) next[j] = ends[((p.segs - 1) * p.heads + bh) * state + at + (int64_t)j * p.dvp];
+    }
+    for (int k = 1; k < p.segs; ++k) {
+        // forward: v is the start of segment s = k; back: the end of segment s = segs - k, and next is F_s
+        const int s = BACK ? p.segs - k : k;
+        const float* const M = runs + (s * p.heads + bh) * run + p.dvp;
+        if (!BACK) {
+            float* const out = starts + (s * p.heads + bh) * state + at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[(int64_t)j * p.dvp] = v[j];
+            if (k + 1 == p.segs) return;
+            const float* const B = runs + (s * p.heads + bh) * run + (int64_t)row * (p.dvp + DKP) + n0 + m;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) next[j] = B[(int64_t)j * (p.dvp + DKP)];
+        }
+        bf16x8 planes[3];
+        split8<3>(v, zero4(), planes);
+#pragma unroll
+        for (int z = 0; z < 3; ++z) __builtin_memcpy(&S[k & 1][z][m][row], &planes[z], 8);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < STEPS; ++q) {
+            const int c = 32 * q + 8 * gq;
+            f32x4 lo, hi;
+            if (BACK) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    lo[j] = M[(int64_t)(c + j) * (p.dvp + DKP) + 16 * wave + m];
+                    hi[j] = M[(int64_t)(c + 4 + j) * (p.dvp + DKP) + 16 * wave + m];
+                }
+            } else {
+                lo = ld4(M + (int64_t)(16 * wave + m) * (p.dvp + DKP) + c);
+                hi = ld4(M + (int64_t)(16 * wave + m) * (p.dvp + DKP) + c + 4);
+            }
+            bf16x8 ma[3], sb[3];
+            split8<3>(lo, hi, ma);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) sb[z] = *reinterpret_cast<const bf16x8*>(&S[k & 1][z][m][c]);
+            mma<3, 3>(next, ma, sb);
+        }
+        v = next;
+        if (BACK) {                                    // this lane's values of F_{s - 1} make room for dS_{s - 1}
+            float* const out = ends + ((s - 1) * p.heads + bh) * state + at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (s > 1) next[j] = out[(int64_t)j * p.dvp];
+                out[(int64_t)j * p.dvp] = v[j];
+            }
+        }
+    }
 }
 
 // ---- gradients of a chunk's rows -----------------------------------------------------
@@ -1762,28 +1894,40 @@ hipError_t prep(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& 
                   (rows > pairs ? rows : pairs) + 4 * kFields * C, s, d, p, a, ws);
 }
 template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
-hipError_t scan_e(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+hipError_t scan_e(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, bool runs,
+                  hipStream_t s) {
     typedef Scan<TS, DKP, GROUPS, PASS, EVEN> L;
     static_assert(L::LDS <= 160 * 1024, "LDS of a compute unit");
-    const int64_t blocks = p.heads * ((d.Dv + L::W - 1) / L::W);
-    if constexpr (PASS == kBack)
-        return launch(delta_back_kernel<TS, DKP, GROUPS, EVEN>, blocks, L::NT, L::LDS, s, d, p, a, ws);
-    else
+    const int64_t tiles = (d.Dv + L::W - 1) / L::W + (PASS == kRuns ? (DKP + L::W - 1) / L::W : 0);
+    const int64_t blocks = p.heads * (PASS == kRuns ? p.runs : p.segs) * tiles;
+    if constexpr (PASS == kBack) {
+        if (runs) return launch(delta_back_kernel<TS, DKP, GROUPS, EVEN, true>, blocks, L::NT, L::LDS, s, d, p, a, ws);
+        return launch(delta_back_kernel<TS, DKP, GROUPS, EVEN, false>, blocks, L::NT, L::LDS, s, d, p, a, ws);
+    } else {
         return launch(delta_scan_kernel<TS, DKP, GROUPS, PASS, EVEN>, blocks, L::NT, L::LDS, s, d, p, a, ws);
+    }
+}
+template <int DKP, bool BACK>
+hipError_t link(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    return launch(delta_link_kernel<DKP, BACK>, p.heads * ((d.Dv + 15) / 16), 4 * DKP, 0, s, d, p, a, ws);
 }
 template <typename TS, int DKP, int PASS>
-hipError_t scan(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+hipError_t scan(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s,
+                bool runs = false) {
     // pieces of eight, on 16 bytes where they go to LDS directly
     auto direct = [](const void* at, const kan_heads_t& s) {
         return aligned(at, 16) && s.seq % 8 == 0 && s.row % 8 == 0 && s.head % 8 == 0;
     };
     bool even = d.Dk % 8 == 0 && d.Dv % 8 == 0;
     if (sizeof(TS) == 2)
-        even = even && direct(a.k, d.k) && (PASS == kStates || direct(a.q, d.q)) && (PASS == kBack || direct(a.v, d.v));
+        even = even && direct(a.k, d.k) && (PASS == kStates || PASS == kRuns || direct(a.q, d.q)) &&
+               (PASS == kBack || direct(a.v, d.v));
     constexpr int WIDE = sizeof(TS) == 4 && PASS == kBack ? 2 : 4;     // groups of 16 columns that LDS has room for
-    if (p.waves == 4 && WIDE == 4)
-        return even ? scan_e<TS, DKP, WIDE, PASS, true>(d, p, a, ws, s) : scan_e<TS, DKP, WIDE, PASS, false>(d, p, a, ws, s);
-    return even ? scan_e<TS, DKP, 2, PASS, true>(d, p, a, ws, s) : scan_e<TS, DKP, 2, PASS, false>(d, p, a, ws, s);
+    // cut sequences have too few heads for wide blocks
+    if constexpr (WIDE == 4 && PASS != kRuns)
+        if (p.groups == 4)
+            return even ? scan_e<TS, DKP, 4, PASS, true>(d, p, a, ws, runs, s) : scan_e<TS, DKP, 4, PASS, false>(d, p, a, ws, runs, s);
+    return even ? scan_e<TS, DKP, 2, PASS, true>(d, p, a, ws, runs, s) : scan_e<TS, DKP, 2, PASS, false>(d, p, a, ws, runs, s);
 }
 template <typename TS, int DKP>
 hipError_t grad(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
@@ -1792,22 +1936,31 @@ hipError_t grad(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& 
                            8 * C + 16;
     return launch(delta_grad_kernel<TS, DKP>, p.heads * p.chunks, GRAD_NT, lds, s, d, p, a, ws);
 }
+// The segments' starts, where sequences are cut.
+template <typename TS, int DKP>
+hipError_t starts(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
+    if (p.segs == 1) return hipSuccess;
+    const hipError_t e = scan<TS, DKP, kRuns>(d, p, a, ws, s);
+    return e != hipSuccess ? e : link<DKP, false>(d, p, a, ws, s);
+}
 template <typename TS, int DKP>
 hipError_t forward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    if (p.chunks > 0) {
-        const hipError_t e = prep<TS, DKP, false>(d, p, a, ws, s);
-        if (e != hipSuccess) return e;
-    }
-    return scan<TS, DKP, kForward>(d, p, a, ws, s);
+    hipError_t e = hipSuccess;
+    if (p.chunks > 0) e = prep<TS, DKP, false>(d, p, a, ws, s);
+    if (e == hipSuccess) e = starts<TS, DKP>(d, p, a, ws, s);
+    return e != hipSuccess ? e : scan<TS, DKP, kForward>(d, p, a, ws, s);
 }
 template <typename TS, int DKP>
 hipError_t backward(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    hipError_t e;
+    hipError_t e = hipSuccess;
     if (p.chunks > 0) {
-        if ((e = prep<TS, DKP, true>(d, p, a, ws, s)) != hipSuccess) return e;
-        if ((e = scan<TS, DKP, kStates>(d, p, a, ws, s)) != hipSuccess) return e;
+        e = prep<TS, DKP, true>(d, p, a, ws, s);
+        if (e == hipSuccess) e = starts<TS, DKP>(d, p, a, ws, s);
+        if (e == hipSuccess) e = scan<TS, DKP, kStates>(d, p, a, ws, s);
+        if (e == hipSuccess && p.segs > 1) e = scan<TS, DKP, kBack>(d, p, a, ws, s, true);
+        if (e == hipSuccess && p.segs > 1) e = link<DKP, true>(d, p, a, ws, s);
     }
-    e = scan<TS, DKP, kBack>(d, p, a, ws, s);
+    if (e == hipSuccess) e = scan<TS, DKP, kBack>(d, p, a, ws, s);
     if (e != hipSuccess || p.chunks == 0) return e;
     if ((e = grad<TS, DKP>(d, p, a, ws, s)) != hipSuccess || d.Hv == d.Hk) return e;
     const int64_t blocks = (d.B * d.T * d.Hk + NT / 64 - 1) / (NT / 64), x = std::min<int64_t>(blocks, 1 << 16);

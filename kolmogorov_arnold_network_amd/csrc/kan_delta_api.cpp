@@ -88,6 +88,36 @@ int join_check(const kan_join_desc_t* d) {
 
 }  // namespace
 
+// Whether sequences are cut.  Times in us, of a chunk of a block (a compute unit
+// has one at a time) and of what a cut costs once; a run goes through 32 columns of
+// the identity for every 32 keys beside those of the values.
+static void segments(const kan_delta_desc_t& d, bool back, DeltaPlan& p) {
+    const bool f32 = d.dtype == KAN_F32;
+    const double pass = f32 ? 5.6 : 4.0, run = f32 ? 4.6 : 3.4, states = f32 ? 4.6 : 4.2, grad = f32 ? 6.5 : 5.5;
+    const int64_t tiles = (d.Dv + 31) / 32, wide = tiles + p.dkp / 32;
+    auto rounds = [](int64_t blocks) { return (double)((blocks + 255) / 256); };
+    double least = 0.0;
+    p.segs = 1;
+    p.seg_chunks = (int)p.chunks;
+    for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+        const int64_t each = (p.chunks + want - 1) / want;
+        if (want > 1 && each < 4) break;
+        const int64_t segs = (p.chunks + each - 1) / std::max<int64_t>(each, 1), runs = segs - (back ? 0 : 1);
+        double t = each * rounds(p.heads * segs * tiles) * (back ? states + grad : pass);
+        if (segs > 1) {
+            t += each * rounds(p.heads * runs * wide) * run + 15.0 + 1.2 * segs;
+            if (back) t += each * rounds(p.heads * segs * tiles) * grad + 10.0 + 1.2 * segs;
+        }
+        if (want == 1 || t < least) {
+            least = t;
+            p.segs = (int)std::max<int64_t>(segs, 1);
+            p.runs = (int)runs;
+            p.seg_chunks = (int)each;
+        }
+    }
+    if (p.segs > 1) p.groups = 2;
+}
+
 int64_t join_max_rows(int64_t D) { return int64_t(1) << (D > 4096 ? 21 : D > 1024 ? 23 : 25); }
 
 DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass) {
@@ -97,7 +127,8 @@ DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass) {
     p.dvp = (int)round_up(d.Dv, 64);
     p.chunks = (d.T + kDeltaChunk - 1) / kDeltaChunk;
     p.heads = d.B * d.Hv;
-    p.waves = p.heads * ((d.Dv + 63) / 64) >= 256 ? 4 : 2;
+    p.groups = p.heads * ((d.Dv + 63) / 64) >= 256 ? 4 : 2;
+    segments(d, back, p);
     // three planes of a triangular matrix hold float32, two what y keeps in bfloat16
     p.mats = (back ? 9 : d.dtype == KAN_F32 ? 6 : 5) * int64_t(6 * 64 * 16);
     size_t off = 0;
@@ -117,6 +148,16 @@ DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass) {
             p.off_dq = take(kDeltaChunk * d.Dk * 4);
             p.off_dk = take(kDeltaChunk * d.Dk * 4);
         }
+    }
+    if (p.segs > 1) {
+        auto segs = [&](int64_t bytes) {
+            const size_t o = off;
+            off += (size_t)round_up(p.heads * p.segs * bytes, 256);
+            return o;
+        };
+        p.off_runs = segs((int64_t)p.dkp * (p.dvp + p.dkp) * 4);
+        p.off_starts = segs((int64_t)p.dkp * p.dvp * 4);
+        if (back) p.off_ends = segs((int64_t)p.dkp * p.dvp * 4);
     }
     p.ws = off;
     return p;
