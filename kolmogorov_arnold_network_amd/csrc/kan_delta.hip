@@ -1419,7 +1419,10 @@ __global__ void __launch_bounds__(4 * DKP) delta_link_kernel(kan_delta_desc_t d,
 // ---- gradients of a chunk's rows -----------------------------------------------------
 
 // A block has a chunk; wave w rows 16 w .. + 15, of which lane (gq, m) has row 16 w + m in
-// four columns 16 x + 4 gq .. of every tile x.
+// four columns 16 x + 4 gq .. of every tile x.  The products with the states come
+// first, 32 of their columns at a time through LDS, then those of the rows among
+// themselves, in the same place: with bfloat16 rows two blocks fit a compute unit
+// and hide each other's loads (GRAD_FIGURE).
 constexpr int GRAD_NT = 256, GS = 32;                // GS: state columns at a time
 template <int DKP>
 __device__ __forceinline__ int slice_at(int row, int c) { return row * GS + ((c ^ (row >> 2)) & 3) * 8; }
@@ -1454,22 +1457,26 @@ __device__ __forceinline__ f32x4 row_values(const uint16_t* lds, int row, int x,
 }
 
 template <typename TS, int DKP>
-__global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
+constexpr int grad_bytes() {                           // of the states' slices, or of the rows and their pairs
+    constexpr int states = 3 * GS * (2 * DKP + C) * 2, pairs = planes_of<TS>::n * C * 2 * DKP * 2 + 2 * C * LC * 4;
+    return states > pairs ? states : pairs;
+}
+template <typename TS, int DKP>
+__global__ void __launch_bounds__(GRAD_NT, sizeof(TS) == 2 ? 2 : 1) delta_grad_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
     extern __shared__ __align__(16) char lds[];
     constexpr int PL = planes_of<TS>::n, DT = DKP / 16, NT = GRAD_NT;
-    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
-    uint16_t* const Q = K + PL * C * DKP;
-    uint16_t* const S0 = Q + PL * C * DKP;                         // [3][DKP][32]
+    uint16_t* const S0 = reinterpret_cast<uint16_t*>(lds);         // [3][DKP][32]
     uint16_t* const S1 = S0 + 3 * DKP * GS;                        // [3][DKP][32]: dS
     uint16_t* const U = S1 + 3 * DKP * GS;                         // [3][64][32]: u
-    float* const PD = reinterpret_cast<float*>(S0);                // [64][LC]: scale dP D, in their place
+    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP], after the states
+    uint16_t* const Q = K + PL * C * DKP;
+    float* const PD = reinterpret_cast<float*>(Q + PL * C * DKP);  // [64][LC]: scale dP D; then dP P - X A
     float* const XD = PD + C * LC;                                 // X D
-    float* const E = XD + C * LC;                                  // dP P - X A, and its sums along rows
-    constexpr int STATES = 3 * GS * (2 * DKP + C) * 2, PAIRS = 3 * C * LC * 4;
-    float* const row = reinterpret_cast<float*>(reinterpret_cast<char*>(S0) + (STATES > PAIRS ? STATES : PAIRS));
+    float* const row = reinterpret_cast<float*>(lds + grad_bytes<TS, DKP>());
     float* const xs = row + kFields * C;                           // [64] parts of rows that come from S0
     float* const zs = xs + C;                                      // [64] parts of rows that reach dS1
-    float* const part = zs + C;                                    // [4] of <dS1, S0>
+    float* const sums = zs + C;                                    // [4][64] parts of dg
+    float* const part = sums + 4 * C;                              // [4] of <dS1, S0>
     const int64_t n = blockIdx.x % (unsigned)p.chunks, bh = blockIdx.x / (unsigned)p.chunks;
     const int64_t b = bh / d.Hv, h = bh % d.Hv, share = d.Hv / d.Hk, hk = h / share;
     const int64_t t0 = n * C, ch = bh * p.chunks + n;
@@ -1494,13 +1501,8 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
         return;
     }
     {
-        Carry<TS, DKP, NT, false> ck, cq;
         CarryBytes<kFields * C * 4, NT> cr;
-        ck.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
-        cq.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, Dk);
         cr.load(reinterpret_cast<const float*>(ws + p.off_rows) + ch * kFields * C);
-        ck.store(K, rows, Dk);
-        cq.store(Q, rows, Dk);
         cr.store(row);
     }
     const float* const in_S = reinterpret_cast<const float*>(ws + p.off_S) + ch * DKP * p.dvp;
@@ -1534,9 +1536,9 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
 #pragma unroll
         for (int z = 0; z < 2; ++z) wn[z] = ld4(in_w + at + 4 * z), rn[z] = ld4(in_r + at + 4 * z);
     };
-    fetch(0);
     const int steps = (Dv + GS - 1) / GS;
     for (int s = 0; s < steps; ++s) {
+        fetch(s);
         bf16x8 ya[PL], ua[3], va[3];
         piece_planes(py, ya);
 #pragma unroll
@@ -1563,7 +1565,6 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
 #pragma unroll
         for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(U + z * C * GS + slice_at<C>(im, gq)) = ua[z];
         __syncthreads();
-        if (s + 1 < steps) fetch(s + 1);
 #pragma unroll
         for (int x = 0; x < DT; ++x) {
             bf16x8 sb[3], db[3];
@@ -1592,6 +1593,14 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
     for (int o = 1; o < 64; o <<= 1) ss += __shfl_xor(ss, o, 64);
     if (lane == 0) part[wave] = ss;
     __syncthreads();                                   // the states' slices are done with
+    {
+        Carry<TS, DKP, NT, false> ck, cq;
+        ck.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, Dk);
+        cq.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, Dk);
+        ck.store(K, rows, Dk);
+        cq.store(Q, rows, Dk);
+    }
+    __syncthreads();
     // the states' parts, with their factors; gradients of q and k as they were divided
     const float from = __builtin_amdgcn_exp2f(row[kHi * C + im] + row[kLo * C + im]), to = decay(row, C - 1, im);
     const float nk = row[kNk * C + im], nq = row[kNq * C + im];
@@ -1630,22 +1639,22 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
             mma<PL, PL>(kk[x], kb, ka);
         }
     }
+    f32x4 e[4];                                        // dP P - X A
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int j0 = 16 * x + 4 * gq;
         const f32x4 nj = ld4(row + kNk * C + j0);
-        f32x4 pd, xd, e;
+        f32x4 pd, xd;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             const int j = j0 + y;
             const float D = j <= im ? decay(row, im, j) : 0.0f;
             pd[y] = j <= im ? d.scale * (dP[x][y] * D) : 0.0f;
             xd[y] = j < im ? X[x][y] * D : 0.0f;
-            e[y] = j < im ? nj[y] * (pd[y] * (nq * qk[x][y]) - xd[y] * (nk * kk[x][y])) : 0.0f;
+            e[x][y] = j < im ? nj[y] * (pd[y] * (nq * qk[x][y]) - xd[y] * (nk * kk[x][y])) : 0.0f;
         }
         st4(PD + im * LC + j0, pd);
         st4(XD + im * LC + j0, xd);
-        st4(E + im * LC + j0, e);
     }
     __syncthreads();
     // products of the pairs with the rows, which are divided here by their pair's factor
@@ -1683,21 +1692,37 @@ __global__ void __launch_bounds__(GRAD_NT) delta_grad_kernel(kan_delta_desc_t d,
             mma<PL, 3>(us[x], kt, xca);
         }
     }
-    // dg: sums of E along rows (wave 0, a row to a lane), then down the columns
-    if (wave == 0) {
-        float sum = 0.0f;
-        for (int j = 0; j < C; ++j) {
-            const float e = E[lane * LC + j];
-            E[lane * LC + j] = sum;                    // over the columns before j
-            sum += e;
-        }
-    }
+    // dg of row t, a lane each: pairs i >= t > j, of which a wave has 16 rows i, ...
     __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 4; ++x) st4(PD + im * LC + 16 * x + 4 * gq, e[x]);     // this wave's rows
+    float dg = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) {
+        const int i = 16 * wave + y;
+        float sum = PD[i * LC + lane];
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const float before = __shfl_up(sum, o, 64);
+            if (lane >= o) sum += before;
+        }
+        const float before = __shfl_up(sum, 1, 64);    // columns j < t
+        if (i >= lane && lane > 0) dg += before;
+    }
+    sums[wave * C + lane] = dg;
+    __syncthreads();
+    // ... rows i >= t that start from S0, rows j < t that reach dS1, and the state itself
     if (wave == 0) {
-        float dg = 0.0f;
-        for (int i = C - 1; i >= lane; --i) dg += E[i * LC + lane] + xs[i];
-        for (int j = 0; j < lane; ++j) dg += zs[j];
-        dg += whole_decay(row) * (part[0] + part[1] + part[2] + part[3]);
+        float x = xs[lane], z = zs[lane];
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const float after = __shfl_down(x, o, 64), before = __shfl_up(z, o, 64);
+            if (lane + o < 64) x += after;
+            if (lane >= o) z += before;
+        }
+        const float earlier = __shfl_up(z, 1, 64);
+        dg = ((sums[lane] + sums[C + lane]) + (sums[2 * C + lane] + sums[3 * C + lane])) + x + (lane > 0 ? earlier : 0.0f) +
+             whole_decay(row) * (part[0] + part[1] + part[2] + part[3]);
         if (lane < inside) a.dg[(b * d.T + t0 + lane) * d.Hv + h] = lane < rows ? dg : 0.0f;
     }
     if (im >= inside) return;
@@ -1931,9 +1956,7 @@ hipError_t scan(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& 
 }
 template <typename TS, int DKP>
 hipError_t grad(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    constexpr size_t states = 3 * GS * (2 * DKP + C) * 2, pairs = 3 * C * LC * 4;
-    constexpr size_t lds = planes_of<TS>::n * C * 2 * DKP * 2 + (states > pairs ? states : pairs) + 4 * kFields * C +
-                           8 * C + 16;
+    constexpr size_t lds = grad_bytes<TS, DKP>() + 4 * kFields * C + 24 * C + 16;
     return launch(delta_grad_kernel<TS, DKP>, p.heads * p.chunks, GRAD_NT, lds, s, d, p, a, ws);
 }
 // The segments' starts, where sequences are cut.
