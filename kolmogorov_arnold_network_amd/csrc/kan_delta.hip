@@ -291,7 +291,7 @@ struct Direct {
         for (int x = 0; x < N; ++x) {
             const int e = threadIdx.x + NT * x, i = e / CH, c = piece_at<W>(i, e % CH) / 8 % CH;
             off[x] = 2 * ((uint32_t)i * (uint32_t)row_stride + 8 * (uint32_t)c);
-            row[x] = 8 * c < D ? i : C;
+            row[x] = 8 * c < D ? i : INT32_MAX;
         }
     }
     __device__ __forceinline__ void load(int x, const uint16_t* base, int rows, char* lds) const {
@@ -387,7 +387,7 @@ __device__ __forceinline__ void mma_f32(f32x4& acc, const f32x4& a, const f32x4&
 
 // G in place of A (strictly lower, LDS pitch LC): G = A - A diag(beta) G.
 __device__ __forceinline__ void solve(float* A, const float* beta) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, gq = lane >> 4;
     // the diagonal blocks of 16, a wave each, column m to a lane ...
     {
         float h[16];                                   // beta_k G[k][m]
@@ -463,27 +463,77 @@ struct out_planes {
 };
 
 constexpr int PREP_NT = 256;
-// Chunk n of head h of sequence b: row fields, G and P (BWD: G and the transposes).
+template <typename TS, int DKP>
+constexpr int prep_bytes() {                           // of K, then of A and P in its place
+    constexpr int rows = 2 * planes_of<TS>::n * C * DKP, pairs = 8 * C * LC;
+    return rows > pairs ? rows : pairs;
+}
+// Chunk n of sequence b for the heads that share a key: row fields, G and P (BWD: G
+// and the transposes).  The products K K^T and Q K^T are the heads' own; rows of Q
+// are left operands straight from HBM.
 template <typename TS, int DKP, bool BWD>
 __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
     extern __shared__ __align__(16) char lds[];
-    constexpr int PL = planes_of<TS>::n;
-    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP], then A and P in their place
-    uint16_t* const Q = K + PL * C * DKP;
+    constexpr int PL = planes_of<TS>::n, STEPS = DKP / 32;
+    uint16_t* const K = reinterpret_cast<uint16_t*>(lds);          // [PL][64][DKP]
     float* const A = reinterpret_cast<float*>(lds);                // [64][LC], G in the end
     float* const P = A + C * LC;
-    constexpr int BODY = 4 * PL * C * DKP > 8 * C * LC ? 4 * PL * C * DKP : 8 * C * LC;
-    float* const row = reinterpret_cast<float*>(lds + BODY);       // [8][64]
-    const int64_t n = blockIdx.x % (unsigned)p.chunks, bh = blockIdx.x / (unsigned)p.chunks;
-    const int64_t b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
-    const int rows = length_of(a, b, d.T) - (int)n * C;
+    float* const row = reinterpret_cast<float*>(lds + prep_bytes<TS, DKP>());      // [8][64]
+    const int64_t n = blockIdx.x % (unsigned)p.chunks, bk = blockIdx.x / (unsigned)p.chunks;
+    const int64_t b = bk / d.Hk, hk = bk % d.Hk;
+    const int rows = length_of(a, b, d.T) - (int)n * C, share = (int)(d.Hv / d.Hk);
     if (rows <= 0) return;                             // uniform
-    const int64_t t0 = n * C, ch = bh * p.chunks + n;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int64_t t0 = n * C;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int im = 16 * wave + m, i0 = 16 * wave + 4 * gq;
+    const TS* const q = static_cast<const TS*>(a.q) + at_row(d.q, b, t0 + (im < rows ? im : 0), hk);
+    Piece<TS> qp[STEPS];
     {
-        Carry<TS, DKP, PREP_NT, false> k, q;
+        Carry<TS, DKP, PREP_NT, false> k;
         k.load(static_cast<const TS*>(a.k) + at_row(d.k, b, t0, hk), d.k.row, rows, (int)d.Dk);
-        q.load(static_cast<const TS*>(a.q) + at_row(d.q, b, t0, hk), d.q.row, rows, (int)d.Dk);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int at = 32 * s + 8 * gq;
+            if (im < rows && at < d.Dk) load_piece(qp[s], q, at, (int)d.Dk);
+            else no_piece(qp[s]);
+        }
+        k.store(K, rows, (int)d.Dk);
+    }
+    if (tid < C) row[kNk * C + tid] = row[kNq * C + tid] = 1.0f;
+    __syncthreads();
+    if (d.flags & KAN_DELTA_UNIT) {
+        unit_factors<PL, DKP, PREP_NT>(K, row + kNk * C);
+        float sq = 0.0f;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(piece_value(qp[s], j), piece_value(qp[s], j), sq);
+        sq += __shfl_xor(sq, 16, 64);
+        sq += __shfl_xor(sq, 32, 64);
+        if (gq == 0) row[kNq * C + im] = 1.0f / sqrtf(sq + kUnitEps);
+    }
+    // this wave's 16 rows of K K^T and Q K^T
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) kk[x] = qk[x] = zero4();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        bf16x8 ka[PL], qa[PL];
+        row_frag<PL, DKP>(K, im, 4 * s + gq, ka);
+        piece_planes(qp[s], qa);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (x > wave) break;
+            bf16x8 kb[PL];
+            row_frag<PL, DKP>(K, 16 * x + m, 4 * s + gq, kb);
+            mma<PL, PL>(kk[x], ka, kb);
+            mma<PL, PL>(qk[x], qa, kb);
+        }
+    }
+    __syncthreads();                                   // the unit factors are there
+#pragma unroll 1
+    for (int z = 0; z < share; ++z) {
+        const int64_t h = hk * share + z, bh = b * d.Hv + h, ch = bh * p.chunks + n;
         if (wave == 0) {
             float g = 0.0f, beta = 0.0f;
             if (lane < rows) {
@@ -498,75 +548,45 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
                 if (lane >= o) c += before;
             }
             const float hi = (float)c, lo = hi - hi == 0.0f ? (float)(c - (double)hi) : 0.0f;
+            const float from = __builtin_amdgcn_exp2f(hi + lo), nk = row[kNk * C + lane];
             row[kHi * C + lane] = hi;
             row[kLo * C + lane] = lo;
             row[kBeta * C + lane] = beta;
-            row[kNk * C + lane] = row[kNq * C + lane] = 1.0f;
-            row[kFk * C + lane] = __builtin_amdgcn_exp2f(hi + lo);
-            row[kTk * C + lane] = __builtin_amdgcn_exp2f((float)(__shfl(c, 63, 64) - c));
+            row[kFk * C + lane] = from * nk;
+            row[kTk * C + lane] = __builtin_amdgcn_exp2f((float)(__shfl(c, 63, 64) - c)) * nk;
+            row[kFq * C + lane] = from;
         }
-        k.store(K, rows, (int)d.Dk);
-        q.store(Q, rows, (int)d.Dk);
-    }
-    __syncthreads();
-    if (d.flags & KAN_DELTA_UNIT) {
-        unit_factors<PL, DKP, PREP_NT>(K, row + kNk * C);
-        unit_factors<PL, DKP, PREP_NT>(Q, row + kNq * C);
-    }
-    // this wave's 16 rows of K K^T and Q K^T
-    f32x4 kk[4], qk[4];
+        __syncthreads();                               // and K, or the matrices of the head before, are done with
+        {
+            const f32x4 hi = ld4(row + kHi * C + i0), lo = ld4(row + kLo * C + i0);
+            const f32x4 ni = ld4(row + kNk * C + i0), nq = d.scale * ld4(row + kNq * C + i0);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) kk[x] = qk[x] = zero4();
+            for (int x = 0; x < 4; ++x) {
+                if (x > (wave | 1)) break;             // blocks that no piece reaches
+                const int j = 16 * x + m;
+                const float nj = row[kNk * C + j], hj = row[kHi * C + j], lj = row[kLo * C + j];
 #pragma unroll
-    for (int s = 0; s < DKP / 32; ++s) {
-        bf16x8 ka[PL], qa[PL];
-        row_frag<PL, DKP>(K, 16 * wave + m, 4 * s + gq, ka);
-        row_frag<PL, DKP>(Q, 16 * wave + m, 4 * s + gq, qa);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (x > wave) break;
-            bf16x8 kb[PL];
-            row_frag<PL, DKP>(K, 16 * x + m, 4 * s + gq, kb);
-            mma<PL, PL>(kk[x], ka, kb);
-            mma<PL, PL>(qk[x], qa, kb);
-        }
-    }
-    __syncthreads();
-    {
-        const int i0 = 16 * wave + 4 * gq;
-        const f32x4 hi = ld4(row + kHi * C + i0), lo = ld4(row + kLo * C + i0);
-        const f32x4 ni = ld4(row + kNk * C + i0), nq = d.scale * ld4(row + kNq * C + i0);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (x > (wave | 1)) break;                 // blocks that no piece reaches
-            const int j = 16 * x + m;
-            const float nj = row[kNk * C + j], hj = row[kHi * C + j], lj = row[kLo * C + j];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int i = i0 + y;
-                const float D = nj * __builtin_amdgcn_exp2f((hi[y] - hj) + (lo[y] - lj));
-                A[i * LC + j] = j < i ? kk[x][y] * (D * ni[y]) : 0.0f;
-                P[i * LC + j] = j <= i ? qk[x][y] * (D * nq[y]) : 0.0f;
+                for (int y = 0; y < 4; ++y) {
+                    const int i = i0 + y;
+                    const float D = nj * __builtin_amdgcn_exp2f((hi[y] - hj) + (lo[y] - lj));
+                    A[i * LC + j] = j < i ? kk[x][y] * (D * ni[y]) : 0.0f;
+                    P[i * LC + j] = j <= i ? qk[x][y] * (D * nq[y]) : 0.0f;
+                }
             }
+            if (m == 0) st4(row + kFq * C + i0, ld4(row + kFq * C + i0) * nq);
         }
+        __syncthreads();
+        float* const out_row = reinterpret_cast<float*>(ws + p.off_rows) + ch * kFields * C;
+        for (int i = tid; i < kFields * C; i += PREP_NT) out_row[i] = row[i];
+        uint16_t* const mats = reinterpret_cast<uint16_t*>(ws + p.off_mats + ch * p.mats);
+        constexpr int NP = out_planes<TS>::n;
+        if (BWD) write_tri<3, true>(P, mats + 6 * kTri, PREP_NT);
+        else write_tri<NP, false>(P, mats + 3 * kTri, PREP_NT);
+        solve(A, row + kBeta * C);
+        write_tri<3, false>(A, mats, PREP_NT);
+        if (BWD) write_tri<3, true>(A, mats + 3 * kTri, PREP_NT);
+        if (z + 1 < share) __syncthreads();            // the rows' fields are done with
     }
-    __syncthreads();
-    if (tid < C) {
-        const float from = row[kFk * C + tid];
-        row[kFk * C + tid] = from * row[kNk * C + tid];
-        row[kTk * C + tid] *= row[kNk * C + tid];
-        row[kFq * C + tid] = d.scale * from * row[kNq * C + tid];
-    }
-    __syncthreads();
-    float* const out_row = reinterpret_cast<float*>(ws + p.off_rows) + ch * kFields * C;
-    for (int i = tid; i < kFields * C; i += PREP_NT) out_row[i] = row[i];
-    uint16_t* const mats = reinterpret_cast<uint16_t*>(ws + p.off_mats + ch * p.mats);
-    constexpr int NP = out_planes<TS>::n;
-    if (BWD) write_tri<3, true>(P, mats + 6 * kTri, PREP_NT);
-    else write_tri<NP, false>(P, mats + 3 * kTri, PREP_NT);
-    solve(A, row + kBeta * C);
-    write_tri<3, false>(A, mats, PREP_NT);
-    if (BWD) write_tri<3, true>(A, mats + 3 * kTri, PREP_NT);
 }
 
 // ---- along a sequence -------------------------------------------------------------
@@ -1482,7 +1502,7 @@ __global__ void __launch_bounds__(GRAD_NT, sizeof(TS) == 2 ? 2 : 1) delta_grad_k
     const int64_t t0 = n * C, ch = bh * p.chunks + n;
     const int Dk = (int)d.Dk, Dv = (int)d.Dv;
     const int rows = length_of(a, b, d.T) - (int)t0;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, gq = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, gq = lane >> 4;
     const int inside = (int)(d.T - t0 < C ? d.T - t0 : C);         // rows of the chunk that the arrays have
     const int im = 16 * wave + m;                                  // this lane's row
     TS* const dq = static_cast<TS*>(a.dq) + at_row(d.dq, b, t0 + im, hk);
@@ -1914,9 +1934,8 @@ hipError_t launch(K kernel, int64_t blocks, int threads, size_t lds, hipStream_t
 
 template <typename TS, int DKP, bool BWD>
 hipError_t prep(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, hipStream_t s) {
-    constexpr size_t rows = 4 * planes_of<TS>::n * C * DKP, pairs = 8 * C * LC;
-    return launch(delta_prep_kernel<TS, DKP, BWD>, p.heads * p.chunks, PREP_NT,
-                  (rows > pairs ? rows : pairs) + 4 * kFields * C, s, d, p, a, ws);
+    return launch(delta_prep_kernel<TS, DKP, BWD>, d.B * d.Hk * p.chunks, PREP_NT, prep_bytes<TS, DKP>() + 4 * kFields * C,
+                  s, d, p, a, ws);
 }
 template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
 hipError_t scan_e(const kan_delta_desc_t& d, const DeltaPlan& p, const DeltaArgs& a, char* ws, bool runs,
