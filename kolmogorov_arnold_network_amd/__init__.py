@@ -8,7 +8,9 @@ does the grouped (per-channel) spline activation ``y[b, i] = phi_{g(i)}(x[b, i])
 and its backward, and the 2-D tensor-product spline layer over pairs of
 inputs.  Around the layers, for models over tokens: an embedding with its
 gradient by sorted tokens, a gated linear recurrence over the rows of a
-sequence, and distillation from a teacher's top logits.  This
+sequence, distillation from a teacher's top logits, the gated delta rule (a
+mixer with a matrix state for each head), and the join between two blocks (norms,
+gate and residual in one pass).  This
 package binds that ABI (``functional``) and wraps it as torch modules
 (``modules``).
 """
@@ -27,7 +29,8 @@ from .functional import (kan_forward, kan_forward_static, kan_backward, kan_prep
                          kan_join_forward, kan_join_backward, kan_join_workspace_size, join_desc)
 from .modules import (KANLayer, KANNetwork, KANFunction, KANGroupedActivation, KANSurfaceLayer,
                       GroupedFunction, SurfaceFunction, KANEmbedding, KANRecurrence, KANDistillLoss,
-                      EmbedFunction, RecurFunction, DistillFunction)
+                      EmbedFunction, RecurFunction, DistillFunction, KANDeltaRule, KANJoin, DeltaFunction,
+                      JoinFunction)
 
 __all__ = ["kan_forward", "kan_forward_static", "kan_backward", "kan_prepare", "kan_basis_eval", "kan_basis_eval_tp",
            "kan_cast_f32_to_bf16",
@@ -41,4 +44,5 @@ __all__ = ["kan_forward", "kan_forward_static", "kan_backward", "kan_prepare", "
            "kan_delta_forward", "kan_delta_backward", "kan_delta_step", "kan_delta_workspace_size", "delta_desc",
            "kan_join_forward", "kan_join_backward", "kan_join_workspace_size", "join_desc",
            "KANGroupedActivation", "KANSurfaceLayer", "GroupedFunction", "SurfaceFunction",
-           "KANEmbedding", "KANRecurrence", "KANDistillLoss", "EmbedFunction", "RecurFunction", "DistillFunction"]
+           "KANEmbedding", "KANRecurrence", "KANDistillLoss", "EmbedFunction", "RecurFunction", "DistillFunction",
+           "KANDeltaRule", "KANJoin", "DeltaFunction", "JoinFunction"]

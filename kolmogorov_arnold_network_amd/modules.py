@@ -377,3 +377,146 @@ class KANDistillLoss(torch.nn.Module):
 
     def extra_repr(self):
         return "temperature=%g, reduction=%s" % (self.temperature, self.reduction)
+
+
+class DeltaFunction(torch.autograd.Function):
+    """The gated delta rule over ``p [B, T, 2 Hk Dk + Hv Dv]``, whose slices are q, k and v."""
+
+    @staticmethod
+    def _slices(p, Hk, Dk, Hv, Dv):
+        n = Hk * Dk
+        return (p[..., :n].unflatten(-1, (Hk, Dk)), p[..., n:2 * n].unflatten(-1, (Hk, Dk)),
+                p[..., 2 * n:].unflatten(-1, (Hv, Dv)))
+
+    @staticmethod
+    def forward(ctx, p, g, beta, h0, lengths, heads):
+        y, hT = F.kan_delta_forward(*DeltaFunction._slices(p, *heads), g, beta, h0, lengths, unit=True)
+        ctx.heads = heads
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(p, g, beta, h0, lengths)
+        return y, hT
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dhT):
+        p, g, beta, h0, lengths = ctx.saved_tensors
+        Hk, Dk, Hv, Dv = ctx.heads
+        dy = p.new_zeros((*p.shape[:2], Hv, Dv)) if dy is None else dy.contiguous()
+        dp = torch.empty(p.shape, dtype=p.dtype, device=p.device)
+        dq, dk, dv = DeltaFunction._slices(dp, *ctx.heads)
+        _, _, _, dg, dbeta, dh0 = F.kan_delta_backward(
+            *DeltaFunction._slices(p, *ctx.heads), g, beta, dy, h0, lengths, None if dhT is None else dhT.contiguous(),
+            unit=True, need_dh0=ctx.needs_input_grad[3], dq=dq, dk=dk, dv=dv)
+        return dp, dg, dbeta, dh0, None, None
+
+
+class KANDeltaRule(torch.nn.Module):
+    """Mixes the rows of a sequence by the gated delta rule: a ``KANLayer`` makes
+    queries and keys of ``key_heads`` heads and values of ``heads`` heads of every row, a
+    second one a decay and a rate for each of ``heads`` heads, both through a sigmoid.
+    Each head keeps a state ``[key_features, value_features]`` that answers keys with
+    values; queries and keys are unit vectors.
+
+    ``forward(x [B, T, in], h0 [B, heads, key_features, value_features], lengths [B])`` returns
+    the rows ``[B, T, heads * value_features]`` and the last states, float32;
+    ``step(x [B, in], state [S, heads, key_features, value_features], slots [B])`` takes one row
+    of each of B sequences and replaces their states in the pool.  The decays start
+    near ``sigmoid(gate_offset)``."""
+
+    def __init__(self, in_features, heads, key_features, value_features, key_heads=None, gate_offset=4.0, **kw):
+        super().__init__()
+        self.in_features = int(in_features)
+        self.heads = int(heads)
+        self.key_heads = int(heads if key_heads is None else key_heads)
+        self.key_features, self.value_features = int(key_features), int(value_features)
+        if self.heads % self.key_heads:
+            raise ValueError("heads must be a multiple of key_heads")
+        self.gate_offset = float(gate_offset)
+        self.layer = KANLayer(in_features, 2 * self.key_heads * self.key_features + self.heads * self.value_features, **kw)
+        self.gates = KANLayer(in_features, 2 * self.heads, **kw)
+
+    def _shape(self):
+        return self.key_heads, self.key_features, self.heads, self.value_features
+
+    def _gates(self, x):
+        a, b = self.gates(x).split(self.heads, -1)
+        return torch.nn.functional.logsigmoid(a + self.gate_offset), torch.sigmoid(b)
+
+    def forward(self, x, h0=None, lengths=None):
+        g, beta = self._gates(x)
+        y, hT = DeltaFunction.apply(self.layer(x), g, beta, None if h0 is None else h0.contiguous(),
+                                    None if lengths is None else lengths.contiguous(), self._shape())
+        return y.flatten(2), hT
+
+    @torch.no_grad()
+    def step(self, x, state, slots=None):
+        g, beta = self._gates(x)
+        q, k, v = DeltaFunction._slices(self.layer(x), *self._shape())
+        return F.kan_delta_step(q, k, v, g, beta, state, None if slots is None else slots.contiguous(),
+                                unit=True).flatten(1)
+
+    def extra_repr(self):
+        return "in=%d, heads=%d (keys %d), key_features=%d, value_features=%d" % (
+            self.in_features, self.heads, self.key_heads, self.key_features, self.value_features)
+
+
+class JoinFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, r, gate, w_post, w_pre, post, pre, activation, scale, eps, row_dtype):
+        y, x, stats = F.kan_join_forward(h, r, gate, w_post, w_pre, post, pre, activation, scale, eps, None, row_dtype)
+        ctx.kw = dict(post=post, activation=activation, scale=scale)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, gate, w_post, w_pre, y, stats)
+        return y, x
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dx):
+        h, gate, w_post, w_pre, y, stats = ctx.saved_tensors
+        dh, dr, dgate, dw_post, dw_pre = F.kan_join_backward(
+            h, y, stats, None if dy is None else dy.contiguous(), None if dx is None else dx.contiguous(), gate, w_post,
+            None if dx is None else w_pre, need_dr=ctx.needs_input_grad[1], **ctx.kw)
+        return (dh, dr, dgate, dw_post, dw_pre) + (None,) * 6
+
+
+class KANJoin(torch.nn.Module):
+    """What stands between two blocks: the norm of the block's output (``post``), its
+    gate, its scale, the residual sum, and the norm of the sum for the next block
+    (``pre``), in one pass over the rows:
+
+        y = residual + scale * act(gate) * w_post * norm(h),   x = w_pre * norm(y)
+
+    ``forward(h [..., D], residual, gate)`` returns ``(y, x)``, or y alone without
+    ``pre``; residual and gate may be None.  ``y`` has the residual's dtype (or h's), x
+    ``row_dtype`` (default h's).  With ``pre=False`` and neither residual nor gate it is a
+    norm.  Parameters ``w_post`` and ``w_pre [D]`` float32, ones at the start."""
+
+    def __init__(self, features, post=True, pre=True, activation="silu", scale=1.0, eps=1e-6, row_dtype=None,
+                 device=None):
+        super().__init__()
+        if activation not in ("silu", "sigmoid"):
+            raise ValueError("activation must be silu or sigmoid")
+        self.features, self.post, self.pre = int(features), bool(post), bool(pre)
+        self.activation, self.scale, self.eps, self.row_dtype = activation, float(scale), float(eps), row_dtype
+        self.w_post = torch.nn.Parameter(torch.ones(features, device=device))
+        self.w_pre = torch.nn.Parameter(torch.ones(features, device=device)) if pre else None
+
+    def forward(self, h, residual=None, gate=None):
+        for name, t in (("residual", residual), ("gate", gate)):
+            if t is not None and t.shape != h.shape:
+                raise ValueError("%s must be %s, got %s" % (name, tuple(h.shape), tuple(t.shape)))
+
+        def rows(t):
+            if t is None:
+                return None
+            t = t.reshape(-1, self.features)
+            return t if t.shape[1] == 1 or t.stride(1) == 1 else t.contiguous()
+
+        y, x = JoinFunction.apply(rows(h), rows(residual), rows(gate), self.w_post, self.w_pre, self.post, self.pre,
+                                  self.activation, self.scale, self.eps, self.row_dtype)
+        y = y.reshape(h.shape)
+        return (y, x.reshape(h.shape)) if self.pre else y
+
+    def extra_repr(self):
+        return "features=%d, post=%s, pre=%s, activation=%s, scale=%g" % (
+            self.features, self.post, self.pre, self.activation, self.scale)

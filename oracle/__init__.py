@@ -20,8 +20,8 @@ Contents
 
 Every function of the layers cites the passage of the pages it follows.
 Pinned by the ``-m "not gpu"`` tests in ``tests/test_oracle.py``,
-``test_oracle_grouped.py``, ``test_oracle_surface.py`` and
-``test_oracle_token.py``; there is no function here whose parity is
+``test_oracle_grouped.py``, ``test_oracle_surface.py``,
+``test_oracle_token.py`` and ``test_oracle_delta.py``; there is no function here whose parity is
 unpinned.
 """
 
