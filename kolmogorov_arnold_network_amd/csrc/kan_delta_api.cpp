@@ -27,6 +27,7 @@ bool distinct(int64_t B, int64_t T, int64_t H, int64_t D, const kan_heads_t& s) 
     struct Dim {
         int64_t n, stride;
     } dims[3] = {{B, s.seq}, {T, s.row}, {H, s.head}};
+    if (B == 0 || T == 0) return true;
     std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
     __int128 inner = D;
     for (const Dim& m : dims) {
