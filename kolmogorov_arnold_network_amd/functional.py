@@ -924,8 +924,10 @@ def kan_join_backward(h, y, stats, dy=None, dx=None, gate=None, w_post=None, w_p
         _whole(dx, "dx", _DTYPES, dev, shape)
     elif w_pre is not None:
         raise ValueError("w_pre has a gradient through x alone: give dx")
-    at = [_addr(t) for t in (y, stats, dy, dx, w_post, w_pre)]
-    if any((p or 0) & 15 for p in at) or dev != _current():
+    at, bits = [_addr(t) for t in (y, stats, dy, dx, w_post, w_pre)], 0
+    for address in at:
+        bits |= address or 0
+    if bits & 15 or dev != _current():
         with torch.cuda.device(dev):
             return kan_join_backward(h, *(_placed(t) for t in (y, stats, dy, dx)), gate, _placed(w_post),
                                      _placed(w_pre), post, activation, scale, need_dr, ws)
