@@ -47,8 +47,10 @@ hipError_t launch_delta_step(const kan_delta_desc_t& d, int64_t S, const DeltaAr
 constexpr int64_t kJoinMaxD = 8192;
 int64_t join_max_rows(int64_t D);
 constexpr int kJoinMaxBlocks = 1024; // blocks of a backward pass, each with its own sums for the weights
+constexpr int kJoinRows = 4;         // of up to 256 columns that a thread has at a time, where there are many
 struct JoinPlan {
     int lanes, vecs;                 // threads of a row, and vectors of four elements that each holds
+    int rows;                        // that a thread has at a time (forward)
     unsigned blocks;
     size_t ws;                       // [blocks][2][D] float32 sums of the weights' gradients (backward)
 };

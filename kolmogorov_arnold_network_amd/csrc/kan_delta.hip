@@ -328,7 +328,8 @@ __device__ __forceinline__ int64_t at_row(const kan_heads_t& s, int64_t b, int64
 }
 // Head and column tile of a scan's block: a head's blocks read the same rows, so
 // they go to one XCD (blocks are dealt to the eight of them in turn) and its L2
-// (8 x 4096 x 16 x 128 bf16: MEASURE_XCD).
+// (the backward scan of 4 x 4096 x 16 x 128 bf16 took 970 us without this and
+// 835 with it; the forward of 8 x 4096, 460 either way).
 __device__ __forceinline__ void head_and_tile(int heads, int tiles, int& head, int& tile) {
     const int group = (int)blockIdx.x / (8 * tiles), at = (int)blockIdx.x % (8 * tiles);
     const int n = heads - 8 * group < 8 ? heads - 8 * group : 8;
@@ -1442,7 +1443,7 @@ __global__ void __launch_bounds__(4 * DKP) delta_link_kernel(kan_delta_desc_t d,
 // four columns 16 x + 4 gq .. of every tile x.  The products with the states come
 // first, 32 of their columns at a time through LDS, then those of the rows among
 // themselves, in the same place: with bfloat16 rows two blocks fit a compute unit
-// and hide each other's loads (GRAD_FIGURE).
+// and hide each other's loads (4 x 4096 x 16 x 128 bf16: 552 us with one, 323 with two).
 constexpr int GRAD_NT = 256, GS = 32;                // GS: state columns at a time
 template <int DKP>
 __device__ __forceinline__ int slice_at(int row, int c) { return row * GS + ((c ^ (row >> 2)) & 3) * 8; }

@@ -10,9 +10,11 @@
 //     dh = n1 (w_post e - t mean(w_post e t)),  dw_post = sum e t,  dw_pre = sum dx z.
 //
 // Each array is read and written once: HBM traffic bounds it.  A row is held in
-// the registers of 32 to 1024 threads between its two norms.  In the backward
+// the registers of 32 to 1024 threads between its two norms (32768 x 2048 with a
+// float32 residual, bf16 else: 144 us, 5.6 TB/s).  In the backward
 // pass a block goes through rows of its own and keeps its sums for the weights in
-// registers; a second launch adds the blocks' sums in order.
+// registers; a second launch adds the blocks' sums in order (32768 x 2048 float32:
+// 426 us, 5.0 TB/s).
 #include "kan_delta.h"
 #include "kan_vec.h"
 
@@ -70,60 +72,87 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
     return v;
 }
 
-// act(g) and act'(g), from the smaller of the two shares.
+// act(g) and act'(g), from the smaller of the two shares.  exp by v_exp_f32 on |g| log2(e), whose
+// rounding is off by |g| 2^-24 of the result as expf's argument is; the reciprocal is within 2^-23.
+// With expf and a division a narrow row's arithmetic takes longer than its bytes (524288 x 128
+// bf16 forward 124 us, 100 so).
 __device__ __forceinline__ void activation(int kind, float g, float& a, float& slope) {
-    const float e = expf(-fabsf(g)), big = 1.0f / (1.0f + e), small = e * big;
+    const float e = __builtin_amdgcn_exp2f(fabsf(g) * -1.44269504f), big = __builtin_amdgcn_rcpf(1.0f + e),
+                small = e * big;
     const float s = g >= 0.0f ? big : small, o = g >= 0.0f ? small : big;      // a NaN is in both
     a = kind == KAN_GATE_SIGMOID ? s : g * s;
     slope = kind == KAN_GATE_SIGMOID ? s * o : s + g * s * o;
 }
+// 1 / sqrt(sum / D + eps): v_rsq_f32 (2^-23) where its argument is no subnormal number.
+__device__ __forceinline__ float factor(float sum, float per, float eps) {
+    const float v = __builtin_fmaf(sum, per, eps);
+    return v >= 0x1p-120f ? __builtin_amdgcn_rsqf(v) : 1.0f / sqrtf(v);
+}
 
-template <typename TH, typename TR, typename TX, int L, int NVEC, int NT>
+// U rows at a time of each thread's: narrow rows give a wave little to wait for, and a
+// block as much work to start as to do (524288 x 128 bf16 with gate and residual:
+// 117 us with one row, 100 with four).
+template <typename TH, typename TR, typename TX, int L, int NVEC, int NT, int U>
 __global__ void __launch_bounds__(NT) join_fwd_kernel(kan_join_desc_t d, JoinArgs a) {
     __shared__ float slots[2][NT / 64];
-    const int64_t row = (int64_t)blockIdx.x * (NT / L) + threadIdx.x / L;
     const int lane = threadIdx.x % L, D = (int)d.D;
-    if (L <= 64 && row >= d.N) return;                 // L > 64: a row to a block
-    float h[NVEC][VE], w[NVEC][VE], y[NVEC][VE], g[NVEC][VE];
-    load_row<TH, NVEC, L>(static_cast<const TH*>(a.h) + row * d.h_row, lane, D, h);
-    if (a.gate) load_row<TH, NVEC, L>(static_cast<const TH*>(a.gate) + row * d.gate_row, lane, D, g);
-    if (a.r) load_row<TR, NVEC, L>(static_cast<const TR*>(a.r) + row * d.r_row, lane, D, y);
+    const float per = 1.0f / (float)D;
+    const int64_t first = (int64_t)blockIdx.x * U * (NT / L) + threadIdx.x / L;
+    if (L <= 64 && first >= d.N) return;               // L > 64: a row to a block
+    float h[U][NVEC][VE], w[NVEC][VE], y[U][NVEC][VE], g[U][NVEC][VE], n1[U], s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        int64_t row = first + u * (NT / L);
+        if (U > 1 && row >= d.N) row = first;          // read again and not stored
+        load_row<TH, NVEC, L>(static_cast<const TH*>(a.h) + row * d.h_row, lane, D, h[u]);
+        if (a.gate) load_row<TH, NVEC, L>(static_cast<const TH*>(a.gate) + row * d.gate_row, lane, D, g[u]);
+        if (a.r) load_row<TR, NVEC, L>(static_cast<const TR*>(a.r) + row * d.r_row, lane, D, y[u]);
+    }
     if (a.w_post) load_row<float, NVEC, L>(a.w_post, lane, D, w);
-    float n1 = 1.0f, n2 = 1.0f;
-    if (d.flags & KAN_JOIN_POST) {
-        float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NVEC; ++i)
+    for (int u = 0; u < U; ++u) {
+        n1[u] = 1.0f;
+        if (d.flags & KAN_JOIN_POST) {
+            float q = 0.0f;
 #pragma unroll
-            for (int j = 0; j < VE; ++j) s = __builtin_fmaf(h[i][j], h[i][j], s);
-        n1 = 1.0f / sqrtf(row_sum<L>(s, slots[0]) / (float)D + d.eps);
-    }
-    float s = 0.0f;
+            for (int i = 0; i < NVEC; ++i)
 #pragma unroll
-    for (int i = 0; i < NVEC; ++i)
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            float p = h[i][j] * n1;
-            if (a.w_post) p *= w[i][j];
-            if (a.gate) {
-                float act, slope;
-                activation(d.activation, g[i][j], act, slope);
-                p *= act;
-            }
-            y[i][j] = a.r ? __builtin_fmaf(d.scale, p, y[i][j]) : d.scale * p;
-            s = __builtin_fmaf(y[i][j], y[i][j], s);
+                for (int j = 0; j < VE; ++j) q = __builtin_fmaf(h[u][i][j], h[u][i][j], q);
+            n1[u] = factor(row_sum<L>(q, slots[0]), per, d.eps);
         }
-    store_row<TR, NVEC, L>(static_cast<TR*>(a.y) + row * d.D, lane, D, y);
-    if (d.flags & KAN_JOIN_PRE) {
-        if (a.w_pre) load_row<float, NVEC, L>(a.w_pre, lane, D, w);
-        n2 = 1.0f / sqrtf(row_sum<L>(s, slots[1]) / (float)D + d.eps);
+        s[u] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NVEC; ++i)
 #pragma unroll
-            for (int j = 0; j < VE; ++j) y[i][j] *= a.w_pre ? n2 * w[i][j] : n2;
-        store_row<TX, NVEC, L>(static_cast<TX*>(a.x) + row * d.D, lane, D, y);
+            for (int j = 0; j < VE; ++j) {
+                float p = h[u][i][j] * n1[u];
+                if (a.w_post) p *= w[i][j];
+                if (a.gate) {
+                    float act, slope;
+                    activation(d.activation, g[u][i][j], act, slope);
+                    p *= act;
+                }
+                y[u][i][j] = a.r ? __builtin_fmaf(d.scale, p, y[u][i][j]) : d.scale * p;
+                s[u] = __builtin_fmaf(y[u][i][j], y[u][i][j], s[u]);
+            }
+        const int64_t row = first + u * (NT / L);
+        if (U == 1 || row < d.N) store_row<TR, NVEC, L>(static_cast<TR*>(a.y) + row * d.D, lane, D, y[u]);
     }
-    if (lane == 0) a.stats[row] = n1, a.stats[d.N + row] = n2;
+    if ((d.flags & KAN_JOIN_PRE) && a.w_pre) load_row<float, NVEC, L>(a.w_pre, lane, D, w);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = first + u * (NT / L);
+        float n2 = 1.0f;
+        if (d.flags & KAN_JOIN_PRE) {
+            n2 = factor(row_sum<L>(s[u], slots[1]), per, d.eps);
+#pragma unroll
+            for (int i = 0; i < NVEC; ++i)
+#pragma unroll
+                for (int j = 0; j < VE; ++j) y[u][i][j] *= a.w_pre ? n2 * w[i][j] : n2;
+            if (U == 1 || row < d.N) store_row<TX, NVEC, L>(static_cast<TX*>(a.x) + row * d.D, lane, D, y[u]);
+        }
+        if (lane == 0 && (U == 1 || row < d.N)) a.stats[row] = n1[u], a.stats[d.N + row] = n2;
+    }
 }
 
 // Block k has rows k R, k R + 1, .. of every `gridDim.x` R, R = NT / L rows at a time.
@@ -132,6 +161,7 @@ __global__ void __launch_bounds__(NT) join_bwd_kernel(kan_join_desc_t d, JoinArg
     __shared__ float slots[4][NT / 64];
     constexpr int R = NT / L;
     const int lane = threadIdx.x % L, D = (int)d.D;
+    const float per = 1.0f / (float)D;
     float wq[NVEC][VE], wp[NVEC][VE], sum_post[NVEC][VE], sum_pre[NVEC][VE];
     if (a.w_post) load_row<float, NVEC, L>(a.w_post, lane, D, wq);
     if (a.w_pre) load_row<float, NVEC, L>(a.w_pre, lane, D, wp);
@@ -168,7 +198,7 @@ __global__ void __launch_bounds__(NT) join_bwd_kernel(kan_join_desc_t d, JoinArg
                     if (a.w_pre) x[i][j] *= wp[i][j];  // c
                     cz = __builtin_fmaf(x[i][j], y[i][j], cz);
                 }
-            cz = row_sum<L>(cz, slots[odd]) / (float)D;
+            cz = row_sum<L>(cz, slots[odd]) * per;
 #pragma unroll
             for (int i = 0; i < NVEC; ++i)
 #pragma unroll
@@ -195,7 +225,7 @@ __global__ void __launch_bounds__(NT) join_bwd_kernel(kan_join_desc_t d, JoinArg
             }
         if (a.gate && a.dgate) store_row<TH, NVEC, L>(static_cast<TH*>(a.dgate) + row * d.D, lane, D, g);
         if (d.flags & KAN_JOIN_POST) {
-            et = row_sum<L>(et, slots[odd + 1]) / (float)D;
+            et = row_sum<L>(et, slots[odd + 1]) * per;
 #pragma unroll
             for (int i = 0; i < NVEC; ++i)
 #pragma unroll
@@ -230,7 +260,9 @@ __global__ void __launch_bounds__(NT) join_bwd_kernel(kan_join_desc_t d, JoinArg
     }
 }
 
-// Sums of the blocks' sums: 64 columns to a block, 16 blocks' worth at a time.
+// Sums of the blocks' sums: 64 columns to a block, 16 blocks' worth at a time and
+// eight such loads on their way (one after the other: 24 us for 1024 blocks of
+// 2048 columns, 9 so).
 __global__ void __launch_bounds__(1024) join_sum_kernel(const float* part, int64_t D, int blocks, float* dw_post,
                                                         float* dw_pre) {
     __shared__ float sums[16][64];
@@ -238,7 +270,13 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const float* part, int64
     const int64_t at = (int64_t)blockIdx.x * 64 + lane;        // of both sums, one after the other
     float v = 0.0f;
     if (at < 2 * D)
-        for (int k = wave; k < blocks; k += 16) v += part[(int64_t)k * 2 * D + at];
+        for (int k = wave; k < blocks; k += 16 * 8) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = k + 16 * i < blocks ? part[(int64_t)(k + 16 * i) * 2 * D + at] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += t[i];
+        }
     sums[wave][lane] = v;
     __syncthreads();
     if (wave != 0 || at >= 2 * D) return;
@@ -254,7 +292,11 @@ __global__ void __launch_bounds__(1024) join_sum_kernel(const float* part, int64
 
 template <typename TH, typename TR, typename TX, int L, int NVEC, int NT>
 hipError_t fwd(const kan_join_desc_t& d, const JoinPlan& p, const JoinArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((join_fwd_kernel<TH, TR, TX, L, NVEC, NT>), dim3(p.blocks), dim3(NT), 0, s, d, a);
+    constexpr int U = NVEC == 1 ? kJoinRows : 1;
+    if (U > 1 && p.rows > 1)
+        hipLaunchKernelGGL((join_fwd_kernel<TH, TR, TX, L, NVEC, NT, U>), dim3(p.blocks), dim3(NT), 0, s, d, a);
+    else
+        hipLaunchKernelGGL((join_fwd_kernel<TH, TR, TX, L, NVEC, NT, 1>), dim3(p.blocks), dim3(NT), 0, s, d, a);
     return hipGetLastError();
 }
 template <typename TH, typename TR, typename TX, int L, int NVEC, int NT>
@@ -282,7 +324,7 @@ hipError_t bwd_t(const kan_join_desc_t& d, const JoinPlan& p, const JoinArgs& a,
         case 32 * 8 + 1: return bwd<TH, TR, TX, 32, 1, 256>(d, p, a, part, s);
         case 64 * 8 + 1: return bwd<TH, TR, TX, 64, 1, 256>(d, p, a, part, s);
         case 64 * 8 + 2: return bwd<TH, TR, TX, 64, 2, 256>(d, p, a, part, s);
-        case 64 * 8 + 4: return bwd<TH, TR, TX, 64, 4, 256>(d, p, a, part, s);
+        case 256 * 8 + 1: return bwd<TH, TR, TX, 256, 1, 256>(d, p, a, part, s);
         case 256 * 8 + 2: return bwd<TH, TR, TX, 256, 2, 256>(d, p, a, part, s);
         case 256 * 8 + 4: return bwd<TH, TR, TX, 256, 4, 256>(d, p, a, part, s);
         default: return bwd<TH, TR, TX, 1024, 2, 1024>(d, p, a, part, s);

@@ -92,22 +92,24 @@ hipError_t launch_delta_step(const kan_delta_desc_t& d, int64_t S, const DeltaAr
     ++launches;
     return hipSuccess;
 }
-static void join(const kan_join_desc_t& d, const JoinPlan& p) {
+static void join(const kan_join_desc_t& d, const JoinPlan& p, bool back) {
     need(d.N > 0 && (int64_t)p.lanes * p.vecs * 4 >= d.D, "a row's threads hold it");
-    need((p.lanes == 32 && p.vecs <= 2) || p.lanes == 64 || p.lanes == 256 || (p.lanes == 1024 && p.vecs == 2),
+    need((p.lanes == 32 && p.vecs == 1) || (p.lanes == 64 && p.vecs <= (back ? 2 : 4)) ||
+             (p.lanes == 256 && p.vecs >= (back ? 1 : 2)) || (p.lanes == 1024 && p.vecs == 2),
          "threads of a row");
     need(p.vecs == 1 || p.vecs == 2 || p.vecs == 4, "vectors of a thread");
     need((int64_t)p.blocks * (p.lanes > 256 ? p.lanes : 256) <= kGrid, "join grid");
 }
 hipError_t launch_join_fwd(const kan_join_desc_t& d, const JoinPlan& p, const JoinArgs& a, hipStream_t) {
-    join(d, p);
+    join(d, p, false);
     need(a.h && a.y && a.stats && a.x, "join forward pointers");
-    need((int64_t)p.blocks * (p.lanes > 256 ? 1 : 256 / p.lanes) >= d.N, "a pass over the rows");
+    need(p.rows == 1 || (p.rows == kJoinRows && p.vecs == 1), "rows of a thread");
+    need((int64_t)p.blocks * p.rows * (p.lanes > 256 ? 1 : 256 / p.lanes) >= d.N, "a pass over the rows");
     ++launches;
     return hipSuccess;
 }
 hipError_t launch_join_bwd(const kan_join_desc_t& d, const JoinPlan& p, const JoinArgs& a, char* ws, hipStream_t) {
-    join(d, p);
+    join(d, p, true);
     need(a.h && a.y_in && a.stats_in && a.dh && ws, "join backward pointers");
     need(p.blocks <= kJoinMaxBlocks && (size_t)p.blocks * 2 * d.D * 4 <= ws_bytes, "blocks' sums fit");
     ++launches;

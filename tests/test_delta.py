@@ -16,6 +16,13 @@ difference of two terms of at most n |d| each, whose errors, of at least e n |d|
 stay when the terms cancel (with one key feature they cancel to 1e-6 of their size).
 Gradients of q and k that are made unit vectors are therefore held against the
 larger of their own rows and n |d|, with d the gradient of u.
+
+A row of one sequence with one key and one value feature is a chain of scalars with
+sums of two terms: v - S'k, S' + ku, dhT + q dy, dS - k du and dS u - S' dw.  A
+rounding of a term stays when they cancel, and there is no other element whose
+size the error could be held against, so it is held against the sizes of the
+terms (with more features the rest of a row keeps its size: a key takes away one
+direction of it).
 """
 
 import numpy as np
@@ -35,6 +42,11 @@ def env():
     assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
     from kolmogorov_arnold_network_amd import functional as F
     return torch, F
+
+
+@pytest.fixture(autouse=True)
+def seeded(env):
+    env[0].manual_seed(0)
 
 
 def _np(t):
@@ -83,7 +95,7 @@ def _error(got, want, terms=None):
     got, want = (np.asarray(t, np.float64).reshape(-1, t.shape[-1]) if t.ndim > 3 else np.asarray(t, np.float64).reshape(-1, 1)
                  for t in (got, want))
     assert got.shape == want.shape and np.isfinite(got).all()
-    size = max(np.sqrt((t ** 2).sum(-1)).max(initial=0) for t in ((want,) if terms is None else (want, terms)))
+    size = max(np.sqrt((np.atleast_1d(t) ** 2).sum(-1)).max(initial=0) for t in ((want,) if terms is None else (want, terms)))
     error = np.sqrt(((got - want) ** 2).sum(-1)).max(initial=0)
     return error / size if size > 0 else error
 
@@ -91,6 +103,15 @@ def _error(got, want, terms=None):
 def _tol(T, dtype=None, back=False):
     t = 5 * np.sqrt(128) * E * np.sqrt(max(1, -(-T // 64))) * (3 if back else 1)
     return t + (2.0 ** -8 + 2.0 ** -16 if dtype == "bf16" else 0)
+
+
+def _scalars(q, k, v, h0, dy, dhT, unit):
+    """Sizes of the terms behind y, hT and the gradients where every array has one element (|k|, beta, exp(g) <= 1)."""
+    q, k, v, h0, dy, dhT = (0.0 if t is None else float(np.abs(t).max(initial=0)) for t in (q, k, v, h0, dy, dhT))
+    nq, nk = (1 / np.sqrt(x * x + O.UNIT_EPS) if unit else 1.0 for x in (q, k))
+    w, d = v + h0, dhT + q * nq * dy
+    return dict(y=q * nq * (h0 + w), hT=h0 + w, dq=nq * dy * (h0 + w), dk=nk * d * (w + h0), dv=d, dg=2 * d * h0, dbeta=d * w,
+                dh0=2 * d)
 
 
 def _lengths(torch, B, T):
@@ -120,7 +141,8 @@ def test_forward(env, B, T, Hk, Hv, Dk, Dv, layout, dtype):
     y = torch.full((B, T, Hv, Dv), float("nan"), dtype=args[0].dtype, device="cuda:0")
     _, hT = F.kan_delta_forward(*args, h0, lengths, scale, unit, out=y)
     wy, wh = O.delta_forward(*map(_np, args), _np(h0), None if lengths is None else lengths.tolist(), scale, unit)
-    assert _error(_np(y), wy) <= _tol(T, dtype) and _error(_np(hT), wh) <= _tol(T)
+    terms = _scalars(*map(_np, (*args[:3], h0, None, None)), unit) if B * T * Dk * Dv == 1 else {}
+    assert _error(_np(y), wy, terms.get("y")) <= _tol(T, dtype) and _error(_np(hT), wh, terms.get("hT")) <= _tol(T)
     if lengths is not None:
         for b, n in enumerate(lengths.tolist()):
             assert not y[b, max(n, 0):].any()
@@ -146,8 +168,8 @@ def test_backward(env, B, T, Hk, Hv, Dk, Dv, layout, dtype):
     assert all(a is b for a, b in zip(got, grads))
     want = O.delta_backward(*map(_np, args), _np(dy), _np(h0), None if lengths is None else lengths.tolist(), _np(dhT),
                             None, unit)
-    terms = {}
-    if unit:                             # n d of q and k
+    terms = _scalars(*map(_np, (*args[:3], h0, dy, dhT)), unit) if B * T * Dk * Dv == 1 else {}
+    if unit and not terms:               # n d of q and k
         u, n = zip(*(O._unit(_np(t), True) for t in args[:2]))
         plain = O.delta_backward(*u, *map(_np, args[2:]), _np(dy), _np(h0),
                                  None if lengths is None else lengths.tolist(), _np(dhT))

@@ -235,6 +235,21 @@ def test_rows_past_32_bits(env):
     assert torch.equal(F.kan_join_forward(far, far, far, w, w)[0], F.kan_join_forward(h[:2], h[:2], h[:2], w, w)[0])
 
 
+@pytest.mark.parametrize("N,D,dtype", [(131072 + 5, 100, "bf16"), (65536 + 1, 256, "f32"), (140001, 31, "f32")])
+def test_many_narrow_rows_equal_few(env, N, D, dtype):
+    """Threads that have several rows at a time: the same bits as a call of few of the rows."""
+    torch, F = env
+    dt = _dt(torch, dtype)
+    h, r, gate = (_rows(torch, N, D, dt, gap) for gap in (0, 3, 8))
+    w, u = torch.rand(D, device="cuda:0"), torch.rand(D, device="cuda:0")
+    whole = F.kan_join_forward(h, r, gate, w, u)
+    for lo, hi in ((0, 700), (N // 2, N // 2 + 333), (N - 41, N)):
+        part = F.kan_join_forward(h[lo:hi], r[lo:hi], gate[lo:hi], w, u)
+        assert torch.equal(whole[0][lo:hi], part[0]) and torch.equal(whole[1][lo:hi], part[1])
+        assert torch.equal(whole[2][:, lo:hi], part[2])
+    assert bool(whole[0].isfinite().all()) and bool(whole[1].isfinite().all())
+
+
 def test_refusals(env):
     torch, F = env
     h, w = torch.randn(4, 16, device="cuda:0"), torch.ones(16, device="cuda:0")
