@@ -537,8 +537,8 @@ int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* 
  * of rows past len are 0.
  *
  * Rows go through in chunks of 64, whose correction is a triangular system.
- * All of it is float32 with values of more than 24 bits for sums of g, in a fixed
- * order.  A NaN or an infinity in a row reaches the rows of its chunk, earlier
+ * All of it is float32, products of floats on matrix instructions with the 24 bits
+ * of each, sums of g in more than that, in a fixed order.  A NaN or an infinity in a row reaches the rows of its chunk, earlier
  * ones included, and all later ones of its sequence and heads.
  *
  * Layouts: q, k [B, T, Hk, Dk], v [B, T, Hv, Dv] and their gradients in `dtype`
@@ -564,7 +564,8 @@ typedef struct {
 
 /* Bytes of workspace a pass (kan_pass_t) needs (SIZE_MAX if `desc` is invalid):
  * the chunks' triangular matrices; for the backward also the states at the
- * chunks' starts and their gradients, and the rows' corrections. */
+ * chunks' starts and their gradients, and the rows' corrections; where few heads
+ * have long sequences, which are cut then, the segments' runs and first states. */
 size_t kan_delta_workspace_size(const kan_delta_desc_t* desc, int pass);
 /* y and hT out (hT may be NULL). */
 int kan_delta_forward(const kan_delta_desc_t* desc, const void* q, const void* k, const void* v, const float* g,
@@ -591,7 +592,8 @@ int kan_delta_step(const kan_delta_desc_t* desc, int64_t S, const void* q, const
  *     x = w_pre y n2 (with KAN_JOIN_PRE),   n2 = 1 / sqrt(mean(y^2) + eps)
  *
  * row by row over D columns.  r, gate, w_post and w_pre may be NULL (0, 1, 1, 1);
- * n2 and x are of y before it is rounded to its storage.  The factors n1 and n2
+ * n2 and x are of y before it is rounded to its storage.  Squares are float32:
+ * rows beyond 1e18 have a norm of infinity and a factor of 0.  The factors n1 and n2
  * (1 where there is no norm) are kept for the backward:
  *
  *     z = y n2,  c = w_pre dx,  d = dy + n2 (c - z mean(c z)),   dr = d
