@@ -130,8 +130,7 @@ DeltaPlan delta_plan(const kan_delta_desc_t& d, int pass) {
     p.heads = d.B * d.Hv;
     p.groups = p.heads * ((d.Dv + 63) / 64) >= 256 ? 4 : 2;
     segments(d, back, p);
-    // three planes of a triangular matrix hold float32, two what y keeps in bfloat16
-    p.mats = (back ? 9 : d.dtype == KAN_F32 ? 6 : 5) * int64_t(6 * 64 * 16);
+    p.mats = (back ? 9 : 6) * int64_t(6 * 64 * 16);    // three planes of each triangular matrix
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t o = off;
