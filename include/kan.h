@@ -530,8 +530,11 @@ int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* 
  * from there to T, hT = S_{len-1} (h0 where len = 0), and nothing of a row past
  * len is used.  With KAN_DELTA_UNIT q and k are divided by sqrt(|.|^2 + 1e-6)
  * first.  Head h of v, g, beta, y and S uses head h / (Hv / Hk) of q and k.
- * g is the logarithm of the decay (a decay of 0, g = -inf, is as good as
- * g = -128); states grow where g > 0 or beta |k|^2 > 2.  Backward, with dy and
+ * g is the logarithm of the decay; below -1024, -inf included, it counts as -1024,
+ * which leaves nothing of a state, also where rows behind it let the state grow.
+ * States grow where g > 0 or beta |k|^2 > 2; a sum of g over rows of a chunk that
+ * follow each other has to stay below 88, whose exponential float32 holds (past
+ * it, infinities and NaN, also where rows write nothing).  Backward, with dy and
  * the gradient dhT of hT (0 if NULL), gives the gradients of q, k, v, g, beta
  * and h0; those of q and k are summed over the heads that share them, and those
  * of rows past len are 0.

@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d,
             if (lane < rows) {
                 g = a.g[(b * d.T + t0 + lane) * d.Hv + h];
                 beta = a.beta[(b * d.T + t0 + lane) * d.Hv + h];
-                g = g < -128.0f ? -128.0f : g;         // exp(-128) is 0; a NaN stays
+                // finite, for differences of sums; 0 also after what growth a float holds; a NaN stays
+                g = g < -1024.0f ? -1024.0f : g;
             }
             double c = (double)g * 1.4426950408889634;
 #pragma unroll
@@ -1869,8 +1870,7 @@ __global__ void __launch_bounds__(NT) delta_step_kernel(kan_delta_desc_t d, int6
         to[lane] = x0 * f;
         to[lane + 64] = x1 * f;
     }
-    float g = a.g[b * d.Hv + h];
-    const float alpha = expf(g < -128.0f ? -128.0f : g), beta = a.beta[b * d.Hv + h];
+    const float alpha = expf(a.g[b * d.Hv + h]), beta = a.beta[b * d.Hv + h];
     const int c = tid & 15, rt = tid >> 4, nn = n0 + 4 * c;
     float* S = state + (slot * d.Hv + h) * Dk * Dv;
     f32x4 s[8];
