@@ -502,6 +502,8 @@ class KANJoin(torch.nn.Module):
         self.w_pre = torch.nn.Parameter(torch.ones(features, device=device)) if pre else None
 
     def forward(self, h, residual=None, gate=None):
+        if h.dim() < 1 or h.shape[-1] != self.features:
+            raise ValueError("h must have rows of %d features, got %s" % (self.features, tuple(h.shape)))
         for name, t in (("residual", residual), ("gate", gate)):
             if t is not None and t.shape != h.shape:
                 raise ValueError("%s must be %s, got %s" % (name, tuple(h.shape), tuple(t.shape)))
