@@ -72,13 +72,18 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
     return v;
 }
 
-// act(g) and act'(g), from the smaller of the two shares.  exp by v_exp_f32 on |g| log2(e), whose
-// rounding is off by |g| 2^-24 of the result as expf's argument is; the reciprocal is within 2^-23.
-// With expf and a division a narrow row's arithmetic takes longer than its bytes (524288 x 128
-// bf16 forward 124 us, 100 so).
+// act(g) and act'(g), from the smaller of the two shares.  exp(-|g|) is v_exp_f32's 2^t (2^-23)
+// of the rounded product t = |g| log2(e), times 1 + ln(2) of what the rounding lost: without that
+// factor its error is |g| 2^-24.  From 128 on the smaller share is 0.  The reciprocal is within 2^-23.
+// With expf and a division a narrow row's arithmetic takes longer than its bytes (524288 x 128 bf16
+// forward 124 us, 102 so).
 __device__ __forceinline__ void activation(int kind, float g, float& a, float& slope) {
-    const float e = __builtin_amdgcn_exp2f(fabsf(g) * -1.44269504f), big = __builtin_amdgcn_rcpf(1.0f + e),
-                small = e * big;
+    const float x = fabsf(g) > 128.0f ? 128.0f : fabsf(g);                     // a NaN stays
+    const float t = x * -0x1.715476p0f;
+    const float lost = __builtin_fmaf(x, -0x1.4ae0cp-26f, __builtin_fmaf(x, -0x1.715476p0f, -t));
+    float e = __builtin_amdgcn_exp2f(t);
+    e = __builtin_fmaf(e * lost, 0.693147182f, e);
+    const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
     const float s = g >= 0.0f ? big : small, o = g >= 0.0f ? small : big;      // a NaN is in both
     a = kind == KAN_GATE_SIGMOID ? s : g * s;
     slope = kind == KAN_GATE_SIGMOID ? s * o : s + g * s * o;
