@@ -38,21 +38,39 @@ bool distinct(int64_t B, int64_t T, int64_t H, int64_t D, const kan_heads_t& s) 
     return true;
 }
 
-struct Slice {                       // of each token's row in an array of gradients
+struct Slice {                       // of an array of gradients
     const void* p;
     kan_heads_t s;
     int64_t H, D;
     Range range(int64_t B, int64_t T, int e) const { return Range{p, (size_t)extent4(B, T, H, D, s) * (size_t)e}; }
-    __int128 width() const { return (__int128)(H - 1) * s.head + D; }
 };
-// Whether two outputs that share a range of memory are slices of the same rows.
+// Whether two outputs that share a range of memory are slices of one array: some dimensions lie inside
+// each slice, whose widths are apart from each other, and the rest, which both have alike, step over both.
 bool slices(const Slice& a, const Slice& b, int64_t B, int64_t T, int e) {
-    if ((B > 1 && a.s.seq != b.s.seq) || (T > 1 && a.s.row != b.s.row)) return false;
     const Slice &lo = reinterpret_cast<uintptr_t>(a.p) < reinterpret_cast<uintptr_t>(b.p) ? a : b, &hi = &lo == &a ? b : a;
     const uintptr_t bytes = reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p);
     if (bytes % (unsigned)e) return false;
-    const __int128 apart = bytes / (unsigned)e, rows = row_distance(B, T, a.s.row, a.s.seq);
-    return apart >= lo.width() && rows - apart >= hi.width();
+    const struct {
+        int64_t n[2], stride[2];
+    } dims[3] = {{{B, B}, {lo.s.seq, hi.s.seq}}, {{T, T}, {lo.s.row, hi.s.row}}, {{lo.H, hi.H}, {lo.s.head, hi.s.head}}};
+    for (int inside = 0; inside < 8; ++inside) {       // a bit for each dimension
+        __int128 width[2] = {lo.D, hi.D};
+        int64_t n[3] = {1, 1, 1}, stride[3] = {};
+        bool alike = true;
+        for (int x = 0; x < 3; ++x) {
+            if (inside >> x & 1) {
+                for (int z = 0; z < 2; ++z) width[z] += (__int128)(dims[x].n[z] - 1) * dims[x].stride[z];
+            } else {
+                n[x] = dims[x].n[0], stride[x] = dims[x].stride[0];
+                alike = alike && dims[x].n[1] == n[x] && (n[x] <= 1 || dims[x].stride[1] == stride[x]);
+            }
+        }
+        const __int128 both = bytes / (unsigned)e + width[1];
+        if (alike && bytes / (unsigned)e >= width[0] && both <= INT64_MAX &&
+            distinct(n[0], n[1], n[2], (int64_t)both, kan_heads_t{stride[0], stride[1], stride[2]}))
+            return true;
+    }
+    return false;
 }
 
 int delta_check(const kan_delta_desc_t* d) {
