@@ -529,7 +529,8 @@ int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* 
  * for t < len = lengths[b] limited to [0, T] (T if `lengths` is NULL); y is 0
  * from there to T, hT = S_{len-1} (h0 where len = 0), and nothing of a row past
  * len is used.  With KAN_DELTA_UNIT q and k are divided by sqrt(|.|^2 + 1e-6)
- * first.  Head h of v, g, beta, y and S uses head h / (Hv / Hk) of q and k.
+ * first (squares are float32: rows beyond 1e18 overflow).  Head h of v, g, beta, y
+ * and S uses head h / (Hv / Hk) of q and k.
  * g is the logarithm of the decay; below -1024, -inf included, it counts as -1024,
  * which leaves nothing of a state, also where rows behind it let the state grow.
  * States grow where g > 0 or beta |k|^2 > 2; a sum of g over rows of a chunk that
@@ -540,14 +541,16 @@ int kan_distill_step(const kan_distill_desc_t* desc, const void* z, const void* 
  * of rows past len are 0.
  *
  * Rows go through in chunks of 64, whose correction is a triangular system.
- * All of it is float32, products of floats on matrix instructions with the 24 bits
- * of each, sums of g in more than that, in a fixed order.  A NaN or an infinity in a row reaches the rows of its chunk, earlier
- * ones included, and all later ones of its sequence and heads.
+ * All of it is float32, whatever the rows' storage: products of floats go through
+ * matrix instructions with the 24 bits of each, sums of g in more than that, in a
+ * fixed order.  A NaN or an infinity in a row reaches the rows of its chunk,
+ * earlier ones included, and all later ones of its sequence and heads.
  *
  * Layouts: q, k [B, T, Hk, Dk], v [B, T, Hv, Dv] and their gradients in `dtype`
  * with a stride (elements) for each of sequence, row and head, so that they may
- * be slices of one projection; y, dy [B, T, Hv, Dv] in `dtype`, g, beta, dg,
- * dbeta [B, T, Hv] and h0, hT, dhT, dh0 [B, Hv, Dk, Dv] float32, contiguous. */
+ * be slices of one projection (of its rows, heads or sequences); y, dy [B, T, Hv,
+ * Dv] in `dtype`, g, beta, dg, dbeta [B, T, Hv] and h0, hT, dhT, dh0 [B, Hv, Dk, Dv]
+ * float32, contiguous. */
 #define KAN_DELTA_UNIT 1
 typedef struct {
     int64_t seq, row, head;         /* strides, >= 0; row at most 2^24 */

@@ -330,8 +330,8 @@ __device__ __forceinline__ int64_t at_row(const kan_heads_t& s, int64_t b, int64
 }
 // Head and column tile of a scan's block: a head's blocks read the same rows, so
 // they go to one XCD (blocks are dealt to the eight of them in turn) and its L2
-// (the backward scan of 4 x 4096 x 16 x 128 bf16 took 970 us without this and
-// 835 with it; the forward of 8 x 4096, 460 either way).
+// (the backward scan of 4 x 4096 x 16 x 128 bf16 takes 393 us without this and 369
+// with it, the forward scan of 8 x 4096 338 and 336).
 __device__ __forceinline__ void head_and_tile(int heads, int tiles, int& head, int& tile) {
     const int group = (int)blockIdx.x / (8 * tiles), at = (int)blockIdx.x % (8 * tiles);
     const int n = heads - 8 * group < 8 ? heads - 8 * group : 8;
@@ -469,7 +469,7 @@ constexpr int prep_bytes() {                           // of K, then of A and P 
 // and the transposes).  The products K K^T and Q K^T are the heads' own; rows of Q
 // are left operands straight from HBM.  SHARED: a key has several heads; the loop over
 // them keeps the products in registers, which one head need not pay for (8 x 4096 x
-// 16 x 128 bf16 forward: 442 us with it, 423 without).
+// 16 x 128 bf16 forward: 139 us with it, 118 without).
 template <typename TS, int DKP, bool BWD, bool SHARED>
 __global__ void __launch_bounds__(PREP_NT) delta_prep_kernel(kan_delta_desc_t d, DeltaPlan p, DeltaArgs a, char* ws) {
     extern __shared__ __align__(16) char lds[];
@@ -594,10 +594,11 @@ enum Pass { kForward, kStates, kRuns, kBack };
 
 constexpr int kan_delta_halves(int dkp, int groups) { return dkp >= 64 && groups == 2 ? 2 : 1; }
 
-// How a scan's block is laid out.  A wave has 16 columns of the state and, where
-// Dk has room for it, half of its rows, so that a pair of waves shares the
-// columns: what each contracts over its rows of the state is added to the
-// other's through LDS.  Two waves to a SIMD hide each other's latency.
+// How a scan's block is laid out.  A wave has 16 columns of the state.  In blocks
+// of two groups with room for it in Dk it has half of the state's rows, and a pair
+// of waves shares the columns: what each contracts over its rows of the state is
+// added to the other's through LDS, and all four SIMDs have a wave.  LDS and
+// registers leave most scans one block a compute unit.
 template <typename TS, int DKP, int GROUPS, int PASS, bool EVEN>
 struct Scan {
     static constexpr int PL = planes_of<TS>::n, NP = 3;          // planes of rows, and of the floats behind y
@@ -623,8 +624,10 @@ struct Scan {
 
 // The products of a scan.  Operands are loaded a group ahead of the instructions
 // that use them, and a group goes plane by plane over its tiles, so that an
-// instruction never waits for the one before it; the compiler, left alone, loads
-// an operand, waits, and chains its planes (7 us a chunk, where this takes 4).
+// instruction never waits for the one before it.  The fences hold the compiler to
+// that order.  They are worth 3 to 7 hundredths of a float32 backward pass with keys
+// of 128 (8 x 4096 x 16 heads: 2897 us with them, 3089 without) and cost a few
+// hundredths in most others (bf16: forward 497 and 489, backward 1582 and 1541).
 #define KAN_FENCE() __builtin_amdgcn_sched_barrier(0)
 
 // acc[t] += a[t] b for T tiles
@@ -822,10 +825,10 @@ __global__ void __launch_bounds__((Scan<TS, DKP, GROUPS, PASS, EVEN>::NT))
     const uint32_t s_off = 8 * gq * (uint32_t)p.dvp + n0 + m;
     TS vn[4][4];
     // Chunk n on its way to LDS, or to registers.  Through registers it goes a few
-    // loads at a time between the products (1 x 32768 x 8 x 128 float32: scan 3215 us
-    // at once, 2927 in eight parts); directly to LDS all of it at once, since loads
-    // between the products hold those up as well (8 x 4096 x 16 x 128 bf16: 332 us at
-    // once, 351 in parts).
+    // loads at a time between the products (1 x 32768 x 8 x 128 float32: scan 428 us
+    // at once, 386 in eight parts); directly to LDS all of it at once, since loads
+    // between the products hold those up as well (8 x 4096 x 16 x 128 bf16: 336 us at
+    // once, 345 in parts; the states of 4 x 4096 257 and 323).
     constexpr int PARTS = DIRECT ? 1 : 8;
     auto fetch = [&](int part, int n) {
         const int64_t t0 = (int64_t)n * C;
@@ -1441,9 +1444,8 @@ __global__ void __launch_bounds__(4 * DKP) delta_link_kernel(kan_delta_desc_t d,
 // four columns 16 x + 4 gq .. of every tile x.  The products with the states come
 // first, 32 of their columns at a time through LDS, then those of the rows among
 // themselves, in the same place: with bfloat16 rows two blocks fit a compute unit
-// and hide each other's loads (4 x 4096 x 16 x 128 bf16: 552 us with one, 323 with two).
+// and hide each other's loads (4 x 4096 x 16 x 128 bf16: 479 us with one, 319 with two).
 constexpr int GRAD_NT = 256, GS = 32;                // GS: state columns at a time
-template <int DKP>
 __device__ __forceinline__ int slice_at(int row, int c) { return row * GS + ((c ^ (row >> 2)) & 3) * 8; }
 __device__ __forceinline__ float quad_sum(float v) {  // over the four lanes of a row
     v += __shfl_xor(v, 16, 64);
@@ -1576,21 +1578,21 @@ __global__ void __launch_bounds__(GRAD_NT, sizeof(TS) == 2 ? 2 : 1) delta_grad_k
             bf16x8 v[3];
             piece_planes(s0[x], v);
 #pragma unroll
-            for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(S0 + z * DKP * GS + slice_at<DKP>(dd, c)) = v[z];
+            for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(S0 + z * DKP * GS + slice_at(dd, c)) = v[z];
             piece_planes(s1[x], v);
 #pragma unroll
-            for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(S1 + z * DKP * GS + slice_at<DKP>(dd, c)) = v[z];
+            for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(S1 + z * DKP * GS + slice_at(dd, c)) = v[z];
         }
 #pragma unroll
-        for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(U + z * C * GS + slice_at<C>(im, gq)) = ua[z];
+        for (int z = 0; z < 3; ++z) *reinterpret_cast<bf16x8*>(U + z * C * GS + slice_at(im, gq)) = ua[z];
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < DT; ++x) {
             bf16x8 sb[3], db[3];
 #pragma unroll
             for (int z = 0; z < 3; ++z) {
-                sb[z] = *reinterpret_cast<const bf16x8*>(S0 + z * DKP * GS + slice_at<DKP>(16 * x + m, gq));
-                db[z] = *reinterpret_cast<const bf16x8*>(S1 + z * DKP * GS + slice_at<DKP>(16 * x + m, gq));
+                sb[z] = *reinterpret_cast<const bf16x8*>(S0 + z * DKP * GS + slice_at(16 * x + m, gq));
+                db[z] = *reinterpret_cast<const bf16x8*>(S1 + z * DKP * GS + slice_at(16 * x + m, gq));
             }
             mma<3, PL>(ys[x], sb, ya);
             mma<3, 3>(vs[x], sb, va);
@@ -1601,7 +1603,7 @@ __global__ void __launch_bounds__(GRAD_NT, sizeof(TS) == 2 ? 2 : 1) delta_grad_k
             if (x > wave) break;
             bf16x8 ub[3];
 #pragma unroll
-            for (int z = 0; z < 3; ++z) ub[z] = *reinterpret_cast<const bf16x8*>(U + z * C * GS + slice_at<C>(16 * x + m, gq));
+            for (int z = 0; z < 3; ++z) ub[z] = *reinterpret_cast<const bf16x8*>(U + z * C * GS + slice_at(16 * x + m, gq));
             mma<3, PL>(dP[x], ub, ya);
             mma<3, 3>(X[x], ub, va);
         }
@@ -1844,7 +1846,7 @@ __global__ void __launch_bounds__(NT) delta_heads_kernel(kan_delta_desc_t d, Del
 template <typename TS>
 __global__ void __launch_bounds__(NT) delta_step_kernel(kan_delta_desc_t d, int64_t pool, DeltaArgs a, float* state,
                                                         const int32_t* slots, int tiles) {
-    __shared__ float ks[kDeltaMaxDk], qs[kDeltaMaxDk], red[2][16][68], factor[2];
+    __shared__ float ks[kDeltaMaxDk], qs[kDeltaMaxDk], red[2][16][68];
     const int64_t bh = blockIdx.x / (unsigned)tiles, b = bh / d.Hv, h = bh % d.Hv, hk = h / (d.Hv / d.Hk);
     const int n0 = (int)(blockIdx.x % (unsigned)tiles) * 64, tid = threadIdx.x;
     const int Dk = (int)d.Dk, Dv = (int)d.Dv;

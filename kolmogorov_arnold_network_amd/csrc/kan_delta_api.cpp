@@ -185,7 +185,7 @@ JoinPlan join_plan(const kan_join_desc_t& d, int pass) {
     JoinPlan p = {};
     const int64_t vectors = (d.D + 3) / 4;
     // A backward pass has nine vectors for each of a row's: at four a thread two waves fill a SIMD's
-    // registers, so wide rows go to four waves (4999 x 770 bf16: 48.6 -> 31.0 us).
+    // registers, so wide rows go to four waves (4999 x 770 bf16: 48.6 us with one, 31.5 with four).
     const int64_t wave = pass == KAN_PASS_FORWARD ? 256 : 128;
     p.lanes = vectors <= 32 ? 32 : vectors <= wave ? 64 : vectors <= 1024 ? 256 : 1024;
     const int64_t each = (vectors + p.lanes - 1) / p.lanes;

@@ -76,7 +76,7 @@ __device__ __forceinline__ float row_sum(float v, float* slots) {
 // of the rounded product t = |g| log2(e), times 1 + ln(2) of what the rounding lost: without that
 // factor its error is |g| 2^-24.  From 128 on the smaller share is 0.  The reciprocal is within 2^-23.
 // With expf and a division a narrow row's arithmetic takes longer than its bytes (524288 x 128 bf16
-// forward 124 us, 102 so).
+// forward 121 us, 102 so).
 __device__ __forceinline__ void activation(int kind, float g, float& a, float& slope) {
     const float x = fabsf(g) > 128.0f ? 128.0f : fabsf(g);                     // a NaN stays
     const float t = x * -0x1.715476p0f;
@@ -95,8 +95,8 @@ __device__ __forceinline__ float factor(float sum, float per, float eps) {
 }
 
 // U rows at a time of each thread's: narrow rows give a wave little to wait for, and a
-// block as much work to start as to do (524288 x 128 bf16 with gate and residual:
-// 117 us with one row, 100 with four).
+// block as much work to start as to do (524288 x 128 bf16 with a gate: 119 us with
+// one row, 102 with four).
 template <typename TH, typename TR, typename TX, int L, int NVEC, int NT, int U>
 __global__ void __launch_bounds__(NT) join_fwd_kernel(kan_join_desc_t d, JoinArgs a) {
     __shared__ float slots[2][NT / 64];
